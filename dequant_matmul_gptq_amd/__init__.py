@@ -1,5 +1,7 @@
 """MI355X (gfx950) quantized linear layer: GPTQ 4-bit and EXL2 mixed-bit codes
-unpacked, scaled and fused into the matmul against float16 activations.
+unpacked, scaled and fused into the matmul against float16 activations; and the
+operators between a decoder's linear layers: rotary positions, a paged
+key/value cache, attention over it, and the root-mean-square norm.
 
 The compute lives in libqlinear.so (hand-written HIP, C ABI in
 include/qlinear.h); this package is its thin Python binding. PyTorch provides
@@ -40,3 +42,17 @@ from ._lib import (  # noqa: F401
     kv_quant,
     kv_dequant,
 )
+from .decoder import (  # noqa: F401
+    ROPE_HALF,
+    ROPE_INTERLEAVED,
+    KVCache,
+    copy_pages,
+    paged_attention,
+    paged_attention_workspace,
+    paged_attention_workspace_bytes,
+    rms_norm,
+    rope,
+    rope_append,
+    rope_table,
+)
+from .page_pool import PagePool  # noqa: F401

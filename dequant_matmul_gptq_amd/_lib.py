@@ -53,6 +53,12 @@ EXPORTS = (
     "qlinear_qgemm_qscale",
     "qlinear_kv_quant",
     "qlinear_kv_dequant",
+    "qlinear_rope",
+    "qlinear_rope_append",
+    "qlinear_paged_attention_workspace_bytes",
+    "qlinear_paged_attention",
+    "qlinear_copy_pages",
+    "qlinear_rms_norm",
 )
 
 ACT_NONE = 0
@@ -86,6 +92,21 @@ class qlinear_epilogue(ctypes.Structure):
         ("residual", ctypes.c_void_p),
         ("activation", ctypes.c_int32),
         ("addend", ctypes.c_void_p),
+    ]
+
+
+class qlinear_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
+        ("group", ctypes.c_int32),
     ]
 
 
@@ -129,6 +150,15 @@ def lib() -> ctypes.CDLL:
         i64 = ctypes.c_int64
         L.qlinear_kv_quant.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp]
         L.qlinear_kv_dequant.argtypes = [vp, vp, i64, i32, i32, i32, vp, vp]
+        cp, f32 = ctypes.POINTER(qlinear_kv_cache), ctypes.c_float
+        L.qlinear_rope.argtypes = [vp, i64, i32, i32, i32, vp, vp, i32, i32, i32, vp, i64, vp]
+        L.qlinear_rope_append.argtypes = [cp, vp, i64, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32,
+                                          vp]
+        L.qlinear_paged_attention_workspace_bytes.argtypes = [cp, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.qlinear_paged_attention.argtypes = [cp, vp, i64, i32, i32, i32, vp, vp, vp, i32, i32, i32, f32, i32, vp, vp,
+                                              sz, vp]
+        L.qlinear_copy_pages.argtypes = [cp, i32, vp, i32, vp]
+        L.qlinear_rms_norm.argtypes = [vp, vp, vp, i32, i32, f32, vp, vp, vp]
         for name in EXPORTS[1:]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L

@@ -105,6 +105,42 @@ size_t lora_workspace_bytes(int M, int K, int rank);
 hipError_t launch_lora_delta(const uint16_t* x, int M, int K, const uint16_t* A, int rank, const uint16_t* B, int N,
                              float scale, bool accumulate, float* delta, void* ws, hipStream_t stream);
 
+// Rotary positions and the append to a paged cache (rope.hip). Rows of one
+// kind (q, k or v heads) that a launch handles; heads may be 0.
+struct RopeArgs {
+  const uint16_t *q, *k, *v;      // k, v NULL: rotation only
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  uint16_t* q_out;
+  int q_heads, head_dim, tokens;
+  const int32_t *positions, *slots;
+  const float* table;
+  int table_rows, rot_dim, layout;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+hipError_t launch_rope_append(const RopeArgs& a, const qlinear_kv_cache& cache, hipStream_t stream);
+
+// Attention over a paged cache (paged_attention.hip).
+struct AttentionArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  int tokens, q_heads, batch;
+  const int32_t *q_start, *kv_len, *block_table;   // q_start NULL: tokens / batch rows each
+  int table_width, max_q_len, max_kv_len, window;
+  float scale;
+  uint16_t* out;
+};
+size_t paged_attention_workspace_bytes(const qlinear_kv_cache& cache, const AttentionArgs& a);
+hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const AttentionArgs& a, void* ws,
+                                  hipStream_t stream);
+
+// Page copies inside `count` caches of one shape (pages.hip).
+hipError_t launch_copy_pages(const qlinear_kv_cache* caches, int count, const int32_t* pairs, int moves,
+                             hipStream_t stream);
+
+// Root-mean-square norm with the residual's addition (rms_norm.hip).
+hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int M, int K,
+                           float eps, uint16_t* y, uint16_t* residual_out, hipStream_t stream);
+
 // Streaming-read floor (measurement helper): grid workgroups of 256 threads
 // read `bytes` (a multiple of 16) with `loads` (4, 8 or 16) 16-byte loads in
 // flight per thread.

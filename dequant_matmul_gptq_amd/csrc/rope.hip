@@ -1,0 +1,170 @@
+// Rotary positions, alone or with the append to a paged cache. Pair (a, b) of
+// a head turns by the token's angle: (a c - b s, b c + a s), (c, s) from a
+// float32 table. Each product and the sum is rounded once (no fused
+// multiply-add), so that the result, and with it the codes of a quantized
+// cache, is the same wherever the formula is computed in float32.
+//
+// HBM-bound at many tokens, launch latency at few. A lane holds 8 elements of
+// a head (16-byte accesses), a row's D / 8 lanes are neighbours in one wave,
+// and in the half layout each also loads its partner's 8 elements (the same
+// cache lines). A thread goes over several heads of one token, so that the
+// table's row is read once for them. A wave reads all of its rows' elements
+// before it writes any, so a row may be rotated in place. Quantized blocks
+// are groups of neighbouring lanes, whose maximum takes lane swaps.
+#include "qlinear_kernels.hpp"
+
+namespace qlinear {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+union Half8 {
+  uint4 v;
+  uint16_t b[8];
+};
+
+__device__ __forceinline__ float half_value(uint16_t b) { return (float)__builtin_bit_cast(_Float16, b); }
+
+// The codec's codes and scale of one lane's 8 elements of a block of G (see
+// kv_codec.hip), written to words + the lane's place u.
+template <int B, int G>
+__device__ __forceinline__ void encode8(const Half8& x, int u, uint32_t* words, uint16_t* scales) {
+  // Magnitudes as integers: their order is the float16 order, with NaN on top.
+  int m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, (int)(x.b[i] & 0x7FFFu));
+#pragma unroll
+  for (int k = 1; k < G / 8; k <<= 1) m = max(m, __shfl_xor(m, k));
+  constexpr int kHalf = 1 << (B - 1);
+  const _Float16 s16 = (_Float16)(half_value((uint16_t)m) / (float)(kHalf - 1));
+  const float s = (float)s16;
+  uint64_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float r = s > 0.0f ? __builtin_rintf(half_value(x.b[i]) / s) : 0.0f;
+    r = fminf(fmaxf(r, (float)-kHalf), (float)(kHalf - 1));
+    w |= (uint64_t)(uint32_t)((int)r + kHalf) << (i * B);
+  }
+  if constexpr (B == 4) {
+    words[u] = (uint32_t)w;
+  } else if constexpr (B == 8) {
+    reinterpret_cast<uint2*>(words)[u] = make_uint2((uint32_t)w, (uint32_t)(w >> 32));
+  } else {   // 8 six-bit codes are 6 bytes: 2-byte aligned
+    uint16_t* p = reinterpret_cast<uint16_t*>(words) + 3 * u;
+    p[0] = (uint16_t)w;
+    p[1] = (uint16_t)(w >> 16);
+    p[2] = (uint16_t)(w >> 32);
+  }
+  if (u % (G / 8) == 0) scales[u / (G / 8)] = __builtin_bit_cast(uint16_t, s16);
+}
+
+// B: 0 rotates q rows only, 16 appends to a float16 cache, 8 / 6 / 4 to a
+// quantized one with blocks of G. Rows of a token: q heads, k heads, v heads.
+template <int B, int G>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, qlinear_kv_cache c, int heads_per_thread) {
+  const int D = a.head_dim, U = D / 8;
+  const int lane = threadIdx.x & 63;
+  const int rows_per_wave = 64 / U;
+  const int in_wave = lane / U, u = lane - in_wave * U;
+  if (in_wave >= rows_per_wave) return;
+  const int t = blockIdx.x;
+  const int total = B == 0 ? a.q_heads : a.q_heads + 2 * c.kv_heads;
+  const int wave = blockIdx.y * (kThreads / 64) + (threadIdx.x >> 6);
+  int row = wave * rows_per_wave * heads_per_thread + in_wave;
+
+  const bool rotated = u * 8 < a.rot_dim;
+  const bool interleaved = a.layout == QLINEAR_ROPE_INTERLEAVED;
+  const int half_units = a.rot_dim / 16;
+  const bool low = u < half_units;
+  float2 cs[8];
+  if (rotated) {
+    const int p = a.positions[t];
+    const bool known = (unsigned)p < (unsigned)a.table_rows;
+    const float2* src = reinterpret_cast<const float2*>(a.table) + (int64_t)(known ? p : 0) * (a.rot_dim / 2) +
+                        (interleaved ? u * 4 : (low ? u : u - half_units) * 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (interleaved && i >= 4) break;
+      cs[i] = known ? src[i] : make_float2(__builtin_nanf(""), __builtin_nanf(""));
+    }
+  }
+  int64_t slot = -1;
+  if constexpr (B != 0) slot = a.slots[t];
+
+  for (int n = 0; n < heads_per_thread; ++n, row += rows_per_wave) {
+    if (row >= total) break;
+    const bool is_q = B == 0 || row < a.q_heads;
+    const bool is_v = B != 0 && row >= a.q_heads + c.kv_heads;
+    const int head = is_q ? row : row - a.q_heads - (is_v ? c.kv_heads : 0);
+    const uint16_t* src = is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride;
+    src += (int64_t)head * D;
+    Half8 x;
+    x.v = *reinterpret_cast<const uint4*>(src + u * 8);
+    if (rotated && !is_v) {
+#pragma clang fp contract(off)
+      Half8 r;
+      if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = half_value(x.b[2 * i]), q = half_value(x.b[2 * i + 1]);
+          r.b[2 * i] = __builtin_bit_cast(uint16_t, (_Float16)(p * cs[i].x - q * cs[i].y));
+          r.b[2 * i + 1] = __builtin_bit_cast(uint16_t, (_Float16)(q * cs[i].x + p * cs[i].y));
+        }
+      } else {
+        Half8 o;
+        o.v = *reinterpret_cast<const uint4*>(src + (low ? u + half_units : u - half_units) * 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = half_value(x.b[i]) * cs[i].x, q = half_value(o.b[i]) * cs[i].y;
+          r.b[i] = __builtin_bit_cast(uint16_t, (_Float16)(low ? p - q : p + q));
+        }
+      }
+      x = r;
+    }
+    if (is_q) {
+      *reinterpret_cast<uint4*>(a.q_out + t * a.out_stride + (int64_t)head * D + u * 8) = x.v;
+    } else if constexpr (B != 0) {
+      if (slot < 0 || slot >= (int64_t)c.num_pages * c.page_size) continue;
+      // Row of (page, head, slot in page) in the pools.
+      const int64_t r = ((slot / c.page_size) * c.kv_heads + head) * c.page_size + slot % c.page_size;
+      void* pool = is_v ? c.v : c.k;
+      if constexpr (B == 16)
+        reinterpret_cast<uint4*>(pool)[r * U + u] = x.v;
+      else
+        encode8<B, G>(x, u, reinterpret_cast<uint32_t*>(pool) + r * (D * B / 32),
+                      (is_v ? c.v_scales : c.k_scales) + r * (D / G));
+    }
+  }
+}
+
+template <int B, int G>
+hipError_t launch(const RopeArgs& a, const qlinear_kv_cache& c, hipStream_t stream) {
+  const int rows_per_group = 64 / (a.head_dim / 8) * (kThreads / 64);
+  const int total = B == 0 ? a.q_heads : a.q_heads + 2 * c.kv_heads;
+  const int heads_per_thread = a.tokens >= 256 ? 4 : 1;
+  const int per = rows_per_group * heads_per_thread;
+  hipLaunchKernelGGL((rope_kernel<B, G>), dim3((unsigned)a.tokens, (unsigned)((total + per - 1) / per)),
+                     dim3(kThreads), 0, stream, a, c, heads_per_thread);
+  return hipGetLastError();
+}
+
+template <int B>
+hipError_t launch_group(const RopeArgs& a, const qlinear_kv_cache& c, hipStream_t stream) {
+  if (c.group == 32) return launch<B, 32>(a, c, stream);
+  if (c.group == 64) return launch<B, 64>(a, c, stream);
+  return launch<B, 128>(a, c, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) { return launch<0, 32>(a, qlinear_kv_cache{}, stream); }
+
+hipError_t launch_rope_append(const RopeArgs& a, const qlinear_kv_cache& cache, hipStream_t stream) {
+  if (cache.bits == 16) return launch<16, 32>(a, cache, stream);
+  if (cache.bits == 8) return launch_group<8>(a, cache, stream);
+  if (cache.bits == 6) return launch_group<6>(a, cache, stream);
+  return launch_group<4>(a, cache, stream);
+}
+
+}  // namespace qlinear

@@ -1,0 +1,338 @@
+"""Binding of the operators between a decoder's linear layers: the paged
+key/value cache, rotary positions, attention, page copies and the norm
+(argument marshalling; the one computation here is the host-made table of
+rotary angles). Checks, streams and errors are those of the other calls:
+wrong tensors raise ValueError, a non-zero status QlinearError.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+
+import numpy as np
+import torch
+
+from ._lib import _check, _dev, _ptr, _stream, lib, qlinear_kv_cache
+
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+
+
+class KVCache:
+    """Key/value pools of one layer (wraps qlinear_kv_cache).
+
+    k, v: float16 [num_pages][kv_heads][page_size][head_dim], or code words
+    int32 [num_pages][kv_heads][page_size][head_dim * bits / 32] with scales
+    float16 [num_pages][kv_heads][page_size][head_dim / group] (the rows of
+    kv_quant; head_dim says how wide they are, and the width follows).
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor | None = None,
+                 v_scales: torch.Tensor | None = None, head_dim: int | None = None):
+        if k.dim() != 4:
+            raise ValueError("k must be [num_pages][kv_heads][page_size][...]")
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("k_scales and v_scales go together")
+        pages, heads, page, width = (int(n) for n in k.shape)
+        if k_scales is None:
+            if head_dim is not None and int(head_dim) != width:
+                raise ValueError(f"k must be [num_pages][kv_heads][page_size][{head_dim}]")
+            self.head_dim, self.bits, self.group = width, 16, 0
+            dtype = torch.float16
+        else:
+            if head_dim is None or head_dim < 1 or 32 * width % head_dim != 0:
+                raise ValueError("a quantized cache needs head_dim, and its rows head_dim * bits / 32 words")
+            if k_scales.dim() != 4 or k_scales.shape[3] < 1 or head_dim % k_scales.shape[3] != 0:
+                raise ValueError("k_scales must be [num_pages][kv_heads][page_size][head_dim / group]")
+            self.head_dim, self.bits = int(head_dim), 32 * width // int(head_dim)
+            self.group = self.head_dim // int(k_scales.shape[3])
+            dtype = torch.int32
+            for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+                _dev(t, name, torch.float16, (pages, heads, page, self.head_dim // self.group))
+        _dev(k, "k", dtype)
+        _dev(v, "v", dtype, tuple(k.shape))
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.num_pages, self.kv_heads, self.page_size = pages, heads, page
+        self.c = qlinear_kv_cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), pages, page, heads, self.head_dim,
+                                  self.bits, self.group)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, head_dim: int, page_size: int = 256, bits: int = 16,
+              group: int = 32, device="cuda") -> "KVCache":
+        """Pools of the given shape, not initialized (slots that no token has
+        been appended to are never used). `group` is for bits 8, 6 and 4."""
+        lead = (num_pages, kv_heads, page_size)
+        if bits == 16:
+            return cls(*(torch.empty(lead + (head_dim,), dtype=torch.float16, device=device) for _ in range(2)))
+        if bits not in (4, 6, 8) or group not in (32, 64, 128) or head_dim % group != 0:
+            raise ValueError("bits must be 16, 8, 6 or 4, group 32, 64 or 128 and a divisor of head_dim")
+        kv = [torch.empty(lead + (head_dim * bits // 32,), dtype=torch.int32, device=device) for _ in range(2)]
+        s = [torch.empty(lead + (head_dim // group,), dtype=torch.float16, device=device) for _ in range(2)]
+        return cls(*kv, *s, head_dim=head_dim)
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def _rows(t: torch.Tensor, name: str, heads: int | None, dim: int | None) -> int:
+    """Check a float16 [tokens][heads][dim] operand whose tokens may be strided
+    (a slice of a fused projection) and return the token stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != torch.float16:
+        raise ValueError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} must be [tokens][{heads or 'heads'}][{dim or 'head_dim'}], got {tuple(t.shape)}")
+    h, d = int(t.shape[1]), int(t.shape[2])
+    if t.numel() == 0:
+        return h * d
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return int(t.stride(0)) if t.shape[0] > 1 else h * d
+
+
+def _same_device(ref: torch.Tensor, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: dict | None = None,
+               device="cpu") -> torch.Tensor:
+    """(cos, sin) of every position and pair, float32 [max_pos][rot_dim / 2][2],
+    computed in 64 bits: angle p * f_i with f_i = base^(-2 i / rot_dim), changed
+    for long contexts by `scaling` (type and its numbers):
+
+    - linear, factor: f_i / factor (positions compressed).
+    - ntk, factor: base * factor^(rot_dim / (rot_dim - 2)) (the lowest
+      frequency is divided by factor, the highest kept).
+    - bands, factor, original (trained length), low, high: with w_i = original *
+      f_i / (2 pi) turns over the trained length, f_i / factor for w_i < low,
+      f_i for w_i > high, and linear in w_i between the two.
+    - yarn, factor, original, beta_fast (32), beta_slow (1), attention (None):
+      between f_i / factor and f_i by a ramp over i, from the pair that makes
+      beta_fast turns over the trained length (rounded down) to that of
+      beta_slow (rounded up); cos and sin are multiplied by `attention`,
+      0.1 ln(factor) + 1 if it is None.
+    """
+    if max_pos < 1 or rot_dim < 2 or rot_dim % 2 != 0 or not base > 0:
+        raise ValueError("rope_table needs max_pos >= 1, an even rot_dim >= 2 and a positive base")
+    i = np.arange(rot_dim // 2, dtype=np.float64)
+    sc = dict(scaling or {"type": "none"})
+    kind = sc.pop("type", None)
+    need = {"none": set(), "linear": {"factor"}, "ntk": {"factor"}, "bands": {"factor", "original", "low", "high"},
+            "yarn": {"factor", "original"}}
+    optional = {"yarn": {"beta_fast", "beta_slow", "attention"}}
+    if kind not in need or not need[kind] <= set(sc) <= need[kind] | optional.get(kind, set()):
+        raise ValueError(f"unknown rotary scaling {scaling!r}")
+    factor = float(sc.get("factor", 1.0))
+    if not factor >= 1.0:
+        raise ValueError("the scaling factor must be at least 1")
+    if kind == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-2.0 * i / rot_dim)
+    amp = 1.0
+    if kind == "linear":
+        f = f / factor
+    elif kind == "bands":
+        low, high = float(sc["low"]), float(sc["high"])
+        if not 0 < low < high:
+            raise ValueError("bands scaling needs 0 < low < high")
+        keep = np.clip((float(sc["original"]) * f / (2 * math.pi) - low) / (high - low), 0.0, 1.0)
+        f = f * keep + f / factor * (1 - keep)
+    elif kind == "yarn":
+        def pair_of(turns):
+            return rot_dim * math.log(float(sc["original"]) / (turns * 2 * math.pi)) / (2 * math.log(base))
+        first = max(math.floor(pair_of(float(sc.get("beta_fast", 32.0)))), 0)
+        last = min(math.ceil(pair_of(float(sc.get("beta_slow", 1.0)))), rot_dim - 1)
+        ramp = np.clip((i - first) / max(last - first, 1e-3), 0.0, 1.0)
+        f = f / factor * ramp + f * (1 - ramp)
+        amp = sc.get("attention")
+        amp = 0.1 * math.log(factor) + 1.0 if amp is None else float(amp)
+    out = np.empty((max_pos, rot_dim // 2, 2), dtype=np.float32)
+    step = max(1, (1 << 22) // (rot_dim // 2))
+    for p in range(0, max_pos, step):
+        ang = np.arange(p, min(p + step, max_pos), dtype=np.float64)[:, None] * f
+        out[p:p + step, :, 0] = np.cos(ang) * amp
+        out[p:p + step, :, 1] = np.sin(ang) * amp
+    return torch.from_numpy(out).to(device)
+
+
+def _rope_operands(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, tokens: int):
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("table must be [positions][rot_dim / 2][2]")
+    _dev(table, "table", torch.float32)
+    _dev(positions, "positions", torch.int32, (tokens,))
+    _same_device(x, table=table, positions=positions)
+    return int(table.shape[0]), 2 * int(table.shape[1])
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: int = ROPE_HALF,
+         out: torch.Tensor | None = None) -> torch.Tensor:
+    """x float16 [tokens][heads][head_dim] (token stride free) rotated to the
+    positions (int32 [tokens]) by the table of rope_table. out may be x."""
+    xs = _rows(x, "x", None, None)
+    T, H, D = (int(n) for n in x.shape)
+    rows, rot = _rope_operands(x, table, positions, T)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.float16, device=x.device)
+    os_ = _rows(out, "out", H, D)
+    if out.shape[0] != T:
+        raise ValueError(f"out must have {T} tokens")
+    _same_device(x, out=out)
+    _check(lib().qlinear_rope(_ptr(x), xs, T, H, D, _ptr(positions), _ptr(table), rows, rot, int(layout), _ptr(out),
+                              os_, _stream(x.device)), "qlinear_rope")
+    return out
+
+
+def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                positions: torch.Tensor | None, slots: torch.Tensor, table: torch.Tensor | None,
+                layout: int = ROPE_HALF, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Rotate q [tokens][q_heads][head_dim] (returned; q_out may be q) and k
+    [tokens][kv_heads][head_dim] to the positions, and write k and v to the
+    cache's slots (int32 [tokens]: page * page_size + place in the page,
+    negative = not appended). table None: no rotation. q None: only the append.
+    """
+    D, T = cache.head_dim, int(k.shape[0])
+    ks, vs = _rows(k, "k", cache.kv_heads, D), _rows(v, "v", cache.kv_heads, D)
+    if v.shape[0] != T:
+        raise ValueError(f"v must have {T} tokens")
+    _dev(slots, "slots", torch.int32, (T,))
+    rows, rot = 0, 0
+    if table is not None:
+        if positions is None:
+            raise ValueError("a table needs positions")
+        rows, rot = _rope_operands(k, table, positions, T)
+    heads = qs = os_ = 0
+    if q is not None:
+        heads = int(q.shape[1]) if q.dim() == 3 else 0
+        qs = _rows(q, "q", None, D)
+        if q.shape[0] != T:
+            raise ValueError(f"q must have {T} tokens")
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=torch.float16, device=q.device)
+        os_ = _rows(q_out, "q_out", heads, D)
+        if q_out.shape[0] != T:
+            raise ValueError(f"q_out must have {T} tokens")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(cache.k, q=q, q_out=q_out, k=k, v=v, slots=slots)
+    _check(lib().qlinear_rope_append(cache.ref, _ptr(q), qs, heads, _ptr(k), ks, _ptr(v), vs, _ptr(q_out), os_, T,
+                                     _ptr(positions) if rot else None, _ptr(slots), _ptr(table), rows, rot,
+                                     int(layout), _stream(k.device)), "qlinear_rope_append")
+    return q_out
+
+
+# ---------------------------------------------------------------- attention
+
+def paged_attention_workspace_bytes(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int,
+                                    max_kv_len: int, window: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().qlinear_paged_attention_workspace_bytes(cache.ref, int(tokens), int(q_heads), int(batch),
+                                                         int(max_q_len), int(max_kv_len), int(window),
+                                                         ctypes.byref(n)),
+           "qlinear_paged_attention_workspace_bytes")
+    return int(n.value)
+
+
+def paged_attention_workspace(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int, max_kv_len: int,
+                              device, window: int = 0) -> torch.Tensor:
+    """A paged_attention workspace for calls of these sizes (scratch: needs no
+    initialization; calls that may overlap in time must not share one)."""
+    n = paged_attention_workspace_bytes(cache, tokens, q_heads, batch, max_q_len, max_kv_len, window)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                    q_start: torch.Tensor | None = None, max_q_len: int | None = None,
+                    max_kv_len: int | None = None, scale: float | None = None, window: int = 0,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of each sequence's new tokens over its cached ones (the
+    new ones among them, appended before the call).
+
+    q float16 [tokens][q_heads][head_dim] (token stride free); block_table
+    int32 [batch][width], a sequence's pages in order; kv_len int32 [batch],
+    tokens in the cache; q_start int32 [batch + 1], sequence b's rows of q are
+    q_start[b] .. q_start[b + 1] - 1 (None: tokens / batch rows each). window
+    w > 0: a token sees the w last positions up to its own. scale: None =
+    head_dim^-0.5. max_q_len and max_kv_len bound the lengths for the launch
+    plan (None: tokens, width * page_size); lengths stay on the device. Returns
+    out float16 [tokens][q_heads][head_dim]; a token that sees nothing gets
+    zeros.
+    """
+    qs = _rows(q, "q", None, cache.head_dim)
+    T, H = int(q.shape[0]), int(q.shape[1])
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][width]")
+    B, W = int(block_table.shape[0]), int(block_table.shape[1])
+    _dev(block_table, "block_table", torch.int32)
+    _dev(kv_len, "kv_len", torch.int32, (B,))
+    if q_start is not None:
+        _dev(q_start, "q_start", torch.int32, (B + 1,))
+    if max_q_len is None:
+        max_q_len = T if q_start is not None or B == 0 else T // B
+    if max_kv_len is None:
+        max_kv_len = min(W * cache.page_size, 2 ** 31 - 1)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    if out is None:
+        out = torch.empty((T, H, cache.head_dim), dtype=torch.float16, device=q.device)
+    _dev(out, "out", torch.float16, (T, H, cache.head_dim))
+    if workspace is None:
+        workspace = paged_attention_workspace(cache, T, H, B, max_q_len, max_kv_len, q.device, window)
+    _dev(workspace, "workspace", torch.uint8)
+    _same_device(cache.k, q=q, block_table=block_table, kv_len=kv_len, q_start=q_start, out=out, workspace=workspace)
+    _check(lib().qlinear_paged_attention(cache.ref, _ptr(q), qs, T, H, B, _ptr(q_start), _ptr(kv_len),
+                                         _ptr(block_table), W, int(max_q_len), int(max_kv_len), float(scale),
+                                         int(window), _ptr(out), _ptr(workspace), workspace.numel(),
+                                         _stream(q.device)), "qlinear_paged_attention")
+    return out
+
+
+# ---------------------------------------------------------------- pages
+
+def copy_pages(caches, pairs: torch.Tensor) -> None:
+    """Page pairs[i][1] becomes a copy of page pairs[i][0] in every cache of
+    `caches` (a model's layers, one shape); pairs int32 [moves][2]. No page may
+    be a target and appear in another pair."""
+    caches = list(caches)
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [moves][2]")
+    _dev(pairs, "pairs", torch.int32)
+    for c in caches:
+        _same_device(c.k, pairs=pairs)
+    arr = (qlinear_kv_cache * max(1, len(caches)))(*[c.c for c in caches])
+    _check(lib().qlinear_copy_pages(arr, len(caches), _ptr(pairs), int(pairs.shape[0]), _stream(pairs.device)),
+           "qlinear_copy_pages")
+
+
+# ---------------------------------------------------------------- norm
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None) -> torch.Tensor:
+    """y = h / sqrt(mean(h^2) + eps) * weight over the last dimension, with
+    h = x + residual rounded to float16 (x without a residual) written to
+    residual_out if it is given (it may be x or residual). out may be x."""
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    K = int(x.shape[-1])
+    _dev(x, "x", torch.float16)
+    _dev(weight, "weight", torch.float16, (K,))
+    if residual is not None:
+        _dev(residual, "residual", torch.float16, tuple(x.shape))
+    if out is None:
+        out = torch.empty_like(x)
+    _dev(out, "out", torch.float16, tuple(x.shape))
+    if residual_out is not None:
+        _dev(residual_out, "residual_out", torch.float16, tuple(x.shape))
+    _same_device(x, weight=weight, residual=residual, out=out, residual_out=residual_out)
+    M = x.numel() // K if K else 0
+    _check(lib().qlinear_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), M, K, float(eps), _ptr(out),
+                                  _ptr(residual_out), _stream(x.device)), "qlinear_rms_norm")
+    return out

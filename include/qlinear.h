@@ -391,6 +391,169 @@ int qlinear_kv_dequant(const uint32_t* codes, const uint16_t* scales, int64_t ro
                        int32_t group, uint16_t* x, void* stream);
 
 /*
+ * Paged key/value cache of one layer: pools of pages, each page holding
+ * page_size token slots of every key/value head, head by head, so that one
+ * head's rows of a page are contiguous.
+ *   bits == 16: k, v float16 [num_pages][kv_heads][page_size][head_dim]
+ *   bits 8, 6, 4: rows in the codec format of qlinear_kv_quant (blocks of
+ *     `group` elements): k, v uint32 [num_pages][kv_heads][page_size]
+ *     [head_dim * bits / 32], k_scales, v_scales float16 [num_pages][kv_heads]
+ *     [page_size][head_dim / group]; the value of an element is the codec's
+ *     dequantized float16. With bits == 16 the scales and group are ignored.
+ * Slot s of the cache is token slot s % page_size of page s / page_size. A
+ * sequence of L tokens owns the pages block_table[0 .. ceil(L / page_size) - 1]:
+ * its token t sits in slot t % page_size of page block_table[t / page_size].
+ * page_size: 16, 32, 64, 128 or 256; head_dim: 64, 128 or 256; num_pages >= 1.
+ * The struct is HOST memory, read during the call only; the pools are device
+ * memory, 16-byte aligned. Errors of every call that takes one:
+ * INVALID_ARGUMENT (NULL, num_pages or kv_heads < 1), UNSUPPORTED (another
+ * page size, head_dim, width or group, head_dim % group != 0, more than 2^30
+ * slots, or kv_heads > 65535), MISALIGNED.
+ */
+typedef struct qlinear_kv_cache {
+  void* k;
+  void* v;
+  uint16_t* k_scales;
+  uint16_t* v_scales;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t bits;
+  int32_t group;
+} qlinear_kv_cache;
+
+/* Which elements of a head's first rot_dim form the pairs that rotary
+ * positions turn. */
+#define QLINEAR_ROPE_HALF 0        /* (i, i + rot_dim / 2) */
+#define QLINEAR_ROPE_INTERLEAVED 1 /* (2 i, 2 i + 1) */
+
+/*
+ * Rotary positions: pair i of a head's first rot_dim elements, (a, b), of a
+ * token at position p becomes
+ *   (a * c - b * s, b * c + a * s), (c, s) = table[p][i]
+ * computed in float32 as written (each product and the sum rounded once) and
+ * rounded once to float16; elements from rot_dim on are copied.
+ *   x         : float16 [tokens][heads][head_dim], token t at x + t * x_stride
+ *               (elements; a slice of a fused projection's output, say)
+ *   positions : int32 [tokens]; a position outside 0 .. table_rows - 1 gives
+ *               NaN in the rotated elements
+ *   table     : float32 [table_rows][rot_dim / 2][2], (cos, sin) of each
+ *               position and pair; any scaling for long contexts is in it
+ *   out       : as x with out_stride; may be x itself with the same stride
+ * head_dim and rot_dim multiples of 16, rot_dim <= head_dim <= 512; strides
+ * multiples of 8, at least heads * head_dim. tokens == 0 or heads == 0 is a
+ * no-op. Errors: INVALID_ARGUMENT (a negative size, NULL, table_rows < 1, a
+ * stride too small), UNSUPPORTED (the dimensions, another layout, a stride
+ * not a multiple of 8, heads > 65535, tokens >= 2^22), MISALIGNED (x, table, out 16 bytes,
+ * positions 4).
+ */
+int qlinear_rope(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t heads, int32_t head_dim,
+                 const int32_t* positions, const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout,
+                 uint16_t* out, int64_t out_stride, void* stream);
+
+/*
+ * The rotary step of a layer and its append to the cache in one launch: q is
+ * rotated into q_out, k is rotated and v taken as it is into the cache slots
+ * slots[t], for a quantized cache through the codec (on the float16 rotated
+ * values; a block holding a NaN gets a NaN scale).
+ *   q, k, v   : float16 [tokens][q_heads or kv_heads][head_dim], each with a
+ *               token stride in elements
+ *   q_out     : float16 [tokens][q_heads][head_dim], token stride
+ *               q_out_stride; may be q itself with the same stride
+ *   slots     : int32 [tokens], distinct; a token whose slot is negative or
+ *               past the pool is not appended (its q is still rotated)
+ *   positions, table, rot_dim, layout : as for qlinear_rope; rot_dim == 0
+ *               appends k as it is (positions and table may be NULL)
+ * q_heads == 0 rotates no q (q and q_out may be NULL). tokens == 0 is a no-op.
+ * Other errors as for qlinear_rope and the cache (k, v MISALIGNED at 16 bytes).
+ */
+int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t q_heads,
+                        const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out,
+                        int64_t q_out_stride, int32_t tokens, const int32_t* positions, const int32_t* slots,
+                        const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout, void* stream);
+
+/*
+ * Attention of each sequence's new tokens over its cached ones, causal. A
+ * batch holds `batch` sequences; sequence b has kv_len[b] = L tokens in the
+ * cache, the last n of them new: its new token i (0 <= i < n) has position
+ * p = L - n + i and sees the tokens t with 0 <= t <= p, and with a window
+ * w > 0 only t > p - w. Query head h reads key/value head
+ * h / (q_heads / kv_heads).
+ *   out[r][h] = RNE_fp16( sum_t softmax_t(scale * q[r][h] . k[t]) v[t] )
+ * over the tokens it sees; zeros where it sees none (p < 0). Scores, the
+ * softmax and all sums are float32; the softmax weights are rounded to
+ * float16 for the product with v. One new token per sequence is decoding;
+ * more are a prompt, a chunk of one, or drafted tokens to verify, and a batch
+ * may mix them.
+ *   q         : float16 [tokens][q_heads][head_dim], token stride q_stride
+ *   q_start   : int32 [batch + 1], sequence b's new tokens are the rows
+ *               q_start[b] .. q_start[b + 1] - 1 of q; non-decreasing. Rows
+ *               of no sequence are not written. NULL: tokens / batch rows
+ *               each (tokens % batch == 0).
+ *   kv_len    : int32 [batch]
+ *   block_table : int32 [batch][table_width], see qlinear_kv_cache; entries
+ *               past a sequence's pages are not read. A length is taken to be
+ *               at most table_width * page_size.
+ *   max_q_len, max_kv_len : upper bounds of n and L that the launch is
+ *               planned for (tokens, table_width * page_size at most are used)
+ *   window    : 0 = none
+ *   out       : float16 [tokens][q_heads][head_dim], contiguous; not q
+ *   workspace : qlinear_paged_attention_workspace_bytes of the same sizes;
+ *               scratch, as for qlinear_qgemv
+ * Cache slots that no new token of the sequence sees never reach its result,
+ * whatever they hold; nor do tokens that other rows see reach a row that does
+ * not see them. A page number outside the pool reads some page inside it.
+ * tokens == 0 or batch == 0 is a no-op.
+ * Errors: INVALID_ARGUMENT (NULL, a negative size, q_heads or table_width
+ * < 1, q_stride < q_heads * head_dim, tokens % batch without q_start, a scale
+ * that is not finite), UNSUPPORTED (q_heads not a multiple of kv_heads,
+ * q_heads > 65535, batch > 65535, q_stride % 8 != 0, more than 2^31 - 1 rows
+ * tokens * q_heads), MISALIGNED (q, out, workspace 16 bytes; the int32 arrays
+ * 4), WORKSPACE.
+ */
+int qlinear_paged_attention_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,
+                                            int32_t batch, int32_t max_q_len, int32_t max_kv_len, int32_t window,
+                                            size_t* bytes);
+int qlinear_paged_attention(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t tokens,
+                            int32_t q_heads, int32_t batch, const int32_t* q_start, const int32_t* kv_len,
+                            const int32_t* block_table, int32_t table_width, int32_t max_q_len, int32_t max_kv_len,
+                            float scale, int32_t window, uint16_t* out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * Copy pages inside each of `count` caches (a model's layers, which share one
+ * page numbering): for every i < moves, page pairs[i][1] becomes a copy of
+ * page pairs[i][0], in k, v and the scales. All copies happen as if at once
+ * only if no page is the target of one pair and the source or target of
+ * another; the call does not check that. A pair with a page outside the pool
+ * is skipped. pairs: int32 [moves][2], device. caches_host: HOST array, all of
+ * one shape (num_pages, page_size, kv_heads, head_dim, bits, group).
+ * count == 0 or moves == 0 is a no-op.
+ * Errors: INVALID_ARGUMENT (NULL, a negative size), UNSUPPORTED (caches of
+ * different shapes), MISALIGNED (pairs 8 bytes), and those of the caches.
+ */
+int qlinear_copy_pages(const qlinear_kv_cache* caches_host, int32_t count, const int32_t* pairs, int32_t moves,
+                       void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h[m][k] = RNE_fp16(x[m][k] + residual[m][k])   (h = x without a residual)
+ *   y[m][k] = RNE_fp16(h[m][k] / sqrt(mean_k h[m][k]^2 + eps) * weight[k])
+ * with float32 sums. The norm is of the rounded h, the value the residual
+ * stream keeps.
+ *   x, residual (or NULL) : float16 [M][K];  weight : float16 [K]
+ *   y            : float16 [M][K]; may be x
+ *   residual_out : float16 [M][K], receives h; may be x or residual; NULL if
+ *                  h is not wanted. Not y.
+ * Any K >= 1. M == 0 is a no-op. Errors: INVALID_ARGUMENT (NULL, M < 0,
+ * K < 1, eps negative or not finite, y == residual_out), UNSUPPORTED
+ * (K > 2^24, M >= 2^22), MISALIGNED (16 bytes).
+ */
+int qlinear_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t M, int32_t K,
+                     float eps, uint16_t* y, uint16_t* residual_out, void* stream);
+
+/*
  * On-the-fly LoRA update of a linear layer (ExLlamaV2 project page, LoRA
  * adapters: the low-rank pair A, B is applied during the forward pass
  * instead of being merged into the weights, and several adapters combine

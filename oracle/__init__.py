@@ -25,6 +25,8 @@ Every function follows the pages' description of the method:
 * The Q4/Q6/Q8 KV-cache codec (ExLlamaV2 blog, comparison table and "How to
   Use Effectively", Step 2): a block format of this package's own
   (``kv_oracle``), since the pages give only the modes and their savings.
+* The operators between the linear layers (``decoder_oracle``): attention over
+  a cache, rotary positions, the root-mean-square norm.
 """
 
 from .qlinear_oracle import (  # noqa: F401
@@ -68,3 +70,4 @@ from .kv_oracle import (  # noqa: F401
     kv_dequantize,
     kv_bytes_per_element,
 )
+from . import decoder_oracle as decoder  # noqa: F401
