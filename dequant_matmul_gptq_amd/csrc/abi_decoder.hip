@@ -25,7 +25,7 @@ int check_cache(const qlinear_kv_cache* c) {
   if (P != 16 && P != 32 && P != 64 && P != 128 && P != 256) return QLINEAR_ERR_UNSUPPORTED;
   if (D != 64 && D != 128 && D != 256) return QLINEAR_ERR_UNSUPPORTED;
   if (c->bits != 16 && c->bits != 8 && c->bits != 6 && c->bits != 4) return QLINEAR_ERR_UNSUPPORTED;
-  if ((int64_t)c->num_pages * P > kMaxSlots || c->kv_heads > 65535) return QLINEAR_ERR_UNSUPPORTED;
+  if ((int64_t)c->num_pages * P > kMaxSlots || c->kv_heads > 4096) return QLINEAR_ERR_UNSUPPORTED;
   if (c->bits != 16) {
     if ((c->group != 32 && c->group != 64 && c->group != 128) || D % c->group != 0) return QLINEAR_ERR_UNSUPPORTED;
     if (!c->k_scales || !c->v_scales) return QLINEAR_ERR_INVALID_ARGUMENT;

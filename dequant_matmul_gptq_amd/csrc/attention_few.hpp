@@ -1,0 +1,531 @@
+// Attention for few query rows per key/value head (single tokens, drafts):
+// bound by reading the cache. The rows of one sequence and key/value head,
+// up to 16 NT (token, head of the group) pairs, are the columns of 16-wide
+// matrix-core tiles, so that the cache is read once for all of them.
+//
+// A workgroup takes a range of the sequence's tokens; its four waves take
+// steps of 32 tokens in turn, each with its own running maximum and sums,
+// and join at the end. Keys and values go from memory straight into matrix
+// fragments, with no LDS between:
+//   - S^T tile i (16 tokens): lane (c, g) = (l % 16, l / 16) holds key c's
+//     elements of k-group g. float16: 8 elements at 32 f + 8 g for fragment
+//     f, so that four lanes cover 64 contiguous bytes of a row. Quantized:
+//     the lane's fragments are one contiguous run of D / 4 elements, which
+//     has one scale per 32 elements at most; q is laid out in the order in
+//     which the codes unpack.
+//   - O^T: lane (c, g) holds tokens 4 g .. + 3 and 16 + 4 g .. + 3 (the rows
+//     of S^T in its accumulators) and elements W c .. W c + W - 1 of them
+//     (W = 8, 4 at D = 64); fragment j pairs up element j of its 8 tokens by
+//     byte permutes (float16) or while unpacking (codes of two tokens share
+//     a register's halves).
+// A step's key loads are issued before the previous step's softmax, its
+// value loads after the previous step's second product.
+#pragma once
+
+#include "attention.hpp"
+
+namespace qlinear {
+namespace attn {
+
+constexpr int kFewWaves = 4;
+
+// Raw registers of one step.
+template <int D, int B>
+struct KeyRaw {
+  static constexpr int kScales = D == 256 ? 2 : 1;
+  // words of a lane's row part (D / 4 codes, or D / 32 fragments of float16)
+  static constexpr int kWords = B == 16 ? D / 8 : D / 4 * B / 32;
+  uint32_t w[2][kWords];
+  uint16_t s[2][kScales];
+};
+
+template <int D, int B>
+struct ValueRaw {
+  static constexpr int W = D == 64 ? 4 : 8;     // elements of a token per lane and part
+  static constexpr int U = D / (16 * W);        // parts (128 elements apart)
+  static constexpr int kWords = B == 16 ? W / 2 : B == 6 ? 2 : (W * B + 31) / 32;
+  uint32_t w[8][U][kWords];
+  uint16_t s[8][U];
+};
+
+// N words, 4-byte aligned.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint32_t* p) {
+  typedef u32x4 __attribute__((aligned(4))) u32x4_a4;
+  typedef u32x2 __attribute__((aligned(4))) u32x2_a4;
+#pragma unroll
+  for (int i = 0; i + 4 <= N; i += 4) {
+    const u32x4 v = *reinterpret_cast<const u32x4_a4*>(p + i);
+    w[i] = v[0];
+    w[i + 1] = v[1];
+    w[i + 2] = v[2];
+    w[i + 3] = v[3];
+  }
+  if constexpr (N % 4 >= 2) {
+    const u32x2 v = *reinterpret_cast<const u32x2_a4*>(p + N / 4 * 4);
+    w[N / 4 * 4] = v[0];
+    w[N / 4 * 4 + 1] = v[1];
+  }
+  if constexpr (N % 2 == 1) w[N - 1] = p[N - 1];
+}
+
+// Keys of tile i: pool row r0 is its first token's.
+template <int D, int B>
+__device__ __forceinline__ void load_keys(KeyRaw<D, B>& k, int i, const qlinear_kv_cache& c, int group_shift,
+                                          int64_t r0, int col, int g) {
+  if constexpr (B == 16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(c.k) + r0 * D + col * D + 8 * g;
+#pragma unroll
+    for (int f = 0; f < D / 32; ++f) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p + 32 * f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k.w[i][4 * f + e] = v[e];
+    }
+  } else {
+    constexpr int kN = KeyRaw<D, B>::kWords;
+    load_words<kN>(k.w[i], reinterpret_cast<const uint32_t*>(c.k) + r0 * (4 * kN) + col * (4 * kN) + g * kN);
+    const int per = D >> group_shift;
+#pragma unroll
+    for (int s = 0; s < KeyRaw<D, B>::kScales; ++s)
+      k.s[i][s] = c.k_scales[r0 * per + col * per + ((g * (D / 4) + 32 * s) >> group_shift)];
+  }
+}
+
+// Values of tile i: tokens 4 g .. 4 g + 3 of it.
+template <int D, int B>
+__device__ __forceinline__ void load_values(ValueRaw<D, B>& v, int i, const qlinear_kv_cache& c, int group_shift,
+                                            int64_t r0, int col, int g) {
+  constexpr int W = ValueRaw<D, B>::W;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int row = 4 * g + t;
+#pragma unroll
+    for (int u = 0; u < ValueRaw<D, B>::U; ++u) {
+      auto& w = v.w[4 * i + t][u];
+      if constexpr (B == 16) {
+        load_words<W / 2>(w, reinterpret_cast<const uint32_t*>(c.v) + r0 * (D / 2) + row * (D / 2) + u * 64 +
+                                 col * (W / 2));
+      } else {
+        const char* p = reinterpret_cast<const char*>(c.v) + r0 * (D * B / 8) + row * (D * B / 8) + u * (16 * B);
+        if constexpr (W * B == 64) {
+          load_words<2>(w, reinterpret_cast<const uint32_t*>(p + col * 8));
+        } else if constexpr (W * B == 32) {
+          w[0] = *reinterpret_cast<const uint32_t*>(p + col * 4);
+        } else if constexpr (W * B == 16) {
+          w[0] = *reinterpret_cast<const uint16_t*>(p + col * 2);
+        } else {
+          // Six bits: 8 codes are 6 bytes, 2-byte aligned; at W = 4 two lanes share them.
+          const uint16_t* q = reinterpret_cast<const uint16_t*>(p + (W == 8 ? col : col / 2) * 6);
+          w[0] = (uint32_t)q[0] | ((uint32_t)q[1] << 16);
+          w[1] = q[2];
+        }
+        const int per = D >> group_shift;
+        v.s[4 * i + t][u] = c.v_scales[r0 * per + row * per + ((u * 128 + col * W) >> group_shift)];
+      }
+    }
+  }
+}
+
+// Fragment f of tile i's keys.
+template <int D, int B>
+__device__ __forceinline__ half8 key_fragment(const KeyRaw<D, B>& k, int i, int f) {
+  u32x4 r;
+  if constexpr (B == 16) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = k.w[i][4 * f + e];
+  } else {
+    const _Float16 s = __builtin_bit_cast(_Float16, k.s[i][KeyRaw<D, B>::kScales == 1 ? 0 : f / 4]);
+    const half2v s2 = {s, s};
+    if constexpr (B == 8) {          // 2 words, byte order
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        r[e] = as_u32(code_pair<8>(__builtin_amdgcn_perm(0u, k.w[i][2 * f + e / 2], e % 2 ? 0x0C030C02u : 0x0C010C00u),
+                                   s2));
+    } else if constexpr (B == 4) {   // 1 word: pairs (e, e + 4)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = as_u32(code_pair<4>((k.w[i][f] >> (4 * e)) & 0x000F000Fu, s2));
+    } else {                         // units 2 (f / 2) and + 1 of 48 bits: pairs across them
+      const uint32_t* w = &k.w[i][f / 2 * 3];
+      // unit a: bits 0 .. 47 of w[0..2], unit b: bits 48 .. 95
+      uint32_t x, y;
+      if (f % 2 == 0) {              // codes 0 .. 3: windows at bits 0 and 12
+        const uint32_t b0 = __builtin_amdgcn_alignbit(w[2], w[1], 16);
+        x = lo_halves(w[0], b0);
+        y = lo_halves(w[0] >> 12, b0 >> 12);
+      } else {                       // codes 4 .. 7: windows at bits 24 and 36
+        x = lo_halves(__builtin_amdgcn_alignbit(w[1], w[0], 24), w[2] >> 8);
+        y = lo_halves(w[1] >> 4, w[2] >> 20);
+      }
+      r[0] = as_u32(code_pair<6>(x & 0x003F003Fu, s2));
+      r[1] = as_u32(code_pair<6>((x >> 6) & 0x003F003Fu, s2));
+      r[2] = as_u32(code_pair<6>(y & 0x003F003Fu, s2));
+      r[3] = as_u32(code_pair<6>((y >> 6) & 0x003F003Fu, s2));
+    }
+  }
+  return __builtin_bit_cast(half8, r);
+}
+
+// Element (0 .. D / 4 - 1, of the lane's run for codes; of its fragments for
+// float16) that position e of fragment f multiplies.
+template <int D, int B>
+__device__ __forceinline__ constexpr int q_element(int f, int e) {
+  if (B == 4) return 8 * f + e / 2 + 4 * (e % 2);
+  if (B == 6) return 8 * (f / 2 * 2 + e % 2) + 4 * (f % 2) + e / 2;
+  return 8 * f + e;
+}
+
+// Fragments of part u's W elements over the lane's 8 tokens.
+template <int D, int B>
+__device__ __forceinline__ void value_fragments(const ValueRaw<D, B>& v, int u, int col,
+                                                u32x4 (&r)[ValueRaw<D, B>::W]) {
+  constexpr int W = ValueRaw<D, B>::W;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {       // tokens 2 t, 2 t + 1
+    const uint32_t* a = v.w[2 * t][u];
+    const uint32_t* b = v.w[2 * t + 1][u];
+    if constexpr (B == 16) {
+#pragma unroll
+      for (int j = 0; j < W / 2; ++j) {
+        r[2 * j][t] = lo_halves(a[j], b[j]);
+        r[2 * j + 1][t] = hi_halves(a[j], b[j]);
+      }
+    } else {
+      const half2v s = {__builtin_bit_cast(_Float16, v.s[2 * t][u]), __builtin_bit_cast(_Float16, v.s[2 * t + 1][u])};
+      if constexpr (B == 8) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const uint32_t k = j % 4;
+          r[j][t] = as_u32(code_pair<8>(__builtin_amdgcn_perm(b[j / 4], a[j / 4], 0x0C000C00u | k | ((4u + k) << 16)), s));
+        }
+      } else if constexpr (B == 4) {
+#pragma unroll
+        for (int h = 0; h < W / 4; ++h) {
+          const uint32_t x = h ? hi_halves(a[0], b[0]) : lo_halves(a[0], b[0]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[4 * h + j][t] = as_u32(code_pair<4>((x >> (4 * j)) & 0x000F000Fu, s));
+        }
+      } else {
+        uint32_t x[4];
+        if constexpr (W == 8) {
+          x[0] = lo_halves(a[0], b[0]);
+          x[1] = lo_halves(a[0] >> 12, b[0] >> 12);
+          x[2] = lo_halves(__builtin_amdgcn_alignbit(a[1], a[0], 24), __builtin_amdgcn_alignbit(b[1], b[0], 24));
+          x[3] = lo_halves(a[1] >> 4, b[1] >> 4);
+        } else {                       // the lane's half of the 48 bits
+          const uint32_t sh = 24 * (col & 1);
+          const uint32_t p = (uint32_t)((((uint64_t)a[1] << 32) | a[0]) >> sh);
+          const uint32_t q = (uint32_t)((((uint64_t)b[1] << 32) | b[0]) >> sh);
+          x[0] = lo_halves(p, q);
+          x[1] = lo_halves(p >> 12, q >> 12);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) r[j][t] = as_u32(code_pair<6>((x[j / 2] >> (6 * (j % 2))) & 0x003F003Fu, s));
+      }
+    }
+  }
+}
+
+template <int D, int B, int NT>
+__global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
+                                                                       Partials part) {
+  typedef ValueRaw<D, B> VR;
+  constexpr int W = VR::W, U = VR::U, kTiles = D / 16, kFrags = D / 32;
+  constexpr int kRow = D + 4;     // LDS row of the join, in floats
+  __shared__ float join[kFewWaves][16][kRow];
+  __shared__ float2 join_ml[kFewWaves][16];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int group = a.q_heads / c.kv_heads;
+  const int split = blockIdx.x, head = blockIdx.y % c.kv_heads, tile = blockIdx.y / c.kv_heads;
+  const int page_shift = __builtin_ctz(c.page_size);
+  const int group_shift = B == 16 ? 0 : __builtin_ctz(c.group);
+
+  Work w;
+  sequence(a, c, blockIdx.z, w);
+  if (tile * 16 * NT >= w.n * group) return;
+  row_tile(a, group, tile * 16 * NT, 16 * NT, w);
+
+  // Steps of the tile and this workgroup's share of them.
+  const int step_lo = w.lo_min / kStep;
+  const int step_end = w.p_max < 0 ? 0 : w.p_max / kStep + 1;
+  const int begin = step_lo + split * plan.chunk;
+  const int end = split == plan.splits - 1 ? step_end : min(begin + plan.chunk, step_end);
+
+  if (begin >= end && plan.splits > 1) {   // nothing in this range
+    for (int r = threadIdx.x; r < w.rows; r += 64 * kFewWaves) {
+      const int rr = w.row0 + r;
+      const int64_t out_row = (int64_t)(w.q0 + rr / group) * a.q_heads + head * group + rr % group;
+      part.ml[(int64_t)split * a.tokens * a.q_heads + out_row] = make_float2(-INFINITY, 0.0f);
+    }
+    return;
+  }
+
+  // Rows: column col of tile nt is row row0 + 16 nt + col of the sequence.
+  int pos[NT], first[NT];
+  half8 q[NT][kFrags];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 16 * nt + col;
+    const bool live = r < w.rows;
+    const int rr = w.row0 + (live ? r : 0);
+    const int tok = rr / group, h = head * group + rr % group;
+    pos[nt] = w.len - w.n + tok;
+    first[nt] = first_seen(pos[nt], a.window);
+    const uint16_t* p = a.q + (w.q0 + tok) * a.q_stride + (int64_t)h * D;
+    uint32_t run[D / 8];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+      u32x4 v = {0, 0, 0, 0};
+      if (live)
+        v = *reinterpret_cast<const u32x4*>(p + (B == 16 ? 32 * f + 8 * g : g * (D / 4) + 8 * f));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) run[4 * f + e] = v[e];
+    }
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int x = q_element<D, B>(f, e);
+        q[nt][f][e] = as_half2(run[x / 2])[x % 2];
+      }
+    }
+  }
+
+  const int32_t* table = a.block_table + (int64_t)w.b * a.table_width;
+  const int last_page = max(w.len - 1, 0) >> page_shift;
+  float4v o[NT][kTiles];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = -INFINITY;
+    l[nt] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) o[nt][j] = float4v{0, 0, 0, 0};
+  }
+  const float sc = a.scale * kLog2e;
+
+  KeyRaw<D, B> kr;
+  VR vr;
+  auto keys = [&](int step) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      load_keys<D, B>(kr, i, c, group_shift,
+                      tile_row(a, c, table, page_shift, last_page, head, step * kStep + 16 * i), col, g);
+  };
+  auto values = [&](int step) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      load_values<D, B>(vr, i, c, group_shift,
+                        tile_row(a, c, table, page_shift, last_page, head, step * kStep + 16 * i), col, g);
+  };
+
+  int step = begin + wave;
+  if (step < end) {
+    keys(step);
+    values(step);
+  }
+  for (; step < end; step += kFewWaves) {
+    const int t0 = step * kStep;
+    const bool more = step + kFewWaves < end;
+    // S^T: tile i, row 4 g + r of it in register r.
+    float4v s[NT][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][i] = float4v{0, 0, 0, 0};
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) {
+        const half8 kf = key_fragment<D, B>(kr, i, f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          s[nt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[nt][f], s[nt][i], 0, 0, 0);
+      }
+    }
+    if (more) keys(step + kFewWaves);
+
+    // A step that some row sees only a part of: hide the rest from it.
+    const bool edge = t0 + kStep - 1 > w.p_min || t0 < w.lo_max;
+    half8 p[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = s[nt][i / 4][i % 4] * sc;
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = t0 + 16 * (i / 4) + 4 * g + i % 4;
+          if (t > pos[nt] || t < first[nt]) x[i] = -INFINITY;
+        }
+      }
+      float mx = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
+      mx = fmaxf(mx, swap16(mx));
+      mx = fmaxf(mx, swap32(mx));
+      const float mn = fmaxf(m[nt], mx);
+      const float base = mn == -INFINITY ? 0.0f : mn;
+      const float alpha = __builtin_amdgcn_exp2f(m[nt] - base);
+      m[nt] = mn;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e = __builtin_amdgcn_exp2f(x[i] - base);
+        sum += e;
+        p[nt][i] = (_Float16)e;
+      }
+      l[nt] = l[nt] * alpha + sum;
+      if (__any(alpha != 1.0f)) {       // the maxima settle after a few steps
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[nt][j][r] *= alpha;
+      }
+    }
+
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      u32x4 vf[W];
+      value_fragments<D, B>(vr, u, col, vf);
+      bool bad = false;
+      if (edge) {
+        // Tokens that no row sees may hold anything: zero. Weights of 0 are
+        // not enough for what only some rows see (0 times infinity): if such
+        // a step holds non-finite values, each row is multiplied on its own.
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int ta = t0 + 16 * (t / 2) + 4 * g + 2 * (t % 2);
+          const uint32_t keep = (ta <= w.p_max && ta >= w.lo_min ? 0x0000FFFFu : 0u) |
+                                (ta + 1 <= w.p_max && ta + 1 >= w.lo_min ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            vf[j][t] &= keep;
+            bad |= nonfinite_pair(vf[j][t]);
+          }
+        }
+        bad = w.p_min != w.p_max && __any(bad);
+      }
+      if (!bad) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            o[nt][u * W + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, vf[j]), p[nt],
+                                                                      o[nt][u * W + j], 0, 0, 0);
+      } else {
+        for (int r = 0; r < 16; ++r) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int pr = __builtin_amdgcn_readlane(pos[nt], r), fr = __builtin_amdgcn_readlane(first[nt], r);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              u32x4 x = vf[j];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const int ta = t0 + 16 * (t / 2) + 4 * g + 2 * (t % 2);
+                x[t] &= (ta <= pr && ta >= fr ? 0x0000FFFFu : 0u) | (ta + 1 <= pr && ta + 1 >= fr ? 0xFFFF0000u : 0u);
+              }
+              const float4v y = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, x), p[nt],
+                                                                       o[nt][u * W + j], 0, 0, 0);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][u * W + j][e] = col == r ? y[e] : o[nt][u * W + j][e];
+            }
+          }
+        }
+      }
+    }
+    if (more) values(step + kFewWaves);
+  }
+
+  // The four waves join. Register r of O^T tile u W + j is element
+  // 128 u + 4 W g + W r + j of row col.
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float sum = l[nt];
+    sum += swap16(sum);
+    sum += swap32(sum);
+    if (nt) __syncthreads();
+    if (g == 0) join_ml[wave][col] = make_float2(m[nt], sum);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < W; j += 4) {
+          const float4v v = {o[nt][u * W + j][r], o[nt][u * W + j + 1][r], o[nt][u * W + j + 2][r],
+                             o[nt][u * W + j + 3][r]};
+          *reinterpret_cast<float4v*>(&join[wave][col][128 * u + 4 * W * g + W * r + j]) = v;
+        }
+    __syncthreads();
+    // Thread: row t / 16 of the tile, D / 16 elements of it.
+    const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 4;
+    const int rr = 16 * nt + row;
+    if (rr < w.rows) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kFewWaves; ++i) top = fmaxf(top, join_ml[i][row].x);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float f[kFewWaves], total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kFewWaves; ++i) {
+        f[i] = __builtin_amdgcn_exp2f(join_ml[i][row].x - base);
+        total += f[i] * join_ml[i][row].y;
+      }
+      const int tok = (w.row0 + rr) / group, h = head * group + (w.row0 + rr) % group;
+      const int pr = w.len - w.n + tok, fr = first_seen(pr, a.window);
+      const int64_t out_row = (int64_t)(w.q0 + tok) * a.q_heads + h;
+      const bool alone = plan.splits == 1;
+      const float inv = pr < fr ? 0.0f : 1.0f / total;
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) {
+        float4v v = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kFewWaves; ++i) {
+          const float4v x = *reinterpret_cast<const float4v*>(&join[i][row][d * 64 + d0]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += f[i] * x[e];
+        }
+        if (alone) {
+          half4 y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = (_Float16)(pr < fr ? 0.0f : v[e] * inv);
+          *reinterpret_cast<half4*>(a.out + out_row * D + d * 64 + d0) = y;
+        } else {
+          *reinterpret_cast<float4v*>(part.o + ((int64_t)split * a.tokens * a.q_heads + out_row) * D + d * 64 + d0) = v;
+        }
+      }
+      if (!alone && d0 == 0) {
+        // A range that the row sees part of, all of it at -infinity, is not an empty one.
+        const bool sees = max(fr, begin * kStep) <= min(pr, end * kStep - 1);
+        part.ml[(int64_t)split * a.tokens * a.q_heads + out_row] =
+            make_float2(top == -INFINITY && sees ? kLowest : top, total);
+      }
+    }
+  }
+}
+
+template <int D, int B>
+hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
+                      hipStream_t stream) {
+  const int group = a.q_heads / c.kv_heads;
+  const int tiles = (int)(((int64_t)a.max_q_len * group + p.rows - 1) / p.rows);
+  const dim3 grid((unsigned)p.splits, (unsigned)(c.kv_heads * tiles), (unsigned)a.batch);
+  if (p.rows == 16)
+    hipLaunchKernelGGL((attention_few_kernel<D, B, 1>), grid, dim3(64 * kFewWaves), 0, stream, a, c, p, part);
+  else if constexpr (D < 256)
+    hipLaunchKernelGGL((attention_few_kernel<D, B, 2>), grid, dim3(64 * kFewWaves), 0, stream, a, c, p, part);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_few_width(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
+                            hipStream_t stream) {
+  if (c.bits == 16) return launch_few<D, 16>(c, a, p, part, stream);
+  if (c.bits == 8) return launch_few<D, 8>(c, a, p, part, stream);
+  if (c.bits == 6) return launch_few<D, 6>(c, a, p, part, stream);
+  return launch_few<D, 4>(c, a, p, part, stream);
+}
+
+}  // namespace attn
+}  // namespace qlinear

@@ -1,13 +1,13 @@
 // Attention of new tokens over a paged cache, one wave per (token, query
 // head): 64 keys a step, one per lane, with the running maximum m and sum l of
 // the softmax; o and l are scaled by exp(m_old - m_new) when m grows.
-#include "qlinear_kernels.hpp"
+#include "attention.hpp"
 
 namespace qlinear {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+using namespace attn;
 
 // Element d of cache row r of a pool.
 __device__ __forceinline__ float cache_value(const void* pool, const uint16_t* scales, int64_t r, int d, int D,
@@ -86,13 +86,100 @@ __global__ __launch_bounds__(256) void attention_row_kernel(AttentionArgs a, qli
         __builtin_bit_cast(uint16_t, (_Float16)(l > 0.0f || l != l ? o[i] / l : 0.0f));
 }
 
+// Joins the partial results of a split call: one workgroup per row, its waves
+// take splits in turn, then add in a fixed order.
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Partials part, int splits, int D) {
+  __shared__ float sums[4][256];
+  __shared__ float totals[4];
+  const int64_t row = blockIdx.x, rows = (int64_t)a.tokens * a.q_heads;
+  const int tok = blockIdx.x / a.q_heads;
+  if (a.q_start && (tok < a.q_start[0] || tok >= a.q_start[a.batch])) return;   // of no sequence
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float top = -INFINITY;
+  for (int s = lane; s < splits; s += 64) top = fmaxf(top, part.ml[s * rows + row].x);
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+  const int n = D / 64;
+  float o[4] = {0, 0, 0, 0}, total = 0.0f;
+  for (int s = wave; s < splits; s += 4) {
+    const float2 ml = part.ml[s * rows + row];
+    if (ml.x == -INFINITY) continue;      // an empty range: o was not written
+    const float f = __builtin_amdgcn_exp2f(ml.x - top);
+    total += f * ml.y;
+    const float* p = part.o + (s * rows + row) * D + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) o[i] += f * p[64 * i];
+  }
+  for (int i = 0; i < n; ++i) sums[wave][64 * i + lane] = o[i];
+  if (lane == 0) totals[wave] = total;
+  __syncthreads();
+  total = totals[0] + totals[1] + totals[2] + totals[3];
+  for (int d = threadIdx.x; d < D; d += 256) {
+    const float v = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
+    a.out[row * D + d] = __builtin_bit_cast(uint16_t, (_Float16)(top == -INFINITY ? 0.0f : v / total));
+  }
+}
+
+// Tokens a row tile can see at most, in steps.
+int64_t plan_steps(const AttentionArgs& a) {
+  int64_t n = a.max_kv_len;
+  if (a.window > 0 && (int64_t)a.window + a.max_q_len < n) n = (int64_t)a.window + a.max_q_len;
+  return n / kStep + 2;
+}
+
+constexpr int kFewRows = 64;       // most rows of a sequence per key/value head in the few-row kernel
+
+Plan make_plan(const qlinear_kv_cache& c, const AttentionArgs& a) {
+  const int64_t group = a.q_heads / c.kv_heads, rows = a.max_q_len * group;
+  Plan p;
+  p.rows = rows <= 16 || c.head_dim == 256 ? 16 : 32;   // two tiles of 256 wide heads do not fit the registers
+  p.splits = 1;
+  p.chunk = INT32_MAX;
+  if (rows > kFewRows) return p;
+  const int64_t tiles = (rows + p.rows - 1) / p.rows * c.kv_heads * a.batch;
+  const int64_t steps = plan_steps(a);
+  // A range is long enough that writing and reading its partial result is
+  // about 1/25 of reading its keys and values, unless that leaves fewer than
+  // two workgroups per CU; short enough for about 4096 workgroups.
+  const int64_t row_bytes = c.bits == 16 ? 2 * c.head_dim : c.head_dim * c.bits / 8 + 2 * c.head_dim / c.group;
+  const int64_t used = rows < p.rows ? rows : p.rows;
+  const int64_t light = 25 * used * c.head_dim * 4 / (row_bytes * kStep);
+  const int64_t even = (tiles * steps + 4095) / 4096;
+  const int64_t fill = (tiles * steps + 511) / 512;
+  int64_t chunk = even > light ? even : light;
+  if (chunk > fill) chunk = fill;
+  if (chunk < 4) chunk = 4;
+  p.splits = (int)((steps + chunk - 1) / chunk);
+  if (p.splits > 1) p.chunk = (int)chunk;
+  return p;
+}
+
 }  // namespace
 
-size_t paged_attention_workspace_bytes(const qlinear_kv_cache&, const AttentionArgs&) { return 0; }
+size_t paged_attention_workspace_bytes(const qlinear_kv_cache& cache, const AttentionArgs& a) {
+  const Plan p = make_plan(cache, a);
+  if (p.splits == 1) return 0;
+  return (size_t)p.splits * a.tokens * a.q_heads * (cache.head_dim + 2) * sizeof(float);
+}
 
-hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const AttentionArgs& a, void*, hipStream_t stream) {
+hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const AttentionArgs& a, void* ws,
+                                  hipStream_t stream) {
+  const Plan p = make_plan(cache, a);
   const int64_t rows = (int64_t)a.tokens * a.q_heads;
-  hipLaunchKernelGGL(attention_row_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, cache);
+  if ((int64_t)a.max_q_len * (a.q_heads / cache.kv_heads) > kFewRows) {
+    hipLaunchKernelGGL(attention_row_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, cache);
+    return hipGetLastError();
+  }
+  Partials part = {};
+  part.o = (float*)ws;
+  if (p.splits > 1) part.ml = (float2*)(part.o + (int64_t)p.splits * rows * cache.head_dim);
+  hipError_t e = cache.head_dim == 64    ? launch_attention_few_64(cache, a, p, part, stream)
+                 : cache.head_dim == 128 ? launch_attention_few_128(cache, a, p, part, stream)
+                                         : launch_attention_few_256(cache, a, p, part, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)rows), dim3(256), 0, stream, a, part, p.splits,
+                     cache.head_dim);
   return hipGetLastError();
 }
 

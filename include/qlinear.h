@@ -408,7 +408,7 @@ int qlinear_kv_dequant(const uint32_t* codes, const uint16_t* scales, int64_t ro
  * memory, 16-byte aligned. Errors of every call that takes one:
  * INVALID_ARGUMENT (NULL, num_pages or kv_heads < 1), UNSUPPORTED (another
  * page size, head_dim, width or group, head_dim % group != 0, more than 2^30
- * slots, or kv_heads > 65535), MISALIGNED.
+ * slots, or kv_heads > 4096), MISALIGNED.
  */
 typedef struct qlinear_kv_cache {
   void* k;
