@@ -107,10 +107,16 @@ __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
-// Whether either float16 of a pair is an infinity or NaN.
-__device__ __forceinline__ bool nonfinite_pair(uint32_t x) {
-  return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
-}
+// Non-finite float16 halves of a pair, as bit 15 of each half: adding to the
+// magnitude carries into that bit from 0x7C00 (infinity) or 0x7C01 (NaN) on.
+constexpr uint32_t kTops = 0x80008000u, kOnes = 0x3C003C00u;   // kOnes: a pair of 1.0
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t x) { return ((x & ~kTops) + 0x04000400u) & kTops; }
+__device__ __forceinline__ uint32_t nan_halves(uint32_t x) { return ((x & ~kTops) + 0x03FF03FFu) & kTops; }
+// Whole halves, or 1.0, where bit 15 says so.
+__device__ __forceinline__ uint32_t spread_top(uint32_t f) { return f | (f - (f >> 15)); }
+__device__ __forceinline__ uint32_t ones_at(uint32_t f) { return (f >> 1) - (f >> 5); }
+// Masks of a pair's halves.
+__device__ __forceinline__ uint32_t both(bool lo, bool hi) { return (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u); }
 
 // ---- codes to values. A code in the low bits of a half, OR-ed into float16
 // 1024.0, is 1024 + code exactly; minus 1024 + half of the range it is the

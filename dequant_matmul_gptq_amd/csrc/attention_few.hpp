@@ -225,14 +225,36 @@ __device__ __forceinline__ void value_fragments(const ValueRaw<D, B>& v, int u, 
   }
 }
 
+// What the infinities and NaN of a value fragment add to the rows that see
+// their tokens (column of `sees`: 1.0 where the row does): counts of tokens
+// with +infinity or NaN, and of ones with -infinity or NaN, from the same
+// matrix product as the finite values. sum: element r of the fragment's
+// result at sum[r * stride].
+__device__ __forceinline__ void add_nonfinite(const u32x4& v, const u32x4& sees, float* sum, int stride) {
+  u32x4 up, down;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t any = nonfinite_halves(v[t]), nan = nan_halves(v[t]);
+    up[t] = ones_at((any & ~v[t]) | nan);
+    down[t] = ones_at((any & v[t]) | nan);
+  }
+  const half8 b = __builtin_bit_cast(half8, sees);
+  const float4v zero = {0, 0, 0, 0};
+  const float4v nu = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, up), b, zero, 0, 0, 0);
+  const float4v nd = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, down), b, zero, 0, 0, 0);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    sum[r * stride] += (nu[r] > 0.0f ? INFINITY : 0.0f) - (nd[r] > 0.0f ? INFINITY : 0.0f);
+}
+
 template <int D, int B, int NT>
-__global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
                                                                        Partials part) {
   typedef ValueRaw<D, B> VR;
   constexpr int W = VR::W, U = VR::U, kTiles = D / 16, kFrags = D / 32;
   constexpr int kRow = D + 4;     // LDS row of the join, in floats
-  __shared__ float join[kFewWaves][16][kRow];
-  __shared__ float2 join_ml[kFewWaves][16];
+  __shared__ float join[NT][kFewWaves][16][kRow];
+  __shared__ float2 join_ml[NT][kFewWaves][16];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
@@ -305,6 +327,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(Attention
   }
   const float sc = a.scale * kLog2e;
 
+  bool nonfinite = false;      // join holds what infinities and NaN add
   KeyRaw<D, B> kr;
   VR vr;
   auto keys = [&](int step) {
@@ -388,52 +411,52 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(Attention
     for (int u = 0; u < U; ++u) {
       u32x4 vf[W];
       value_fragments<D, B>(vr, u, col, vf);
-      bool bad = false;
       if (edge) {
-        // Tokens that no row sees may hold anything: zero. Weights of 0 are
-        // not enough for what only some rows see (0 times infinity): if such
-        // a step holds non-finite values, each row is multiplied on its own.
+        // Tokens that no row sees may hold anything: zero.
+        uint32_t bad = 0;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int ta = t0 + 16 * (t / 2) + 4 * g + 2 * (t % 2);
-          const uint32_t keep = (ta <= w.p_max && ta >= w.lo_min ? 0x0000FFFFu : 0u) |
-                                (ta + 1 <= w.p_max && ta + 1 >= w.lo_min ? 0xFFFF0000u : 0u);
+          const uint32_t keep = both(ta <= w.p_max && ta >= w.lo_min, ta < w.p_max && ta + 1 >= w.lo_min);
 #pragma unroll
           for (int j = 0; j < W; ++j) {
             vf[j][t] &= keep;
-            bad |= nonfinite_pair(vf[j][t]);
+            bad |= nonfinite_halves(vf[j][t]);
           }
         }
-        bad = w.p_min != w.p_max && __any(bad);
-      }
-      if (!bad) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            o[nt][u * W + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, vf[j]), p[nt],
-                                                                      o[nt][u * W + j], 0, 0, 0);
-      } else {
-        for (int r = 0; r < 16; ++r) {
+        // A weight of 0 does not hide an infinity or NaN from the rows that
+        // do not see it (0 times infinity). Such values are taken out here, and
+        // what they add is kept apart, in this wave's rows of `join`.
+        if (w.p_min != w.p_max && __any(bad != 0)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const int pr = __builtin_amdgcn_readlane(pos[nt], r), fr = __builtin_amdgcn_readlane(first[nt], r);
+            if (!nonfinite)
+              for (int d = lane; d < 16 * kRow; d += 64) (&join[nt][wave][0][0])[d] = 0.0f;
+            u32x4 sees;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const int ta = t0 + 16 * (t / 2) + 4 * g + 2 * (t % 2);
+              sees[t] = kOnes & both(ta <= pos[nt] && ta >= first[nt], ta < pos[nt] && ta + 1 >= first[nt]);
+            }
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-              u32x4 x = vf[j];
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const int ta = t0 + 16 * (t / 2) + 4 * g + 2 * (t % 2);
-                x[t] &= (ta <= pr && ta >= fr ? 0x0000FFFFu : 0u) | (ta + 1 <= pr && ta + 1 >= fr ? 0xFFFF0000u : 0u);
-              }
-              const float4v y = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, x), p[nt],
-                                                                       o[nt][u * W + j], 0, 0, 0);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][u * W + j][e] = col == r ? y[e] : o[nt][u * W + j][e];
+              add_nonfinite(vf[j], sees, &join[nt][wave][col][128 * u + 4 * W * g + j], W);
+              __builtin_amdgcn_sched_barrier(0);     // rare: few registers matter more than overlap
             }
           }
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) vf[j][t] &= ~spread_top(nonfinite_halves(vf[j][t]));
+          nonfinite = true;
         }
       }
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          o[nt][u * W + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, vf[j]), p[nt],
+                                                                    o[nt][u * W + j], 0, 0, 0);
     }
     if (more) values(step + kFewWaves);
   }
@@ -445,32 +468,35 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(Attention
     float sum = l[nt];
     sum += swap16(sum);
     sum += swap32(sum);
-    if (nt) __syncthreads();
-    if (g == 0) join_ml[wave][col] = make_float2(m[nt], sum);
+    if (g == 0) join_ml[nt][wave][col] = make_float2(m[nt], sum);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int j = 0; j < W; j += 4) {
-          const float4v v = {o[nt][u * W + j][r], o[nt][u * W + j + 1][r], o[nt][u * W + j + 2][r],
-                             o[nt][u * W + j + 3][r]};
-          *reinterpret_cast<float4v*>(&join[wave][col][128 * u + 4 * W * g + W * r + j]) = v;
+          float4v* at = reinterpret_cast<float4v*>(&join[nt][wave][col][128 * u + 4 * W * g + W * r + j]);
+          float4v v = {o[nt][u * W + j][r], o[nt][u * W + j + 1][r], o[nt][u * W + j + 2][r], o[nt][u * W + j + 3][r]};
+          if (nonfinite) v += *at;
+          *at = v;
         }
-    __syncthreads();
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
     // Thread: row t / 16 of the tile, D / 16 elements of it.
     const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 4;
     const int rr = 16 * nt + row;
     if (rr < w.rows) {
       float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kFewWaves; ++i) top = fmaxf(top, join_ml[i][row].x);
+      for (int i = 0; i < kFewWaves; ++i) top = fmaxf(top, join_ml[nt][i][row].x);
       const float base = top == -INFINITY ? 0.0f : top;
       float f[kFewWaves], total = 0.0f;
 #pragma unroll
       for (int i = 0; i < kFewWaves; ++i) {
-        f[i] = __builtin_amdgcn_exp2f(join_ml[i][row].x - base);
-        total += f[i] * join_ml[i][row].y;
+        f[i] = __builtin_amdgcn_exp2f(join_ml[nt][i][row].x - base);
+        total += f[i] * join_ml[nt][i][row].y;
       }
       const int tok = (w.row0 + rr) / group, h = head * group + (w.row0 + rr) % group;
       const int pr = w.len - w.n + tok, fr = first_seen(pr, a.window);
@@ -482,7 +508,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(Attention
         float4v v = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < kFewWaves; ++i) {
-          const float4v x = *reinterpret_cast<const float4v*>(&join[i][row][d * 64 + d0]);
+          const float4v x = *reinterpret_cast<const float4v*>(&join[nt][i][row][d * 64 + d0]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += f[i] * x[e];
         }

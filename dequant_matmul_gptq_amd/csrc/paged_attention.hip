@@ -1,6 +1,7 @@
 // Attention of new tokens over a paged cache, one wave per (token, query
 // head): 64 keys a step, one per lane, with the running maximum m and sum l of
 // the softmax; o and l are scaled by exp(m_old - m_new) when m grows.
+#include <stdlib.h>
 #include "attention.hpp"
 
 namespace qlinear {
@@ -86,39 +87,62 @@ __global__ __launch_bounds__(256) void attention_row_kernel(AttentionArgs a, qli
         __builtin_bit_cast(uint16_t, (_Float16)(l > 0.0f || l != l ? o[i] / l : 0.0f));
 }
 
-// Joins the partial results of a split call: one workgroup per row, its waves
-// take splits in turn, then add in a fixed order.
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Partials part, int splits, int D) {
-  __shared__ float sums[4][256];
-  __shared__ float totals[4];
+// Joins the partial results of a split call, one workgroup per row: the
+// ranges' weights 2^(m - max m) first (kJoinBatch at a time in LDS), then the
+// sum over ranges with D / 4 threads to a range and several loads in flight.
+// Threads and ranges are added in a fixed order.
+constexpr int kJoinBatch = 256;
+template <int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Partials part, int splits) {
+  constexpr int kSide = 256 / (D / 4);    // ranges at a time
+  __shared__ float weight[kJoinBatch];
+  __shared__ float tops[4], sums[4];
+  __shared__ float4v o_part[kSide][D / 4];
   const int64_t row = blockIdx.x, rows = (int64_t)a.tokens * a.q_heads;
   const int tok = blockIdx.x / a.q_heads;
   if (a.q_start && (tok < a.q_start[0] || tok >= a.q_start[a.batch])) return;   // of no sequence
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = threadIdx.x, side = t / (D / 4), d = t % (D / 4);
   float top = -INFINITY;
-  for (int s = lane; s < splits; s += 64) top = fmaxf(top, part.ml[s * rows + row].x);
+  for (int s = t; s < splits; s += 256) top = fmaxf(top, part.ml[s * rows + row].x);
 #pragma unroll
   for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
-  const int n = D / 64;
-  float o[4] = {0, 0, 0, 0}, total = 0.0f;
-  for (int s = wave; s < splits; s += 4) {
-    const float2 ml = part.ml[s * rows + row];
-    if (ml.x == -INFINITY) continue;      // an empty range: o was not written
-    const float f = __builtin_amdgcn_exp2f(ml.x - top);
-    total += f * ml.y;
-    const float* p = part.o + (s * rows + row) * D + lane;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) o[i] += f * p[64 * i];
-  }
-  for (int i = 0; i < n; ++i) sums[wave][64 * i + lane] = o[i];
-  if (lane == 0) totals[wave] = total;
+  if ((t & 63) == 0) tops[t >> 6] = top;
   __syncthreads();
-  total = totals[0] + totals[1] + totals[2] + totals[3];
-  for (int d = threadIdx.x; d < D; d += 256) {
-    const float v = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
-    a.out[row * D + d] = __builtin_bit_cast(uint16_t, (_Float16)(top == -INFINITY ? 0.0f : v / total));
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+
+  float total = 0.0f;
+  float4v o = {0, 0, 0, 0};
+  for (int s0 = 0; s0 < splits; s0 += kJoinBatch) {
+    const int n = min(kJoinBatch, splits - s0);
+    if (s0) __syncthreads();
+    if (t < n) {
+      const float2 ml = part.ml[(s0 + t) * rows + row];
+      // An empty range (m = -infinity) has weight 0 and its o is not written.
+      const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+      weight[t] = ml.x == -INFINITY ? -1.0f : f;
+      total += f * ml.y;
+    }
+    __syncthreads();
+    const float4v* p = reinterpret_cast<const float4v*>(part.o) + ((int64_t)s0 * rows + row) * (D / 4) + d;
+#pragma unroll 4
+    for (int s = side; s < n; s += kSide) {
+      const float f = weight[s];
+      if (f >= 0.0f || f != f) o += f * p[s * rows * (D / 4)];
+    }
   }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k);
+  if ((t & 63) == 0) sums[t >> 6] = total;
+  o_part[side][d] = o;
+  __syncthreads();
+  if (side != 0) return;
+  total = sums[0] + sums[1] + sums[2] + sums[3];
+#pragma unroll
+  for (int i = 1; i < kSide; ++i) o += o_part[i][d];
+  half4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (_Float16)(top == -INFINITY ? 0.0f : o[e] / total);
+  *reinterpret_cast<half4*>(a.out + row * D + 4 * d) = y;
 }
 
 // Tokens a row tile can see at most, in steps.
@@ -150,6 +174,7 @@ Plan make_plan(const qlinear_kv_cache& c, const AttentionArgs& a) {
   int64_t chunk = even > light ? even : light;
   if (chunk > fill) chunk = fill;
   if (chunk < 4) chunk = 4;
+  if (getenv("QL_CHUNK")) chunk = atoi(getenv("QL_CHUNK"));
   p.splits = (int)((steps + chunk - 1) / chunk);
   if (p.splits > 1) p.chunk = (int)chunk;
   return p;
@@ -178,8 +203,10 @@ hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const Attention
                  : cache.head_dim == 128 ? launch_attention_few_128(cache, a, p, part, stream)
                                          : launch_attention_few_256(cache, a, p, part, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)rows), dim3(256), 0, stream, a, part, p.splits,
-                     cache.head_dim);
+  auto join = cache.head_dim == 64    ? attention_join_kernel<64>
+              : cache.head_dim == 128 ? attention_join_kernel<128>
+                                      : attention_join_kernel<256>;
+  hipLaunchKernelGGL(join, dim3((unsigned)rows), dim3(256), 0, stream, a, part, p.splits);
   return hipGetLastError();
 }
 
