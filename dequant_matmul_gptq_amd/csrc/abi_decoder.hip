@@ -18,6 +18,9 @@ int hip_status(hipError_t e) { return e == hipSuccess ? QLINEAR_OK : QLINEAR_ERR
 constexpr int64_t kMaxSlots = (int64_t)1 << 30;
 // Tokens and norm rows are a grid dimension, whose threads must stay below 2^32.
 constexpr int kMaxRows = (1 << 22) - 1;
+// Query rows of one attention call (a workgroup of 256 threads takes 128 rows
+// of a sequence and key/value head, or fewer where a sequence ends).
+constexpr int64_t kMaxQueryRows = (int64_t)1 << 29;
 
 int check_cache(const qlinear_kv_cache* c) {
   if (!c || !c->k || !c->v || c->num_pages < 1 || c->kv_heads < 1) return QLINEAR_ERR_INVALID_ARGUMENT;
@@ -62,7 +65,8 @@ int check_attention(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_hea
   if (tokens < 0 || batch < 0 || q_heads < 1 || max_q_len < 0 || max_kv_len < 0 || window < 0)
     return QLINEAR_ERR_INVALID_ARGUMENT;
   if (q_heads % cache->kv_heads != 0 || q_heads > 65535 || batch > 65535) return QLINEAR_ERR_UNSUPPORTED;
-  if ((int64_t)tokens * q_heads > INT32_MAX) return QLINEAR_ERR_UNSUPPORTED;
+  if ((int64_t)tokens * q_heads > kMaxQueryRows || (int64_t)batch * cache->kv_heads > kMaxQueryRows / 128)
+    return QLINEAR_ERR_UNSUPPORTED;
   return QLINEAR_OK;
 }
 
@@ -72,7 +76,7 @@ AttentionArgs attention_sizes(int32_t tokens, int32_t q_heads, int32_t batch, in
   a.tokens = tokens;
   a.q_heads = q_heads;
   a.batch = batch;
-  a.max_q_len = max_q_len < tokens ? max_q_len : tokens;
+  a.max_q_len = max_q_len < tokens ? (max_q_len > 1 ? max_q_len : 1) : tokens;
   a.max_kv_len = max_kv_len;
   a.window = window;
   return a;

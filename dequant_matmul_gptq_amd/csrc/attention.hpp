@@ -32,21 +32,34 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.4028234663852886e38f;
 
-// The launch's plan: row tiles of `rows` (token, head of the group) pairs,
-// each tile's visible tokens cut into `splits` ranges of `chunk` steps of
-// kStep tokens (the last range takes what is left).
+// A launch's plan: row tiles of `rows` (token, head of the group) pairs, each
+// tile's visible tokens cut into `splits` ranges of `chunk` steps (the last
+// range takes what is left). It serves the sequences whose rows per
+// key/value head number min_rows to max_rows.
 struct Plan {
   int rows;
   int splits;
   int chunk;
+  int min_rows, max_rows;
 };
-constexpr int kStep = 32;
+constexpr int kStep = 32;          // tokens of a step, few-row kernel
+constexpr int kChunkRows = 128;    // rows of a tile, chunk kernel
+constexpr int kFewRows = 64;       // most rows of a sequence per key/value head in the few-row kernel
+__host__ __device__ constexpr int chunk_step(int D) { return D == 256 ? 32 : 64; }   // tokens of its step
 
-// Partial results of a split call: o [splits][tokens * q_heads][D] and
-// (m, l) [splits][tokens * q_heads], float32.
+// Row tiles of the chunk kernel, at most, whatever the sequences' lengths.
+inline int64_t chunk_tiles(const AttentionArgs& a, int group) {
+  return (int64_t)a.tokens * group / kChunkRows + a.batch;
+}
+
+// Partial results of a split launch, float32: o [splits][rows][D] and (m, l)
+// [splits][rows]. Rows: those of the output (chunk kernel), or `cap` for each
+// sequence and key/value head (few-row kernel, whose sequences have no more).
 struct Partials {
   float* o;
   float2* ml;
+  int64_t rows;
+  int cap;
 };
 
 // One workgroup's sequence, row tile and token range.
@@ -94,9 +107,78 @@ __device__ __forceinline__ int64_t tile_row(const AttentionArgs& a, const qlinea
   return (((int64_t)pg * c.kv_heads + head) << page_shift) + (t & (c.page_size - 1));
 }
 
-// Maximum and sum over the four lanes l % 16 == c (l / 16 = 0 .. 3).
-__device__ __forceinline__ float swap16(float v) { return __shfl_xor(v, 16); }
-__device__ __forceinline__ float swap32(float v) { return __shfl_xor(v, 32); }
+// The sequence and row tile of tile number y, counting the tiles of the
+// sequences of at least min_rows rows, found by all lanes together. False if
+// there are fewer.
+__device__ __forceinline__ bool find_tile(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                          int group, int y, Work& w, int& tile) {
+  if (!a.q_start || a.batch == 1) {
+    sequence(a, c, 0, w);
+    const int per = (int)(((int64_t)w.n * group + kChunkRows - 1) / kChunkRows);
+    if (per == 0 || (int64_t)w.n * group < plan.min_rows) return false;
+    const int b = y / per;
+    if (b >= a.batch) return false;
+    sequence(a, c, b, w);
+    tile = y - b * per;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    int n = 0;
+    if (b0 + lane < a.batch) {
+      Work t;
+      sequence(a, c, b0 + lane, t);
+      const int64_t rows = (int64_t)t.n * group;
+      n = rows < plan.min_rows ? 0 : (int)((rows + kChunkRows - 1) / kChunkRows);
+    }
+    int upto = n;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+      const int o = __shfl_up(upto, k);
+      if (lane >= k) upto += o;
+    }
+    const uint64_t past = __ballot(upto > y);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      tile = y - __builtin_amdgcn_readlane(upto - n, at);
+      sequence(a, c, b0 + at, w);
+      return true;
+    }
+    y -= __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// Lane swaps: both halves' (rows of 16 lanes', pairwise) values of x in every lane.
+struct Two {
+  float a, b;
+};
+__device__ __forceinline__ Two swap32(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return {__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+__device__ __forceinline__ Two swap16(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return {__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+__device__ __forceinline__ float max32(float x) {
+  const Two t = swap32(x);
+  return fmaxf(t.a, t.b);
+}
+__device__ __forceinline__ float max16(float x) {
+  const Two t = swap16(x);
+  return fmaxf(t.a, t.b);
+}
+__device__ __forceinline__ float sum32(float x) {
+  const Two t = swap32(x);
+  return t.a + t.b;
+}
+__device__ __forceinline__ float sum16(float x) {
+  const Two t = swap16(x);
+  return t.a + t.b;
+}
 
 __device__ __forceinline__ half2v as_half2(uint32_t x) { return __builtin_bit_cast(half2v, x); }
 __device__ __forceinline__ uint32_t as_u32(half2v x) { return __builtin_bit_cast(uint32_t, x); }
@@ -139,5 +221,11 @@ hipError_t launch_attention_few_128(const qlinear_kv_cache& c, const AttentionAr
                                     const attn::Partials& part, hipStream_t stream);
 hipError_t launch_attention_few_256(const qlinear_kv_cache& c, const AttentionArgs& a, const attn::Plan& p,
                                     const attn::Partials& part, hipStream_t stream);
+hipError_t launch_attention_chunk_64(const qlinear_kv_cache& c, const AttentionArgs& a, const attn::Plan& p,
+                                     const attn::Partials& part, hipStream_t stream);
+hipError_t launch_attention_chunk_128(const qlinear_kv_cache& c, const AttentionArgs& a, const attn::Plan& p,
+                                      const attn::Partials& part, hipStream_t stream);
+hipError_t launch_attention_chunk_256(const qlinear_kv_cache& c, const AttentionArgs& a, const attn::Plan& p,
+                                      const attn::Partials& part, hipStream_t stream);
 
 }  // namespace qlinear

@@ -1,0 +1,11 @@
+// Chunk attention kernels for heads of 256 (attention_chunk.hpp).
+#include "attention_chunk.hpp"
+
+namespace qlinear {
+
+hipError_t launch_attention_chunk_256(const qlinear_kv_cache& c, const AttentionArgs& a, const attn::Plan& p,
+                                      const attn::Partials& part, hipStream_t stream) {
+  return attn::launch_chunk_width<256>(c, a, p, part, stream);
+}
+
+}  // namespace qlinear

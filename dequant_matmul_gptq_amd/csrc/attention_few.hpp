@@ -265,7 +265,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
 
   Work w;
   sequence(a, c, blockIdx.z, w);
-  if (tile * 16 * NT >= w.n * group) return;
+  const int64_t seq_rows = (int64_t)w.n * group;
+  if (tile * 16 * NT >= seq_rows || seq_rows > plan.max_rows) return;
   row_tile(a, group, tile * 16 * NT, 16 * NT, w);
 
   // Steps of the tile and this workgroup's share of them.
@@ -274,12 +275,10 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
   const int begin = step_lo + split * plan.chunk;
   const int end = split == plan.splits - 1 ? step_end : min(begin + plan.chunk, step_end);
 
+  const int64_t part_row0 = ((int64_t)w.b * c.kv_heads + head) * part.cap + w.row0;
   if (begin >= end && plan.splits > 1) {   // nothing in this range
-    for (int r = threadIdx.x; r < w.rows; r += 64 * kFewWaves) {
-      const int rr = w.row0 + r;
-      const int64_t out_row = (int64_t)(w.q0 + rr / group) * a.q_heads + head * group + rr % group;
-      part.ml[(int64_t)split * a.tokens * a.q_heads + out_row] = make_float2(-INFINITY, 0.0f);
-    }
+    for (int r = threadIdx.x; r < w.rows; r += 64 * kFewWaves)
+      part.ml[split * part.rows + part_row0 + r] = make_float2(-INFINITY, 0.0f);
     return;
   }
 
@@ -385,8 +384,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
       float mx = x[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
-      mx = fmaxf(mx, swap16(mx));
-      mx = fmaxf(mx, swap32(mx));
+      mx = max32(max16(mx));
       const float mn = fmaxf(m[nt], mx);
       const float base = mn == -INFINITY ? 0.0f : mn;
       const float alpha = __builtin_amdgcn_exp2f(m[nt] - base);
@@ -465,9 +463,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
   // 128 u + 4 W g + W r + j of row col.
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float sum = l[nt];
-    sum += swap16(sum);
-    sum += swap32(sum);
+    const float sum = sum32(sum16(l[nt]));
     if (g == 0) join_ml[nt][wave][col] = make_float2(m[nt], sum);
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -518,13 +514,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
           for (int e = 0; e < 4; ++e) y[e] = (_Float16)(pr < fr ? 0.0f : v[e] * inv);
           *reinterpret_cast<half4*>(a.out + out_row * D + d * 64 + d0) = y;
         } else {
-          *reinterpret_cast<float4v*>(part.o + ((int64_t)split * a.tokens * a.q_heads + out_row) * D + d * 64 + d0) = v;
+          *reinterpret_cast<float4v*>(part.o + (split * part.rows + part_row0 + rr) * D + d * 64 + d0) = v;
         }
       }
       if (!alone && d0 == 0) {
         // A range that the row sees part of, all of it at -infinity, is not an empty one.
         const bool sees = max(fr, begin * kStep) <= min(pr, end * kStep - 1);
-        part.ml[(int64_t)split * a.tokens * a.q_heads + out_row] =
+        part.ml[split * part.rows + part_row0 + rr] =
             make_float2(top == -INFINITY && sees ? kLowest : top, total);
       }
     }
@@ -535,7 +531,8 @@ template <int D, int B>
 hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
                       hipStream_t stream) {
   const int group = a.q_heads / c.kv_heads;
-  const int tiles = (int)(((int64_t)a.max_q_len * group + p.rows - 1) / p.rows);
+  const int64_t most = (int64_t)a.max_q_len * group;
+  const int tiles = (int)(((most < p.max_rows ? most : p.max_rows) + p.rows - 1) / p.rows);
   const dim3 grid((unsigned)p.splits, (unsigned)(c.kv_heads * tiles), (unsigned)a.batch);
   if (p.rows == 16)
     hipLaunchKernelGGL((attention_few_kernel<D, B, 1>), grid, dim3(64 * kFewWaves), 0, stream, a, c, p, part);

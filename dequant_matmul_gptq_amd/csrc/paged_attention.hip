@@ -1,6 +1,5 @@
-// Attention of new tokens over a paged cache, one wave per (token, query
-// head): 64 keys a step, one per lane, with the running maximum m and sum l of
-// the softmax; o and l are scaled by exp(m_old - m_new) when m grows.
+// Attention over a paged cache: the launch plan, the join of split calls, and
+// the choice between the two kernels (attention_few.hpp, attention_chunk.hpp).
 #include <stdlib.h>
 #include "attention.hpp"
 
@@ -10,97 +9,39 @@ namespace {
 
 using namespace attn;
 
-// Element d of cache row r of a pool.
-__device__ __forceinline__ float cache_value(const void* pool, const uint16_t* scales, int64_t r, int d, int D,
-                                             int bits, int group) {
-  if (bits == 16) return (float)reinterpret_cast<const _Float16*>(pool)[r * D + d];
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(pool) + r * (D * bits / 32);
-  const int pos = d * bits, k = pos >> 5, sh = pos & 31;
-  uint32_t v = w[k] >> sh;
-  if (sh + bits > 32) v |= w[k + 1] << (32 - sh);
-  const float s = (float)__builtin_bit_cast(_Float16, scales[r * (D / group) + d / group]);
-  return (float)(_Float16)(s * (float)((int)(v & ((1u << bits) - 1u)) - (1 << (bits - 1))));
-}
-
-__global__ __launch_bounds__(256) void attention_row_kernel(AttentionArgs a, qlinear_kv_cache c) {
-  __shared__ float qs[4][256];
-  const int D = c.head_dim, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t row = (int64_t)blockIdx.x * 4 + wv;
-  const bool live = row < (int64_t)a.tokens * a.q_heads;
-  const int tok = live ? (int)(row / a.q_heads) : 0, h = live ? (int)(row % a.q_heads) : 0;
-  const int hk = h / (a.q_heads / c.kv_heads);
-  int b = -1, first = 0, last = 0;
-  if (a.q_start) {
-    for (int i = 0; i < a.batch; ++i)
-      if (tok >= a.q_start[i] && tok < a.q_start[i + 1]) {
-        b = i;
-        first = a.q_start[i];
-        last = a.q_start[i + 1];
-      }
-  } else {
-    const int n = a.tokens / a.batch;
-    b = tok / n;
-    first = b * n;
-    last = first + n;
-  }
-  for (int d = lane; d < D; d += 64)
-    qs[wv][d] = live ? (float)__builtin_bit_cast(_Float16, a.q[tok * a.q_stride + (int64_t)h * D + d]) : 0.0f;
-  __syncthreads();
-  if (!live || b < 0) return;
-  const int64_t cap = (int64_t)a.table_width * c.page_size;
-  const int L = (int)min((int64_t)max(a.kv_len[b], 0), cap);
-  const int p = L - (last - first) + (tok - first);
-  const int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  float m = -INFINITY, l = 0.0f, o[4] = {0, 0, 0, 0};
-  auto slot = [&](int t) {
-    int pg = a.block_table[(int64_t)b * a.table_width + t / c.page_size];
-    pg = min(max(pg, 0), c.num_pages - 1);
-    return ((int64_t)pg * c.kv_heads + hk) * c.page_size + t % c.page_size;
-  };
-  for (int t0 = lo; t0 <= p; t0 += 64) {
-    const int t = t0 + lane;
-    float s = -INFINITY;
-    if (t <= p) {
-      const int64_t r = slot(t);
-      s = 0.0f;
-      for (int d = 0; d < D; ++d) s += qs[wv][d] * cache_value(c.k, c.k_scales, r, d, D, c.bits, c.group);
-      s *= a.scale * kLog2e;
-    }
-    float mx = s;
-    for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k));
-    const float mn = fmaxf(m, mx);
-    const float alpha = exp2f(m - mn), e = t <= p ? exp2f(s - mn) : 0.0f;
-    float es = e;
-    for (int k = 1; k < 64; k <<= 1) es += __shfl_xor(es, k);
-    l = l * alpha + es;
-    m = mn;
-    for (int i = 0; i < 4; ++i) o[i] *= alpha;
-    for (int j = 0; j < 64 && t0 + j <= p; ++j) {
-      const float pj = __shfl(e, j);
-      const int64_t r = slot(t0 + j);
-      for (int i = 0; i < D / 64; ++i)
-        o[i] += pj * cache_value(c.v, c.v_scales, r, lane + 64 * i, D, c.bits, c.group);
-    }
-  }
-  for (int i = 0; i < D / 64; ++i)
-    a.out[((int64_t)tok * a.q_heads + h) * D + lane + 64 * i] =
-        __builtin_bit_cast(uint16_t, (_Float16)(l > 0.0f || l != l ? o[i] / l : 0.0f));
-}
-
-// Joins the partial results of a split call, one workgroup per row: the
+// Joins the partial results of a split launch, one workgroup per row: the
 // ranges' weights 2^(m - max m) first (kJoinBatch at a time in LDS), then the
 // sum over ranges with D / 4 threads to a range and several loads in flight.
 // Threads and ranges are added in a fixed order.
+// FEW: workgroup (row, key/value head, sequence); else (row tile and head,
+// row).
 constexpr int kJoinBatch = 256;
-template <int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Partials part, int splits) {
+template <int D, bool FEW>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
+                                                             Partials part) {
   constexpr int kSide = 256 / (D / 4);    // ranges at a time
   __shared__ float weight[kJoinBatch];
   __shared__ float tops[4], sums[4];
   __shared__ float4v o_part[kSide][D / 4];
-  const int64_t row = blockIdx.x, rows = (int64_t)a.tokens * a.q_heads;
-  const int tok = blockIdx.x / a.q_heads;
-  if (a.q_start && (tok < a.q_start[0] || tok >= a.q_start[a.batch])) return;   // of no sequence
+  const int group = a.q_heads / c.kv_heads;
+  Work w;
+  int r, head;
+  if constexpr (FEW) {
+    r = blockIdx.x;
+    head = blockIdx.y;
+    sequence(a, c, blockIdx.z, w);
+    const int64_t seq_rows = (int64_t)w.n * group;
+    if (r >= seq_rows || seq_rows > plan.max_rows) return;
+  } else {
+    int tile = 0;
+    head = blockIdx.x % c.kv_heads;
+    if (!find_tile(a, c, plan, group, blockIdx.x / c.kv_heads, w, tile)) return;
+    r = tile * kChunkRows + blockIdx.y;
+    if (r >= w.n * group) return;
+  }
+  const int64_t out_row = (int64_t)(w.q0 + r / group) * a.q_heads + head * group + r % group;
+  const int64_t row = FEW ? ((int64_t)w.b * c.kv_heads + head) * part.cap + r : out_row, rows = part.rows;
+  const int splits = plan.splits;
   const int t = threadIdx.x, side = t / (D / 4), d = t % (D / 4);
   float top = -INFINITY;
   for (int s = t; s < splits; s += 256) top = fmaxf(top, part.ml[s * rows + row].x);
@@ -117,13 +58,13 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
     if (s0) __syncthreads();
     if (t < n) {
       const float2 ml = part.ml[(s0 + t) * rows + row];
-      // An empty range (m = -infinity) has weight 0 and its o is not written.
+      // An empty range (m = -infinity) has no o: weight -1 says so.
       const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
       weight[t] = ml.x == -INFINITY ? -1.0f : f;
       total += f * ml.y;
     }
     __syncthreads();
-    const float4v* p = reinterpret_cast<const float4v*>(part.o) + ((int64_t)s0 * rows + row) * (D / 4) + d;
+    const float4v* p = reinterpret_cast<const float4v*>(part.o) + (s0 * rows + row) * (D / 4) + d;
 #pragma unroll 4
     for (int s = side; s < n; s += kSide) {
       const float f = weight[s];
@@ -142,72 +83,143 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   half4 y;
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = (_Float16)(top == -INFINITY ? 0.0f : o[e] / total);
-  *reinterpret_cast<half4*>(a.out + row * D + 4 * d) = y;
+  *reinterpret_cast<half4*>(a.out + out_row * D + 4 * d) = y;
 }
 
-// Tokens a row tile can see at most, in steps.
-int64_t plan_steps(const AttentionArgs& a) {
+// Steps of `tokens` that a row tile can span at most.
+int64_t plan_steps(const AttentionArgs& a, int tokens) {
   int64_t n = a.max_kv_len;
   if (a.window > 0 && (int64_t)a.window + a.max_q_len < n) n = (int64_t)a.window + a.max_q_len;
-  return n / kStep + 2;
+  return n / tokens + 2;
 }
 
-constexpr int kFewRows = 64;       // most rows of a sequence per key/value head in the few-row kernel
+// The sequences of a call are served by their number of rows per key/value
+// head: up to kFewRows by the few-row kernel, more by the chunk kernel. A call
+// launches the kernels that it may need.
+struct Route {
+  bool few, chunk;
+  Plan few_plan, chunk_plan;
+  int few_cap;                      // rows per sequence and key/value head
+  int64_t few_rows, chunk_rows;     // rows of the partial results, 0 if not split
+};
 
-Plan make_plan(const qlinear_kv_cache& c, const AttentionArgs& a) {
-  const int64_t group = a.q_heads / c.kv_heads, rows = a.max_q_len * group;
-  Plan p;
-  p.rows = rows <= 16 || c.head_dim == 256 ? 16 : 32;   // two tiles of 256 wide heads do not fit the registers
-  p.splits = 1;
-  p.chunk = INT32_MAX;
-  if (rows > kFewRows) return p;
-  const int64_t tiles = (rows + p.rows - 1) / p.rows * c.kv_heads * a.batch;
-  const int64_t steps = plan_steps(a);
-  // A range is long enough that writing and reading its partial result is
-  // about 1/25 of reading its keys and values, unless that leaves fewer than
-  // two workgroups per CU; short enough for about 4096 workgroups.
-  const int64_t row_bytes = c.bits == 16 ? 2 * c.head_dim : c.head_dim * c.bits / 8 + 2 * c.head_dim / c.group;
-  const int64_t used = rows < p.rows ? rows : p.rows;
-  const int64_t light = 25 * used * c.head_dim * 4 / (row_bytes * kStep);
-  const int64_t even = (tiles * steps + 4095) / 4096;
-  const int64_t fill = (tiles * steps + 511) / 512;
-  int64_t chunk = even > light ? even : light;
-  if (chunk > fill) chunk = fill;
-  if (chunk < 4) chunk = 4;
-  if (getenv("QL_CHUNK")) chunk = atoi(getenv("QL_CHUNK"));
-  p.splits = (int)((steps + chunk - 1) / chunk);
-  if (p.splits > 1) p.chunk = (int)chunk;
-  return p;
+Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
+  const int64_t group = a.q_heads / c.kv_heads, most = a.max_q_len * group;
+  Route r = {};
+  r.chunk = most > kFewRows;
+  r.few = !r.chunk || a.batch > 1;
+  if (r.few) {
+    Plan& p = r.few_plan;
+    r.few_cap = (int)(most < kFewRows ? most : kFewRows);
+    // Two tiles of 256 wide heads do not fit the registers.
+    p.rows = r.few_cap <= 16 || c.head_dim == 256 ? 16 : 32;
+    p.min_rows = 1;
+    p.max_rows = kFewRows;
+    p.splits = 1;
+    p.chunk = INT32_MAX;
+    const int64_t tiles = (int64_t)(r.few_cap + p.rows - 1) / p.rows * c.kv_heads * a.batch;
+    const int64_t steps = plan_steps(a, kStep);
+    // A range is long enough that writing and reading its partial result is
+    // about 1/25 of reading its keys and values, unless that leaves fewer than
+    // two workgroups per CU; short enough for about 4096 workgroups.
+    const int64_t row_bytes = c.bits == 16 ? 2 * c.head_dim : c.head_dim * c.bits / 8 + 2 * c.head_dim / c.group;
+    const int64_t used = r.few_cap < p.rows ? r.few_cap : p.rows;
+    const int64_t light = 25 * used * c.head_dim * 4 / (row_bytes * kStep);
+    const int64_t even = (tiles * steps + 4095) / 4096;
+    const int64_t fill = (tiles * steps + 511) / 512;
+    int64_t chunk = even > light ? even : light;
+    if (chunk > fill) chunk = fill;
+    if (chunk < 4) chunk = 4;
+    if (getenv("QL_CHUNK")) chunk = atoi(getenv("QL_CHUNK"));
+    p.splits = (int)((steps + chunk - 1) / chunk);
+    if (p.splits > 1) {
+      p.chunk = (int)chunk;
+      r.few_rows = (int64_t)a.batch * c.kv_heads * r.few_cap;
+    }
+  }
+  if (r.chunk) {
+    Plan& p = r.chunk_plan;
+    p.rows = kChunkRows;
+    p.min_rows = r.few ? kFewRows + 1 : 1;
+    p.max_rows = INT32_MAX;
+    p.splits = 1;
+    p.chunk = INT32_MAX;
+    // Two workgroups per CU, each with at least eight steps.
+    const int64_t groups = chunk_tiles(a, (int)group) * c.kv_heads;
+    const int64_t steps = plan_steps(a, chunk_step(c.head_dim));
+    int64_t splits = 512 / groups;
+    if (splits > steps / 8) splits = steps / 8;
+    if (getenv("QL_SPLITS")) splits = atoi(getenv("QL_SPLITS"));
+    if (splits > 1) {
+      p.chunk = (int)((steps + splits - 1) / splits);
+      p.splits = (int)((steps + p.chunk - 1) / p.chunk);
+      r.chunk_rows = (int64_t)a.tokens * a.q_heads;
+    }
+  }
+  return r;
+}
+
+size_t partial_bytes(const Plan& p, int64_t rows, int D) { return (size_t)p.splits * rows * (D + 2) * sizeof(float); }
+
+Partials partials(void* ws, const Plan& p, int64_t rows, int cap, int D) {
+  Partials part = {};
+  if (rows == 0) return part;
+  part.o = (float*)ws;
+  part.ml = (float2*)(part.o + (int64_t)p.splits * rows * D);
+  part.rows = rows;
+  part.cap = cap;
+  return part;
 }
 
 }  // namespace
 
+// The two kernels' launches follow one another on the stream and share the workspace.
 size_t paged_attention_workspace_bytes(const qlinear_kv_cache& cache, const AttentionArgs& a) {
-  const Plan p = make_plan(cache, a);
-  if (p.splits == 1) return 0;
-  return (size_t)p.splits * a.tokens * a.q_heads * (cache.head_dim + 2) * sizeof(float);
+  const Route r = make_route(cache, a);
+  const size_t few = partial_bytes(r.few_plan, r.few_rows, cache.head_dim);
+  const size_t chunk = partial_bytes(r.chunk_plan, r.chunk_rows, cache.head_dim);
+  return few > chunk ? few : chunk;
 }
 
 hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const AttentionArgs& a, void* ws,
                                   hipStream_t stream) {
-  const Plan p = make_plan(cache, a);
-  const int64_t rows = (int64_t)a.tokens * a.q_heads;
-  if ((int64_t)a.max_q_len * (a.q_heads / cache.kv_heads) > kFewRows) {
-    hipLaunchKernelGGL(attention_row_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, cache);
-    return hipGetLastError();
+  const Route r = make_route(cache, a);
+  const int D = cache.head_dim, group = a.q_heads / cache.kv_heads;
+  if (r.chunk) {
+    const Plan& p = r.chunk_plan;
+    const Partials part = partials(ws, p, r.chunk_rows, 0, D);
+    const hipError_t e = D == 64    ? launch_attention_chunk_64(cache, a, p, part, stream)
+                         : D == 128 ? launch_attention_chunk_128(cache, a, p, part, stream)
+                                    : launch_attention_chunk_256(cache, a, p, part, stream);
+    if (e != hipSuccess) return e;
+    if (r.chunk_rows > 0) {
+      auto join = D == 64    ? attention_join_kernel<64, false>
+                  : D == 128 ? attention_join_kernel<128, false>
+                             : attention_join_kernel<256, false>;
+      hipLaunchKernelGGL(join, dim3((unsigned)(chunk_tiles(a, group) * cache.kv_heads), kChunkRows), dim3(256), 0,
+                         stream, a, cache, p, part);
+      const hipError_t j = hipGetLastError();
+      if (j != hipSuccess) return j;
+    }
   }
-  Partials part = {};
-  part.o = (float*)ws;
-  if (p.splits > 1) part.ml = (float2*)(part.o + (int64_t)p.splits * rows * cache.head_dim);
-  hipError_t e = cache.head_dim == 64    ? launch_attention_few_64(cache, a, p, part, stream)
-                 : cache.head_dim == 128 ? launch_attention_few_128(cache, a, p, part, stream)
-                                         : launch_attention_few_256(cache, a, p, part, stream);
-  if (e != hipSuccess || p.splits == 1) return e;
-  auto join = cache.head_dim == 64    ? attention_join_kernel<64>
-              : cache.head_dim == 128 ? attention_join_kernel<128>
-                                      : attention_join_kernel<256>;
-  hipLaunchKernelGGL(join, dim3((unsigned)rows), dim3(256), 0, stream, a, part, p.splits);
-  return hipGetLastError();
+  // Without q_start all sequences have the same length.
+  if (r.few && (!r.chunk || a.q_start || (int64_t)(a.tokens / a.batch) * group <= kFewRows)) {
+    const Plan& p = r.few_plan;
+    const Partials part = partials(ws, p, r.few_rows, r.few_cap, D);
+    const hipError_t e = D == 64    ? launch_attention_few_64(cache, a, p, part, stream)
+                         : D == 128 ? launch_attention_few_128(cache, a, p, part, stream)
+                                    : launch_attention_few_256(cache, a, p, part, stream);
+    if (e != hipSuccess) return e;
+    if (r.few_rows > 0) {
+      auto join = D == 64    ? attention_join_kernel<64, true>
+                  : D == 128 ? attention_join_kernel<128, true>
+                             : attention_join_kernel<256, true>;
+      hipLaunchKernelGGL(join, dim3((unsigned)r.few_cap, (unsigned)cache.kv_heads, (unsigned)a.batch), dim3(256), 0,
+                         stream, a, cache, p, part);
+      return hipGetLastError();
+    }
+  }
+  return hipSuccess;
 }
 
 }  // namespace qlinear

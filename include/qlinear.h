@@ -495,8 +495,9 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
  *   block_table : int32 [batch][table_width], see qlinear_kv_cache; entries
  *               past a sequence's pages are not read. A length is taken to be
  *               at most table_width * page_size.
- *   max_q_len, max_kv_len : upper bounds of n and L that the launch is
- *               planned for (tokens, table_width * page_size at most are used)
+ *   max_q_len : upper bound of n; a sequence with more may be left out
+ *   max_kv_len : upper bound of L, for the launch plan only (too small a one
+ *               costs speed)
  *   window    : 0 = none
  *   out       : float16 [tokens][q_heads][head_dim], contiguous; not q
  *   workspace : qlinear_paged_attention_workspace_bytes of the same sizes;
@@ -508,8 +509,8 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
  * Errors: INVALID_ARGUMENT (NULL, a negative size, q_heads or table_width
  * < 1, q_stride < q_heads * head_dim, tokens % batch without q_start, a scale
  * that is not finite), UNSUPPORTED (q_heads not a multiple of kv_heads,
- * q_heads > 65535, batch > 65535, q_stride % 8 != 0, more than 2^31 - 1 rows
- * tokens * q_heads), MISALIGNED (q, out, workspace 16 bytes; the int32 arrays
+ * q_heads > 65535, batch > 65535, q_stride % 8 != 0, tokens * q_heads > 2^29,
+ * batch * kv_heads > 2^22), MISALIGNED (q, out, workspace 16 bytes; the int32 arrays
  * 4), WORKSPACE.
  */
 int qlinear_paged_attention_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,

@@ -162,8 +162,9 @@ def test_long_split():
     b.check(b.run())
     b.check(b.run(max_kv_len=9000))
     b.check(b.run(window=5000), window=5000)
-    # bounds that are too small cost speed, not tokens
-    b.check(b.run(max_kv_len=100, max_q_len=1))
+    # a length bound that is too small costs speed, not tokens; so do large ones
+    b.check(b.run(max_kv_len=100, max_q_len=4))
+    b.check(b.run(max_kv_len=1 << 20, max_q_len=1000))
     b = Batch(2, 2, 64, 64, 4, 32, [40], [5000], seed=4)
     b.check(b.run())
 
@@ -173,6 +174,7 @@ def test_uniform_rows_without_q_start():
     for n in (1, 3, 40):
         b = Batch(4, 2, 64, 32, 16, 64, [n] * 3, [n, n + 50, n + 7], seed=n)
         b.check(b.run(uniform=True))
+        b.check(b.run(uniform=True, max_q_len=1000))
 
 
 def test_rows_that_see_nothing_are_zero():
