@@ -99,12 +99,22 @@ __device__ __forceinline__ void row_tile(const AttentionArgs& a, int group, int 
   w.lo_max = first_seen(w.p_max, a.window);
 }
 
-// First pool row of token slot t's 16-token tile (t a multiple of 16): page
-// numbers are taken into the pool and table places to the sequence's last.
-__device__ __forceinline__ int64_t tile_row(const AttentionArgs& a, const qlinear_kv_cache& c, const int32_t* table,
-                                            int page_shift, int last_page, int head, int t) {
-  const int pg = min(max(table[min(t >> page_shift, last_page)], 0), c.num_pages - 1);
-  return (((int64_t)pg * c.kv_heads + head) << page_shift) + (t & (c.page_size - 1));
+// A sequence's page numbers, through the scalar cache where the place is
+// uniform (the table is not written during a launch).
+typedef const __attribute__((address_space(4))) int32_t* PageTable;
+__device__ __forceinline__ PageTable page_table(const AttentionArgs& a, int b) {
+  return (PageTable)(uintptr_t)(a.block_table + (int64_t)b * a.table_width);
+}
+
+// The page of token t: numbers are taken into the pool, table places to the
+// sequence's last.
+__device__ __forceinline__ int page_of(const qlinear_kv_cache& c, PageTable table, int page_shift, int last_page,
+                                       int t) {
+  return min(max(table[min(t >> page_shift, last_page)], 0), c.num_pages - 1);
+}
+// The pool row of token t in that page.
+__device__ __forceinline__ int64_t pool_row(const qlinear_kv_cache& c, int page, int page_shift, int head, int t) {
+  return (((int64_t)page * c.kv_heads + head) << page_shift) + (t & (c.page_size - 1));
 }
 
 // The sequence and row tile of tile number y, counting the tiles of the

@@ -136,27 +136,37 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   }
   const float sc = fabsf(a.scale) * kLog2e;
 
-  const int32_t* table = a.block_table + (int64_t)w.b * a.table_width;
+  const PageTable table = page_table(a, w.b);
   const int last_page = max(w.len - 1, 0) >> page_shift;
 
   // ---- staging
+  typedef __attribute__((address_space(3))) uint16_t* Lds;
+  typedef __attribute__((address_space(3))) u32x4* Lds4;
   // float16: a wave brings in every fourth 1024-byte group of rows, each lane
-  // the 16 bytes whose place in LDS is its own.
-  auto stage_direct = [&](int step, int buf) {
-    constexpr int kGroupRows = 1024 / (2 * D);
+  // the 16 bytes whose place in LDS is its own. The groups' pages are looked
+  // up a step ahead.
+  constexpr int kGroupRows = 1024 / (2 * D), kGroups = T / kGroupRows / 4;
+  int pages[kGroups];
+  auto look_up = [&](int step) {
+    if constexpr (B == 16)
 #pragma unroll
-    for (int i = 0; i < T / kGroupRows / 4; ++i) {
+      for (int i = 0; i < kGroups; ++i)
+        pages[i] = page_of(c, table, page_shift, last_page, step * T + (4 * i + wave) * kGroupRows);
+  };
+  auto stage_direct = [&](int step, Lds kn, Lds vn) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
       const int r0 = (4 * i + wave) * kGroupRows;
-      const int64_t pool = tile_row(a, c, table, page_shift, last_page, head, step * T + r0) * D;
+      const int64_t pool = pool_row(c, pages[i], page_shift, head, step * T + r0) * D;
       // lane's row and piece in LDS order
       const int r = r0 + lane / Sh::kPieces, x = lane % Sh::kPieces;
       typedef const __attribute__((address_space(1))) void* gptr;
       typedef __attribute__((address_space(3))) void* lptr;
       const int in = (lane / Sh::kPieces) * D;
       __builtin_amdgcn_global_load_lds((gptr)((const uint16_t*)c.k + pool + in + key_piece<D>(r, x) * 8),
-                                       (lptr)(&ks[buf][r0 * D]), 16, 0, 0);
+                                       (lptr)(kn + r0 * D), 16, 0, 0);
       __builtin_amdgcn_global_load_lds((gptr)((const uint16_t*)c.v + pool + in + value_piece<D>(r, x) * 8),
-                                       (lptr)(&vs[buf][r0 * D]), 16, 0, 0);
+                                       (lptr)(vn + r0 * D), 16, 0, 0);
     }
   };
   // Quantized: a thread takes kRun neighbouring elements of one token.
@@ -166,8 +176,8 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const int my_row = threadIdx.x / kPerRow, my_run = threadIdx.x % kPerRow;
   auto fetch = [&](int step) {
     if constexpr (B != 16) {
-      const int64_t pool = tile_row(a, c, table, page_shift, last_page, head, step * T + (my_row & ~15)) + (my_row & 15);
-      typedef u32x4 __attribute__((aligned(4))) u32x4_a4;
+      const int t = step * T + my_row;
+      const int64_t pool = pool_row(c, page_of(c, table, page_shift, last_page, t), page_shift, head, t);
       const uint32_t* kp = (const uint32_t*)c.k + pool * (D * B / 32) + my_run * Sh::kRunWords;
       const uint32_t* vp = (const uint32_t*)c.v + pool * (D * B / 32) + my_run * Sh::kRunWords;
 #pragma unroll
@@ -180,7 +190,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       vscale = c.v_scales[at];
     }
   };
-  auto unpack = [&](int buf) {
+  auto unpack = [&](Lds kn, Lds vn) {
     if constexpr (B != 16) {
       const _Float16 sk = __builtin_bit_cast(_Float16, kscale), sv = __builtin_bit_cast(_Float16, vscale);
 #pragma unroll
@@ -202,19 +212,17 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
           vb = i % 2 ? vw[o + 2] >> 16 : vw[o + 1];
         }
         const int x = my_run * (Sh::kRun / 8) + i;
-        *reinterpret_cast<u32x4*>(&ks[buf][my_row * D + key_piece<D>(my_row, x) * 8]) =
-            decode8<B>(ka, kb, half2v{sk, sk});
-        *reinterpret_cast<u32x4*>(&vs[buf][my_row * D + value_piece<D>(my_row, x) * 8]) =
-            decode8<B>(va, vb, half2v{sv, sv});
+        *(Lds4)(kn + my_row * D + key_piece<D>(my_row, x) * 8) = decode8<B>(ka, kb, half2v{sk, sk});
+        *(Lds4)(vn + my_row * D + value_piece<D>(my_row, x) * 8) = decode8<B>(va, vb, half2v{sv, sv});
       }
     }
   };
 
   // V^T fragment of 16-token chunk cc, 32-element tile dt: lane (d = l % 32)
   // gets tokens 16 cc + 4 h + 0 .. 3 and + 8 of element 32 dt + d.
-  auto value_fragment = [&](int buf, int cc, int dt) {
+  auto value_fragment = [&](Lds vc, int cc, int dt) {
     typedef short short4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) short4* lptr;
+    typedef __attribute__((address_space(3))) short4* Lds2;
     const int j = lane & 15, sub = (lane >> 4) & 1;
     const int x = 4 * dt + 2 * sub + (j & 3) / 2;     // 16-byte piece
     u32x4 r;
@@ -222,7 +230,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     for (int i = 0; i < 2; ++i) {
       const int t = 16 * cc + 8 * i + 4 * h + j / 4;
       const short4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lptr)(&vs[buf][t * D + value_piece<D>(t, x) * 8 + (j & 1) * 4]));
+          (Lds2)(vc + t * D + value_piece<D>(t, x) * 8 + (j & 1) * 4));
       const u32x2 u = __builtin_bit_cast(u32x2, v);
       r[2 * i] = u[0];
       r[2 * i + 1] = u[1];
@@ -237,22 +245,18 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
   float m = -INFINITY, l = 0.0f;
 
-  if (begin < end) {
-    if constexpr (B == 16) {
-      stage_direct(begin, begin & 1);
-    } else {
-      fetch(begin);
-      unpack(begin & 1);
-    }
-  }
-  for (int step = begin; step < end; ++step) {
-    const int buf = step & 1, t0 = step * T;
-    __syncthreads();     // this step's rows are in LDS; the other buffer is free
+  // One step: rows in kc, vc; the next step's go to kn, vn. That the two pairs
+  // are apart (restrict) lets the reads of one pass the writes of the other.
+  auto one_step = [&](int step, Lds __restrict__ kc, Lds __restrict__ vc, Lds __restrict__ kn,
+                      Lds __restrict__ vn) __attribute__((always_inline)) {
+    const int t0 = step * T;
     if (step + 1 < end) {
-      if constexpr (B == 16)
-        stage_direct(step + 1, buf ^ 1);
-      else
+      if constexpr (B == 16) {
+        stage_direct(step + 1, kn, vn);
+        look_up(step + 2);
+      } else {
         fetch(step + 1);
+      }
     }
 
     // A step that some row of the workgroup sees only a part of.
@@ -263,7 +267,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       uint32_t bad = 0;
       for (int i = threadIdx.x; i < T * D / 8; i += kChunkThreads) {
         const int t = t0 + i / Sh::kPieces;
-        u32x4* at = reinterpret_cast<u32x4*>(&vs[buf][i * 8]);
+        const Lds4 at = (Lds4)(vc + i * 8);
         if (t > w.p_max || t < w.lo_min) {
           *at = u32x4{0, 0, 0, 0};
         } else {
@@ -288,7 +292,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
 #pragma unroll
         for (int k = 0; k < kKeyTiles; ++k) {
           const int key = 32 * k + n32;
-          const half8 kf = *reinterpret_cast<const half8*>(&ks[buf][key * D + key_piece<D>(key, 2 * f + h) * 8]);
+          const half8 kf = __builtin_bit_cast(half8, *(Lds4)(kc + key * D + key_piece<D>(key, 2 * f + h) * 8));
           s[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[f], s[k], 0, 0, 0);
         }
 
@@ -348,7 +352,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
           }
 #pragma unroll
           for (int d = 0; d < kOutTiles; ++d) {
-            const u32x4 v = value_fragment(buf, cc, d);
+            const u32x4 v = value_fragment(vc, cc, d);
             u32x4 up, down;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -373,7 +377,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       }
       __syncthreads();
       for (int i = threadIdx.x; i < T * D / 8; i += kChunkThreads) {
-        u32x4* at = reinterpret_cast<u32x4*>(&vs[buf][i * 8]);
+        const Lds4 at = (Lds4)(vc + i * 8);
         u32x4 v = *at;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] &= ~spread_top(nonfinite_halves(v[e]));
@@ -387,12 +391,27 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       for (int cc = 0; cc < T / 16; ++cc)
 #pragma unroll
         for (int d = 0; d < kOutTiles; ++d)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, value_fragment(buf, cc, d)), p[cc],
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, value_fragment(vc, cc, d)), p[cc],
                                                         o[d], 0, 0, 0);
     }
     if constexpr (B != 16) {
-      if (step + 1 < end) unpack(buf ^ 1);
+      if (step + 1 < end) unpack(kn, vn);
     }
+  };
+
+  if (begin < end) {
+    look_up(begin);
+    if constexpr (B == 16) {
+      stage_direct(begin, (Lds)ks[0], (Lds)vs[0]);
+      look_up(begin + 1);
+    } else {
+      fetch(begin);
+      unpack((Lds)ks[0], (Lds)vs[0]);
+    }
+  }
+  for (int step = begin, buf = 0; step < end; ++step, buf ^= 1) {
+    __syncthreads();     // this step's rows are in LDS; the other buffers are free
+    one_step(step, (Lds)ks[buf], (Lds)vs[buf], (Lds)ks[buf ^ 1], (Lds)vs[buf ^ 1]);
   }
 
   // Register r of tile d is element 32 d + 8 (r / 4) + 4 h + r % 4 as stored.

@@ -313,7 +313,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
     }
   }
 
-  const int32_t* table = a.block_table + (int64_t)w.b * a.table_width;
+  const PageTable table = page_table(a, w.b);
   const int last_page = max(w.len - 1, 0) >> page_shift;
   float4v o[NT][kTiles];
   float m[NT], l[NT];
@@ -329,17 +329,20 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
   bool nonfinite = false;      // join holds what infinities and NaN add
   KeyRaw<D, B> kr;
   VR vr;
+  auto row_of = [&](int t) {
+    return pool_row(c, page_of(c, table, page_shift, last_page, t), page_shift, head, t);
+  };
   auto keys = [&](int step) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       load_keys<D, B>(kr, i, c, group_shift,
-                      tile_row(a, c, table, page_shift, last_page, head, step * kStep + 16 * i), col, g);
+                      row_of(step * kStep + 16 * i), col, g);
   };
   auto values = [&](int step) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       load_values<D, B>(vr, i, c, group_shift,
-                        tile_row(a, c, table, page_shift, last_page, head, step * kStep + 16 * i), col, g);
+                        row_of(step * kStep + 16 * i), col, g);
   };
 
   int step = begin + wave;
