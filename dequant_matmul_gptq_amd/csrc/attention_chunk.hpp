@@ -123,18 +123,19 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   half8 q[kFrags];
   {
     const uint16_t* p = a.q + (w.q0 + tok) * a.q_stride + (int64_t)qh * D + 8 * h;
-    const uint32_t flip = a.scale < 0.0f ? kTops : 0u;   // the kernel's scale is the magnitude
+    // The kernel's scale is positive: a negative one turns q, 0 makes it 0.
+    const uint32_t flip = a.scale < 0.0f ? kTops : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
       u32x4 v = *reinterpret_cast<const u32x4*>(p + 16 * f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] ^= flip;
+      for (int e = 0; e < 4; ++e) v[e] = (v[e] ^ flip) & keep;
       const half8 x = __builtin_bit_cast(half8, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) q[f][e] = x[unpacked<B>(e)];
     }
   }
-  const float sc = fabsf(a.scale) * kLog2e;
+  const float sc = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
 
   const PageTable table = page_table(a, w.b);
   const int last_page = max(w.len - 1, 0) >> page_shift;
@@ -313,24 +314,22 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[k][r]);
       mx = max32(mx);
       const float mn = fmaxf(m, mx);
-      if (__any(mn != m)) {      // the maxima settle after a few steps
-        // base of the exponents: m scaled, or 0 before any token is seen
-        const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m * sc - mn * sc);
-        m = mn;
-        l *= alpha;
+      // Always rescaled: around a branch that skips it when no maximum grew,
+      // the compiler copies all of o twice, which costs more.
+      const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m * sc - mn * sc);
+      m = mn;
+      l *= alpha;
 #pragma unroll
-        for (int d = 0; d < kOutTiles; ++d)
+      for (int d = 0; d < kOutTiles; ++d)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
-      }
+        for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
       const float base = m == -INFINITY ? 0.0f : m * sc;
       float sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < kKeyTiles; ++k)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          float e = __builtin_amdgcn_exp2f(s[k][r] * sc - base);
-          if (edge && s[k][r] == -INFINITY) e = 0.0f;     // also where the scale is 0
+          const float e = __builtin_amdgcn_exp2f(s[k][r] * sc - base);
           sum += e;
           p[2 * k + r / 8][r % 8] = (_Float16)e;
         }

@@ -400,12 +400,10 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
         p[nt][i] = (_Float16)e;
       }
       l[nt] = l[nt] * alpha + sum;
-      if (__any(alpha != 1.0f)) {       // the maxima settle after a few steps
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
+      for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[nt][j][r] *= alpha;
-      }
+        for (int r = 0; r < 4; ++r) o[nt][j][r] *= alpha;
     }
 
 #pragma unroll
