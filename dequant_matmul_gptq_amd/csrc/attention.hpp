@@ -62,6 +62,13 @@ struct Partials {
   int cap;
 };
 
+// The kernels' loops come in three kinds of step: whole ones that all rows see
+// all of, edge ones with masks, and, where an edge step holds infinities or
+// NaN (rare), the whole range again with careful steps. Kept apart so that the
+// common loops hold no registers for the rare ones.
+// kEither decides between the first two step by step.
+enum StepKind { kWhole, kEdgeStep, kEither, kCareful };
+
 // One workgroup's sequence, row tile and token range.
 struct Work {
   int b;             // sequence

@@ -18,6 +18,8 @@
 // so that the lanes of one LDS cycle hit different banks.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.hpp"
 
 namespace qlinear {
@@ -115,10 +117,8 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const int tok = rr / group, qh = head * group + rr - tok * group;
   const int pos = w.len - w.n + tok, first = first_seen(pos, a.window);
   const int64_t out_row = (int64_t)(w.q0 + tok) * a.q_heads + qh;
-  const bool wave_live = 32 * wave < w.rows;
   const int wr0 = w.row0 + 32 * wave, wr1 = w.row0 + min(32 * wave + 31, w.rows - 1);
-  const int wp_min = w.len - w.n + wr0 / group, wp_max = w.len - w.n + wr1 / group;
-  const int wlo_min = first_seen(wp_min, a.window), wlo_max = first_seen(wp_max, a.window);
+  const int wp_max = w.len - w.n + wr1 / group, wlo_min = first_seen(w.len - w.n + wr0 / group, a.window);
 
   half8 q[kFrags];
   {
@@ -240,17 +240,18 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   };
 
   float16v o[kOutTiles];
-#pragma unroll
-  for (int d = 0; d < kOutTiles; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
+  float m, l;
 
   // One step: rows in kc, vc; the next step's go to kn, vn. That the two pairs
   // are apart (restrict) lets the reads of one pass the writes of the other.
-  auto one_step = [&](int step, Lds __restrict__ kc, Lds __restrict__ vc, Lds __restrict__ kn,
-                      Lds __restrict__ vn) __attribute__((always_inline)) {
+  // kind: see StepKind. False: an edge step has infinities or NaN that only
+  // some rows see.
+  auto one_step = [&](auto kind, int step, Lds __restrict__ kc, Lds __restrict__ vc, Lds __restrict__ kn,
+                      Lds __restrict__ vn) __attribute__((always_inline)) -> bool {
+    constexpr bool kSplit = decltype(kind)::value == kCareful;
     const int t0 = step * T;
+    const bool edge = decltype(kind)::value == kEither ? t0 + T - 1 > w.p_min || t0 < w.lo_max
+                                                       : decltype(kind)::value != kWhole;
     if (step + 1 < end) {
       if constexpr (B == 16) {
         stage_direct(step + 1, kn, vn);
@@ -260,9 +261,8 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       }
     }
 
-    // A step that some row of the workgroup sees only a part of.
     bool nonfinite = false;
-    if (t0 + T - 1 > w.p_min || t0 < w.lo_max) {
+    if (edge) {
       // Values of tokens that no row sees may be anything: zero. A weight of
       // 0 does not hide an infinity or NaN of a token that only some rows see.
       uint32_t bad = 0;
@@ -278,9 +278,10 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
         }
       }
       nonfinite = __syncthreads_or(bad != 0) && w.p_min != w.p_max;
+      if (!kSplit && nonfinite) return false;
     }
 
-    const bool active = wave_live && t0 <= wp_max && t0 + T - 1 >= wlo_min;
+    const bool active = !edge || (t0 <= wp_max && t0 + T - 1 >= wlo_min);
     half8 p[T / 16];
     if (active) {
       float16v s[kKeyTiles];
@@ -297,7 +298,6 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
           s[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[f], s[k], 0, 0, 0);
         }
 
-      const bool edge = t0 + T - 1 > wp_min || t0 < wlo_max;
       if (edge) {
 #pragma unroll
         for (int k = 0; k < kKeyTiles; ++k)
@@ -336,7 +336,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       l += sum;
     }
 
-    if (nonfinite) {
+    if (kSplit && nonfinite) {
       // What infinities and NaN add to the rows that see them: counts of
       // tokens with +infinity or NaN, and with -infinity or NaN, from the
       // same product with weights of 1. Then they are taken out of LDS.
@@ -396,9 +396,17 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     if constexpr (B != 16) {
       if (step + 1 < end) unpack(kn, vn);
     }
+    return true;
   };
 
-  if (begin < end) {
+  auto start = [&]() {
+#pragma unroll
+    for (int d = 0; d < kOutTiles; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+    m = -INFINITY;
+    l = 0.0f;
+    if (begin >= end) return;
     look_up(begin);
     if constexpr (B == 16) {
       stage_direct(begin, (Lds)ks[0], (Lds)vs[0]);
@@ -407,10 +415,37 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       fetch(begin);
       unpack((Lds)ks[0], (Lds)vs[0]);
     }
+  };
+  int step = begin, buf = 0;
+  // Steps of one kind up to `to`; each turns the buffers.
+  auto steps_to = [&](auto kind, int to) __attribute__((always_inline)) -> bool {
+    for (; step < to; ++step, buf ^= 1) {
+      __syncthreads();     // this step's rows are in LDS; the other buffers are free
+      if (!one_step(kind, step, (Lds)ks[buf], (Lds)vs[buf], (Lds)ks[buf ^ 1], (Lds)vs[buf ^ 1])) return false;
+    }
+    return true;
+  };
+  start();
+  bool done = true;
+  if constexpr (D < 256) {
+    // Steps at the window's start, whole steps, steps at the diagonal: two
+    // rounds of whole and then edge steps, so that each kind's code is there once.
+    const int whole_lo = (w.lo_max + T - 1) / T, whole_hi = max((w.p_min + 1) / T, whole_lo);
+    for (int round = 0; round < 2 && done; ++round) {
+      steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end));
+      done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
+    }
+  } else {
+    // Its accumulators take half the registers, and going from loop to loop
+    // costs more than the branch does (4096 tokens, 16/4 heads: 543 to 331 us).
+    done = steps_to(std::integral_constant<int, kEither>{}, end);
   }
-  for (int step = begin, buf = 0; step < end; ++step, buf ^= 1) {
-    __syncthreads();     // this step's rows are in LDS; the other buffers are free
-    one_step(step, (Lds)ks[buf], (Lds)vs[buf], (Lds)ks[buf ^ 1], (Lds)vs[buf ^ 1]);
+  if (!done) {
+    __syncthreads();       // the staging under way has ended
+    step = begin;
+    buf = 0;
+    start();
+    steps_to(std::integral_constant<int, kCareful>{}, end);
   }
 
   // Register r of tile d is element 32 d + 8 (r / 4) + 4 h + r % 4 as stored.

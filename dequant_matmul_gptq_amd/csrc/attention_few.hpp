@@ -22,6 +22,8 @@
 // value loads after the previous step's second product.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.hpp"
 
 namespace qlinear {
@@ -248,7 +250,7 @@ __device__ __forceinline__ void add_nonfinite(const u32x4& v, const u32x4& sees,
 }
 
 template <int D, int B, int NT>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
+__global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
                                                                        Partials part) {
   typedef ValueRaw<D, B> VR;
   constexpr int W = VR::W, U = VR::U, kTiles = D / 16, kFrags = D / 32;
@@ -317,16 +319,9 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
   const int last_page = max(w.len - 1, 0) >> page_shift;
   float4v o[NT][kTiles];
   float m[NT], l[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = -INFINITY;
-    l[nt] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) o[nt][j] = float4v{0, 0, 0, 0};
-  }
   const float sc = a.scale * kLog2e;
 
-  bool nonfinite = false;      // join holds what infinities and NaN add
+  bool nonfinite = false;      // this wave's rows of join hold what infinities and NaN add
   KeyRaw<D, B> kr;
   VR vr;
   auto row_of = [&](int t) {
@@ -345,12 +340,10 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
                         row_of(step * kStep + 16 * i), col, g);
   };
 
-  int step = begin + wave;
-  if (step < end) {
-    keys(step);
-    values(step);
-  }
-  for (; step < end; step += kFewWaves) {
+  // One step; kind: see StepKind. False: an edge step has infinities or NaN
+  // that only some rows see.
+  auto one_step = [&](auto kind, int step) __attribute__((always_inline)) -> bool {
+    constexpr bool kEdge = decltype(kind)::value != kWhole, kSplit = decltype(kind)::value == kCareful;
     const int t0 = step * kStep;
     const bool more = step + kFewWaves < end;
     // S^T: tile i, row 4 g + r of it in register r.
@@ -369,15 +362,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
     }
     if (more) keys(step + kFewWaves);
 
-    // A step that some row sees only a part of: hide the rest from it.
-    const bool edge = t0 + kStep - 1 > w.p_min || t0 < w.lo_max;
     half8 p[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = s[nt][i / 4][i % 4] * sc;
-      if (edge) {
+      if constexpr (kEdge) {      // hide what the row does not see
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int t = t0 + 16 * (i / 4) + 4 * g + i % 4;
@@ -410,7 +401,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
     for (int u = 0; u < U; ++u) {
       u32x4 vf[W];
       value_fragments<D, B>(vr, u, col, vf);
-      if (edge) {
+      if constexpr (kEdge) {
         // Tokens that no row sees may hold anything: zero.
         uint32_t bad = 0;
 #pragma unroll
@@ -426,7 +417,9 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
         // A weight of 0 does not hide an infinity or NaN from the rows that
         // do not see it (0 times infinity). Such values are taken out here, and
         // what they add is kept apart, in this wave's rows of `join`.
-        if (w.p_min != w.p_max && __any(bad != 0)) {
+        const bool apart = w.p_min != w.p_max && __any(bad != 0);
+        if (!kSplit && apart) return false;
+        if (kSplit && apart) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (!nonfinite)
@@ -458,6 +451,41 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
                                                                     o[nt][u * W + j], 0, 0, 0);
     }
     if (more) values(step + kFewWaves);
+    return true;
+  };
+
+  int step;
+  auto start = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = -INFINITY;
+      l[nt] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) o[nt][j] = float4v{0, 0, 0, 0};
+    }
+    step = begin + wave;
+    if (step < end) {
+      keys(step);
+      values(step);
+    }
+  };
+  auto steps_to = [&](auto kind, int to) __attribute__((always_inline)) -> bool {
+    for (; step < to; step += kFewWaves)
+      if (!one_step(kind, step)) return false;
+    return true;
+  };
+  start();
+  // Steps at the window's start, whole steps, steps at the diagonal: two rounds
+  // of whole and then edge steps, so that each kind's code is there once.
+  const int whole_lo = (w.lo_max + kStep - 1) / kStep, whole_hi = max((w.p_min + 1) / kStep, whole_lo);
+  bool done = true;
+  for (int round = 0; round < 2 && done; ++round) {
+    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end));
+    done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
+  }
+  if (!done) {
+    start();
+    steps_to(std::integral_constant<int, kCareful>{}, end);
   }
 
   // The four waves join. Register r of O^T tile u W + j is element
