@@ -67,7 +67,7 @@ struct Partials {
 // NaN (rare), the whole range again with careful steps. Kept apart so that the
 // common loops hold no registers for the rare ones.
 // kEither decides between the first two step by step.
-enum StepKind { kWhole, kEdgeStep, kEither, kCareful };
+enum StepKind { kWhole, kGrow, kEdgeStep, kEither, kCareful };
 
 // One workgroup's sequence, row tile and token range.
 struct Work {

@@ -26,6 +26,7 @@ namespace qlinear {
 namespace attn {
 
 constexpr int kChunkThreads = 256;
+constexpr int kAheadK = 6, kAheadV = 4;     // fragments read ahead of the products
 
 // The place of 16-byte piece x of row `row` (keys: eight rows of one piece in
 // a cycle; values: four rows of 64 neighbouring bytes).
@@ -66,6 +67,20 @@ __device__ __forceinline__ u32x4 decode8(uint32_t a, uint32_t b, half2v s) {
     r[3] = as_u32(code_pair<6>((y >> 6) & 0x003F003Fu, s));
   }
   return r;
+}
+
+// Scheduling of a run of N matrix products fed by R LDS reads each: `Ahead`
+// products' reads first, then one product for every further R reads.
+template <int N, int R, int Ahead>
+__device__ __forceinline__ void feed_ahead() {
+  constexpr int kMfma = 0x8, kDsRead = 0x100;
+  __builtin_amdgcn_sched_group_barrier(kDsRead, R * Ahead, 0);
+#pragma unroll
+  for (int i = 0; i < N - Ahead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kDsRead, R, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(kMfma, Ahead, 0);
 }
 
 template <int D, int B>
@@ -135,6 +150,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       for (int e = 0; e < 8; ++e) q[f][e] = x[unpacked<B>(e)];
     }
   }
+  const float slack = 8.0f / (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e);
   const float sc = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
 
   const PageTable table = page_table(a, w.b);
@@ -251,8 +267,8 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     constexpr bool kSplit = decltype(kind)::value == kCareful;
     const int t0 = step * T;
     const bool edge = decltype(kind)::value == kEither ? t0 + T - 1 > w.p_min || t0 < w.lo_max
-                                                       : decltype(kind)::value != kWhole;
-    if (step + 1 < end) {
+                                                       : decltype(kind)::value != kWhole && decltype(kind)::value != kGrow;
+    if (decltype(kind)::value != kGrow && step + 1 < end) {
       if constexpr (B == 16) {
         stage_direct(step + 1, kn, vn);
         look_up(step + 2);
@@ -297,6 +313,8 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
           const half8 kf = __builtin_bit_cast(half8, *(Lds4)(kc + key * D + key_piece<D>(key, 2 * f + h) * 8));
           s[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[f], s[k], 0, 0, 0);
         }
+      feed_ahead<kFrags * kKeyTiles, 1, kAheadK>();
+      __builtin_amdgcn_sched_barrier(0);
 
       if (edge) {
 #pragma unroll
@@ -313,16 +331,18 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
 #pragma unroll
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[k][r]);
       mx = max32(mx);
-      const float mn = fmaxf(m, mx);
-      // Always rescaled: around a branch that skips it when no maximum grew,
-      // the compiler copies all of o twice, which costs more.
-      const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m * sc - mn * sc);
-      m = mn;
-      l *= alpha;
+      if constexpr (decltype(kind)::value == kWhole) {
+        if (__any(mx > m + slack)) return false;
+      } else {
+        const float mn = fmaxf(m, mx);
+        const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m * sc - mn * sc);
+        m = mn;
+        l *= alpha;
 #pragma unroll
-      for (int d = 0; d < kOutTiles; ++d)
+        for (int d = 0; d < kOutTiles; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
+          for (int r = 0; r < 16; ++r) o[d][r] *= alpha;
+      }
       const float base = m == -INFINITY ? 0.0f : m * sc;
       float sum = 0.0f;
 #pragma unroll
@@ -386,12 +406,15 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     }
 
     if (active) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int cc = 0; cc < T / 16; ++cc)
 #pragma unroll
         for (int d = 0; d < kOutTiles; ++d)
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, value_fragment(vc, cc, d)), p[cc],
                                                         o[d], 0, 0, 0);
+      feed_ahead<T / 16 * kOutTiles, 2, kAheadV>();
+      __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (B != 16) {
       if (step + 1 < end) unpack(kn, vn);
@@ -419,9 +442,21 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   int step = begin, buf = 0;
   // Steps of one kind up to `to`; each turns the buffers.
   auto steps_to = [&](auto kind, int to) __attribute__((always_inline)) -> bool {
-    for (; step < to; ++step, buf ^= 1) {
-      __syncthreads();     // this step's rows are in LDS; the other buffers are free
-      if (!one_step(kind, step, (Lds)ks[buf], (Lds)vs[buf], (Lds)ks[buf ^ 1], (Lds)vs[buf ^ 1])) return false;
+    while (step < to) {
+      for (; step < to; ++step, buf ^= 1) {
+        __syncthreads();     // this step's rows are in LDS; the other buffers are free
+        if (!one_step(kind, step, (Lds)ks[buf], (Lds)vs[buf], (Lds)ks[buf ^ 1], (Lds)vs[buf ^ 1])) break;
+      }
+      if constexpr (decltype(kind)::value == kWhole) {
+        if (step < to) {
+          one_step(std::integral_constant<int, kGrow>{}, step, (Lds)ks[buf], (Lds)vs[buf], (Lds)ks[buf ^ 1],
+                   (Lds)vs[buf ^ 1]);
+          ++step;
+          buf ^= 1;
+        }
+      } else {
+        return step == to;
+      }
     }
     return true;
   };
