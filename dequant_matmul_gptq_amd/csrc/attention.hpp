@@ -49,7 +49,7 @@ __host__ __device__ constexpr int chunk_step(int D) { return D == 256 ? 32 : 64;
 
 // Row tiles of the chunk kernel, at most, whatever the sequences' lengths.
 inline int64_t chunk_tiles(const AttentionArgs& a, int group) {
-  return (int64_t)a.tokens * group / kChunkRows + a.batch;
+  return ((int64_t)a.tokens * group + (kChunkRows - 1) * (int64_t)a.batch) / kChunkRows;
 }
 
 // Partial results of a split launch, float32: o [splits][rows][D] and (m, l)
@@ -62,12 +62,12 @@ struct Partials {
   int cap;
 };
 
-// The kernels' loops come in three kinds of step: whole ones that all rows see
-// all of, edge ones with masks, and, where an edge step holds infinities or
-// NaN (rare), the whole range again with careful steps. Kept apart so that the
-// common loops hold no registers for the rare ones.
-// kEither decides between the first two step by step.
-enum StepKind { kWhole, kGrow, kEdgeStep, kEither, kCareful };
+// The kernels' loops come in kinds of step: whole ones that all rows see all
+// of (kGrow: with the accumulators rescaled), edge ones with masks, and, where
+// an edge step holds infinities or NaN (rare), the whole range again with
+// careful steps. Kept apart so that the common loops hold no registers for the
+// rare ones.
+enum StepKind { kWhole, kGrow, kEdgeStep, kCareful };
 
 // One workgroup's sequence, row tile and token range.
 struct Work {

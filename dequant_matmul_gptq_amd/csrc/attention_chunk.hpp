@@ -266,8 +266,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
                       Lds __restrict__ vn) __attribute__((always_inline)) -> bool {
     constexpr bool kSplit = decltype(kind)::value == kCareful;
     const int t0 = step * T;
-    const bool edge = decltype(kind)::value == kEither ? t0 + T - 1 > w.p_min || t0 < w.lo_max
-                                                       : decltype(kind)::value != kWhole && decltype(kind)::value != kGrow;
+    constexpr bool kEdge = decltype(kind)::value == kEdgeStep || kSplit;
     if (decltype(kind)::value != kGrow && step + 1 < end) {
       if constexpr (B == 16) {
         stage_direct(step + 1, kn, vn);
@@ -278,7 +277,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     }
 
     bool nonfinite = false;
-    if (edge) {
+    if constexpr (kEdge) {
       // Values of tokens that no row sees may be anything: zero. A weight of
       // 0 does not hide an infinity or NaN of a token that only some rows see.
       uint32_t bad = 0;
@@ -297,7 +296,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       if (!kSplit && nonfinite) return false;
     }
 
-    const bool active = !edge || (t0 <= wp_max && t0 + T - 1 >= wlo_min);
+    const bool active = !kEdge || (t0 <= wp_max && t0 + T - 1 >= wlo_min);
     half8 p[T / 16];
     if (active) {
       float16v s[kKeyTiles];
@@ -316,7 +315,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       feed_ahead<kFrags * kKeyTiles, 1, kAheadK>();
       __builtin_amdgcn_sched_barrier(0);
 
-      if (edge) {
+      if constexpr (kEdge) {
 #pragma unroll
         for (int k = 0; k < kKeyTiles; ++k)
 #pragma unroll
@@ -462,18 +461,12 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   };
   start();
   bool done = true;
-  if constexpr (D < 256) {
-    // Steps at the window's start, whole steps, steps at the diagonal: two
-    // rounds of whole and then edge steps, so that each kind's code is there once.
-    const int whole_lo = (w.lo_max + T - 1) / T, whole_hi = max((w.p_min + 1) / T, whole_lo);
-    for (int round = 0; round < 2 && done; ++round) {
-      steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end));
-      done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
-    }
-  } else {
-    // Its accumulators take half the registers, and going from loop to loop
-    // costs more than the branch does (4096 tokens, 16/4 heads: 543 to 331 us).
-    done = steps_to(std::integral_constant<int, kEither>{}, end);
+  // Steps at the window's start, whole steps, steps at the diagonal: two rounds
+  // of whole and then edge steps, so that each kind's code is there once.
+  const int whole_lo = (w.lo_max + T - 1) / T, whole_hi = max((w.p_min + 1) / T, whole_lo);
+  for (int round = 0; round < 2 && done; ++round) {
+    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end));
+    done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
   }
   if (!done) {
     __syncthreads();       // the staging under way has ended
