@@ -261,12 +261,12 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int group = a.q_heads / c.kv_heads;
-  const int split = blockIdx.x, head = blockIdx.y % c.kv_heads, tile = blockIdx.y / c.kv_heads;
+  const int split = blockIdx.z, head = blockIdx.x % c.kv_heads, tile = blockIdx.x / c.kv_heads;
   const int page_shift = __builtin_ctz(c.page_size);
   const int group_shift = B == 16 ? 0 : __builtin_ctz(c.group);
 
   Work w;
-  sequence(a, c, blockIdx.z, w);
+  sequence(a, c, blockIdx.y, w);
   const int64_t seq_rows = (int64_t)w.n * group;
   if (tile * 16 * NT >= seq_rows || seq_rows > plan.max_rows) return;
   row_tile(a, group, tile * 16 * NT, 16 * NT, w);
@@ -562,7 +562,9 @@ hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const P
   const int group = a.q_heads / c.kv_heads;
   const int64_t most = (int64_t)a.max_q_len * group;
   const int tiles = (int)(((most < p.max_rows ? most : p.max_rows) + p.rows - 1) / p.rows);
-  const dim3 grid((unsigned)p.splits, (unsigned)(c.kv_heads * tiles), (unsigned)a.batch);
+  // Ranges vary slowest: those past a sequence's end are then neighbours in the
+  // grid, and what work there is goes to all XCDs alike.
+  const dim3 grid((unsigned)(c.kv_heads * tiles), (unsigned)a.batch, (unsigned)p.splits);
   if (p.rows == 16)
     hipLaunchKernelGGL((attention_few_kernel<D, B, 1>), grid, dim3(64 * kFewWaves), 0, stream, a, c, p, part);
   else if constexpr (D < 256)
