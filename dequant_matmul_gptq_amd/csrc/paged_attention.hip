@@ -9,12 +9,87 @@ namespace {
 
 using namespace attn;
 
-// Joins the partial results of a split launch, one workgroup per row: the
-// ranges' weights 2^(m - max m) first (kJoinBatch at a time in LDS), then the
-// sum over ranges with D / 4 threads to a range and several loads in flight.
-// Threads and ranges are added in a fixed order.
-// FEW: workgroup (row, key/value head, sequence); else (row tile and head,
-// row).
+// The row of a join's workgroup: FEW, row r of (key/value head, sequence) in
+// the grid's y and z; else row r of the tile and head in y. False: no such row.
+struct JoinRow {
+  int64_t out, part;     // row of the output, of the partial results
+};
+template <bool FEW>
+__device__ __forceinline__ bool join_row(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                         const Partials& part, int r, JoinRow& j) {
+  const int group = a.q_heads / c.kv_heads;
+  Work w;
+  int head;
+  if constexpr (FEW) {
+    head = blockIdx.y;
+    sequence(a, c, blockIdx.z, w);
+    const int64_t seq_rows = (int64_t)w.n * group;
+    if (r >= seq_rows || seq_rows > plan.max_rows) return false;
+  } else {
+    int tile = 0;
+    head = blockIdx.y % c.kv_heads;
+    if (!find_tile(a, c, plan, group, blockIdx.y / c.kv_heads, w, tile)) return false;
+    r += tile * kChunkRows;
+    if (r >= w.n * group) return false;
+  }
+  j.out = (int64_t)(w.q0 + r / group) * a.q_heads + head * group + r % group;
+  j.part = FEW ? ((int64_t)w.b * c.kv_heads + head) * part.cap + r : j.out;
+  return true;
+}
+
+// Joins the partial results of a split launch: o = sum_s f_s o_s / sum_s f_s
+// l_s with f_s = 2^(m_s - max m), an empty range (m = -infinity, o not
+// written) left out. Bound by the latency of its reads, so few of them wait
+// for one another. Up to kJoinFew ranges: one wave a row, all reads at once.
+constexpr int kJoinFew = 16;
+template <int D, bool FEW>
+__global__ __launch_bounds__(256) void attention_join_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
+                                                                 Partials part) {
+  constexpr int kLanes = D / 4, kSide = 64 / kLanes;     // lanes to a range, ranges at a time
+  const int lane = threadIdx.x & 63, side = lane / kLanes, d = lane % kLanes;
+  JoinRow row;
+  if (!join_row<FEW>(a, c, plan, part, blockIdx.x * 4 + (threadIdx.x >> 6), row)) return;
+  const int splits = plan.splits;
+  float2 ml = make_float2(-INFINITY, 0.0f);
+  if (lane < splits) ml = part.ml[lane * part.rows + row.part];
+  const float4v* p = reinterpret_cast<const float4v*>(part.o) + row.part * kLanes + d;
+  float4v x[kJoinFew / kSide];
+#pragma unroll
+  for (int i = 0; i < kJoinFew / kSide; ++i) {
+    const int s = i * kSide + side;
+    x[i] = p[(s < splits ? s : 0) * part.rows * kLanes];
+  }
+  float top = ml.x;
+#pragma unroll
+  for (int k = 1; k < kJoinFew; k <<= 1) top = fmaxf(top, __shfl_xor(top, k, kJoinFew));
+  top = __shfl(top, 0);
+  const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+  float total = f * ml.y;
+#pragma unroll
+  for (int k = 1; k < kJoinFew; k <<= 1) total += __shfl_xor(total, k, kJoinFew);
+  total = __shfl(total, 0);
+  float4v o = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kJoinFew / kSide; ++i) {
+    const int s = i * kSide + side;
+    const float fs = __shfl(f, s), ms = __shfl(ml.x, s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += ms == -INFINITY ? 0.0f : fs * x[i][e];
+  }
+#pragma unroll
+  for (int k = kLanes; k < 64; k <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], k);
+  if (side != 0) return;
+  half4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (_Float16)(top == -INFINITY ? 0.0f : o[e] / total);
+  *reinterpret_cast<half4*>(a.out + row.out * D + 4 * d) = y;
+}
+
+// More ranges: a workgroup a row, the weights kJoinBatch at a time in LDS,
+// then D / 4 threads to a range and several loads in flight. Threads and
+// ranges are added in a fixed order.
 constexpr int kJoinBatch = 256;
 template <int D, bool FEW>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
@@ -23,24 +98,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, ql
   __shared__ float weight[kJoinBatch];
   __shared__ float tops[4], sums[4];
   __shared__ float4v o_part[kSide][D / 4];
-  const int group = a.q_heads / c.kv_heads;
-  Work w;
-  int r, head;
-  if constexpr (FEW) {
-    r = blockIdx.x;
-    head = blockIdx.y;
-    sequence(a, c, blockIdx.z, w);
-    const int64_t seq_rows = (int64_t)w.n * group;
-    if (r >= seq_rows || seq_rows > plan.max_rows) return;
-  } else {
-    int tile = 0;
-    head = blockIdx.x % c.kv_heads;
-    if (!find_tile(a, c, plan, group, blockIdx.x / c.kv_heads, w, tile)) return;
-    r = tile * kChunkRows + blockIdx.y;
-    if (r >= w.n * group) return;
-  }
-  const int64_t out_row = (int64_t)(w.q0 + r / group) * a.q_heads + head * group + r % group;
-  const int64_t row = FEW ? ((int64_t)w.b * c.kv_heads + head) * part.cap + r : out_row, rows = part.rows;
+  JoinRow at;
+  if (!join_row<FEW>(a, c, plan, part, blockIdx.x, at)) return;
+  const int64_t row = at.part, rows = part.rows;
   const int splits = plan.splits;
   const int t = threadIdx.x, side = t / (D / 4), d = t % (D / 4);
   float top = -INFINITY;
@@ -58,9 +118,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, ql
     if (s0) __syncthreads();
     if (t < n) {
       const float2 ml = part.ml[(s0 + t) * rows + row];
-      // An empty range (m = -infinity) has no o: weight -1 says so.
       const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-      weight[t] = ml.x == -INFINITY ? -1.0f : f;
+      weight[t] = ml.x == -INFINITY ? -1.0f : f;       // -1: left out
       total += f * ml.y;
     }
     __syncthreads();
@@ -83,14 +142,33 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, ql
   half4 y;
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = (_Float16)(top == -INFINITY ? 0.0f : o[e] / total);
-  *reinterpret_cast<half4*>(a.out + out_row * D + 4 * d) = y;
+  *reinterpret_cast<half4*>(a.out + at.out * D + 4 * d) = y;
 }
 
-// Steps of `tokens` that a row tile can span at most.
+template <int D, bool FEW>
+hipError_t launch_join_width(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
+                             int rows, dim3 grid, hipStream_t stream) {
+  const bool few = p.splits <= kJoinFew;
+  grid.x = (unsigned)(few ? (rows + 3) / 4 : rows);
+  auto kernel = few ? attention_join_few_kernel<D, FEW> : attention_join_kernel<D, FEW>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, c, p, part);
+  return hipGetLastError();
+}
+
+// `rows` rows for each place of the grid's y and z.
+template <bool FEW>
+hipError_t launch_join(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
+                       int rows, dim3 grid, hipStream_t stream) {
+  if (c.head_dim == 64) return launch_join_width<64, FEW>(c, a, p, part, rows, grid, stream);
+  if (c.head_dim == 128) return launch_join_width<128, FEW>(c, a, p, part, rows, grid, stream);
+  return launch_join_width<256, FEW>(c, a, p, part, rows, grid, stream);
+}
+
+// Steps of `tokens` tokens that a row tile spans at most.
 int64_t plan_steps(const AttentionArgs& a, int tokens) {
-  int64_t n = a.max_kv_len;
-  if (a.window > 0 && (int64_t)a.window + a.max_q_len < n) n = (int64_t)a.window + a.max_q_len;
-  return n / tokens + 2;
+  const int64_t reach = (int64_t)a.window + a.max_q_len;       // a window's start is inside a step
+  if (a.window > 0 && reach < a.max_kv_len) return (reach + tokens - 1) / tokens + 1;
+  return (a.max_kv_len + (int64_t)tokens - 1) / tokens;
 }
 
 // The sequences of a call are served by their number of rows per key/value
@@ -119,19 +197,17 @@ Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
     p.chunk = INT32_MAX;
     const int64_t tiles = (int64_t)(r.few_cap + p.rows - 1) / p.rows * c.kv_heads * a.batch;
     const int64_t steps = plan_steps(a, kStep);
-    // A range is long enough that writing and reading its partial result is
-    // about 1/25 of reading its keys and values, unless that leaves fewer than
-    // two workgroups per CU; short enough for about 4096 workgroups.
-    const int64_t row_bytes = c.bits == 16 ? 2 * c.head_dim : c.head_dim * c.bits / 8 + 2 * c.head_dim / c.group;
-    const int64_t used = r.few_cap < p.rows ? r.few_cap : p.rows;
-    const int64_t light = 25 * used * c.head_dim * 4 / (row_bytes * kStep);
-    const int64_t even = (tiles * steps + 4095) / 4096;
-    const int64_t fill = (tiles * steps + 511) / 512;
-    int64_t chunk = even > light ? even : light;
-    if (chunk > fill) chunk = fill;
+    // Ranges for two workgroups per CU (what their registers allow), of 4 to
+    // 64 steps: shorter ones cost more in partial results than they spread
+    // (64 sequences of 2048 tokens, 64/8 heads: 96.8 us whole, 102.6, 107, 123
+    // us in ranges of 64, 16, 4 steps), longer ones leave CUs idle at the end
+    // (one of 32768: 31.0, 31.1, 40.1 us in ranges of 16, 64, 96).
+    int64_t chunk = (tiles * steps + 511) / 512;
     if (chunk < 4) chunk = 4;
+    if (chunk > 64) chunk = 64;
     if (getenv("QL_CHUNK")) chunk = atoi(getenv("QL_CHUNK"));
     p.splits = (int)((steps + chunk - 1) / chunk);
+    if (p.splits < 1) p.splits = 1;
     if (p.splits > 1) {
       p.chunk = (int)chunk;
       r.few_rows = (int64_t)a.batch * c.kv_heads * r.few_cap;
@@ -193,12 +269,9 @@ hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const Attention
                                     : launch_attention_chunk_256(cache, a, p, part, stream);
     if (e != hipSuccess) return e;
     if (r.chunk_rows > 0) {
-      auto join = D == 64    ? attention_join_kernel<64, false>
-                  : D == 128 ? attention_join_kernel<128, false>
-                             : attention_join_kernel<256, false>;
-      hipLaunchKernelGGL(join, dim3((unsigned)(chunk_tiles(a, group) * cache.kv_heads), kChunkRows), dim3(256), 0,
-                         stream, a, cache, p, part);
-      const hipError_t j = hipGetLastError();
+      // Splitting needs few workgroups, so the grid's y holds them.
+      const hipError_t j = launch_join<false>(cache, a, p, part, kChunkRows,
+                                              dim3(1, (unsigned)(chunk_tiles(a, group) * cache.kv_heads)), stream);
       if (j != hipSuccess) return j;
     }
   }
@@ -210,14 +283,9 @@ hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const Attention
                          : D == 128 ? launch_attention_few_128(cache, a, p, part, stream)
                                     : launch_attention_few_256(cache, a, p, part, stream);
     if (e != hipSuccess) return e;
-    if (r.few_rows > 0) {
-      auto join = D == 64    ? attention_join_kernel<64, true>
-                  : D == 128 ? attention_join_kernel<128, true>
-                             : attention_join_kernel<256, true>;
-      hipLaunchKernelGGL(join, dim3((unsigned)r.few_cap, (unsigned)cache.kv_heads, (unsigned)a.batch), dim3(256), 0,
-                         stream, a, cache, p, part);
-      return hipGetLastError();
-    }
+    if (r.few_rows > 0)
+      return launch_join<true>(cache, a, p, part, r.few_cap,
+                               dim3(1, (unsigned)cache.kv_heads, (unsigned)a.batch), stream);
   }
   return hipSuccess;
 }
