@@ -13,10 +13,53 @@ import math
 import numpy as np
 import torch
 
-from ._lib import _check, _dev, _ptr, _stream, lib, qlinear_kv_cache
+from ._lib import _check, _dev, _ptr, lib, qlinear_kv_cache
 
 ROPE_HALF = 0
 ROPE_INTERLEAVED = 1
+
+_F16, _F32, _I32, _U8 = torch.float16, torch.float32, torch.int32, torch.uint8
+
+# These calls are short on the GPU (a few microseconds for one token), so the
+# checks below are kept to a few attribute reads, and the stream is taken as
+# the raw handle (0.1 us; a Stream object takes 2 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
+
+
+def _operand(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
+    """Check a contiguous operand on GPU `device` and return its pointer."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        _dev(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on GPU {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, tokens: int | None, heads: int | None, dim: int | None, device: int):
+    """Check a float16 [tokens][heads][dim] operand on GPU `device` whose tokens
+    may be strided (a slice of a fused projection). Returns its pointer, shape
+    and token stride."""
+    if t.dtype is not _F16 or t.get_device() != device or t.dim() != 3:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.dtype is not _F16:
+            raise ValueError(f"{name} must be {_F16}, got {t.dtype}")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [tokens][heads][head_dim], got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be on GPU {device}, got {t.device}")
+    T, h, d = t.shape
+    if (tokens is not None and T != tokens) or (heads is not None and h != heads) or (dim is not None and d != dim):
+        want = [n if v is None else v for n, v in (("tokens", tokens), ("heads", heads), ("head_dim", dim))]
+        raise ValueError(f"{name} must be [{want[0]}][{want[1]}][{want[2]}], got {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if T < 2 or h == 0 or d == 0:
+        st = h * d
+    if T > 0 and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), T, h, d, st
 
 
 class KVCache:
@@ -56,6 +99,11 @@ class KVCache:
         self.num_pages, self.kv_heads, self.page_size = pages, heads, page
         self.c = qlinear_kv_cache(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), pages, page, heads, self.head_dim,
                                   self.bits, self.group)
+        self.ref, self.raw = ctypes.byref(self.c), bytes(self.c)
+        self.device = k.get_device()
+        for name, t in (("v", v), ("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None and t.get_device() != self.device:
+                raise ValueError(f"{name} must be on GPU {self.device}, got {t.device}")
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, head_dim: int, page_size: int = 256, bits: int = 16,
@@ -70,33 +118,6 @@ class KVCache:
         kv = [torch.empty(lead + (head_dim * bits // 32,), dtype=torch.int32, device=device) for _ in range(2)]
         s = [torch.empty(lead + (head_dim // group,), dtype=torch.float16, device=device) for _ in range(2)]
         return cls(*kv, *s, head_dim=head_dim)
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
-
-
-def _rows(t: torch.Tensor, name: str, heads: int | None, dim: int | None) -> int:
-    """Check a float16 [tokens][heads][dim] operand whose tokens may be strided
-    (a slice of a fused projection) and return the token stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype != torch.float16:
-        raise ValueError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} must be [tokens][{heads or 'heads'}][{dim or 'head_dim'}], got {tuple(t.shape)}")
-    h, d = int(t.shape[1]), int(t.shape[2])
-    if t.numel() == 0:
-        return h * d
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return int(t.stride(0)) if t.shape[0] > 1 else h * d
-
-
-def _same_device(ref: torch.Tensor, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -164,30 +185,25 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: dict 
     return torch.from_numpy(out).to(device)
 
 
-def _rope_operands(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, tokens: int):
+def _rope_operands(table: torch.Tensor, positions: torch.Tensor, tokens: int, device: int):
     if table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("table must be [positions][rot_dim / 2][2]")
-    _dev(table, "table", torch.float32)
-    _dev(positions, "positions", torch.int32, (tokens,))
-    _same_device(x, table=table, positions=positions)
-    return int(table.shape[0]), 2 * int(table.shape[1])
+    rows, half, _ = table.shape
+    return (_operand(positions, "positions", _I32, (tokens,), device),
+            _operand(table, "table", _F32, (rows, half, 2), device), rows, 2 * half)
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: int = ROPE_HALF,
          out: torch.Tensor | None = None) -> torch.Tensor:
     """x float16 [tokens][heads][head_dim] (token stride free) rotated to the
     positions (int32 [tokens]) by the table of rope_table. out may be x."""
-    xs = _rows(x, "x", None, None)
-    T, H, D = (int(n) for n in x.shape)
-    rows, rot = _rope_operands(x, table, positions, T)
+    dev = x.get_device()
+    xp, T, H, D, xs = _rows(x, "x", None, None, None, dev)
+    pos, tab, rows, rot = _rope_operands(table, positions, T, dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.float16, device=x.device)
-    os_ = _rows(out, "out", H, D)
-    if out.shape[0] != T:
-        raise ValueError(f"out must have {T} tokens")
-    _same_device(x, out=out)
-    _check(lib().qlinear_rope(_ptr(x), xs, T, H, D, _ptr(positions), _ptr(table), rows, rot, int(layout), _ptr(out),
-                              os_, _stream(x.device)), "qlinear_rope")
+        out = torch.empty((T, H, D), dtype=_F16, device=x.device)
+    op, _, _, _, ost = _rows(out, "out", T, H, D, dev)
+    _check(lib().qlinear_rope(xp, xs, T, H, D, pos, tab, rows, rot, layout, op, ost, _stream(dev)), "qlinear_rope")
     return out
 
 
@@ -199,33 +215,25 @@ def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torc
     cache's slots (int32 [tokens]: page * page_size + place in the page,
     negative = not appended). table None: no rotation. q None: only the append.
     """
-    D, T = cache.head_dim, int(k.shape[0])
-    ks, vs = _rows(k, "k", cache.kv_heads, D), _rows(v, "v", cache.kv_heads, D)
-    if v.shape[0] != T:
-        raise ValueError(f"v must have {T} tokens")
-    _dev(slots, "slots", torch.int32, (T,))
-    rows, rot = 0, 0
+    dev, D, Hk = cache.device, cache.head_dim, cache.kv_heads
+    kp, T, _, _, ks = _rows(k, "k", None, Hk, D, dev)
+    vp, _, _, _, vs = _rows(v, "v", T, Hk, D, dev)
+    sp = _operand(slots, "slots", _I32, (T,), dev)
+    pos = tab = qp = op = None
+    rows = rot = heads = qs = ost = 0
     if table is not None:
         if positions is None:
             raise ValueError("a table needs positions")
-        rows, rot = _rope_operands(k, table, positions, T)
-    heads = qs = os_ = 0
+        pos, tab, rows, rot = _rope_operands(table, positions, T, dev)
     if q is not None:
-        heads = int(q.shape[1]) if q.dim() == 3 else 0
-        qs = _rows(q, "q", None, D)
-        if q.shape[0] != T:
-            raise ValueError(f"q must have {T} tokens")
+        qp, _, heads, _, qs = _rows(q, "q", T, None, D, dev)
         if q_out is None:
-            q_out = torch.empty((T, heads, D), dtype=torch.float16, device=q.device)
-        os_ = _rows(q_out, "q_out", heads, D)
-        if q_out.shape[0] != T:
-            raise ValueError(f"q_out must have {T} tokens")
+            q_out = torch.empty((T, heads, D), dtype=_F16, device=q.device)
+        op, _, _, _, ost = _rows(q_out, "q_out", T, heads, D, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _same_device(cache.k, q=q, q_out=q_out, k=k, v=v, slots=slots)
-    _check(lib().qlinear_rope_append(cache.ref, _ptr(q), qs, heads, _ptr(k), ks, _ptr(v), vs, _ptr(q_out), os_, T,
-                                     _ptr(positions) if rot else None, _ptr(slots), _ptr(table), rows, rot,
-                                     int(layout), _stream(k.device)), "qlinear_rope_append")
+    _check(lib().qlinear_rope_append(cache.ref, qp, qs, heads, kp, ks, vp, vs, op, ost, T, pos, sp, tab, rows, rot,
+                                     layout, _stream(dev)), "qlinear_rope_append")
     return q_out
 
 
@@ -266,32 +274,29 @@ def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, 
     out float16 [tokens][q_heads][head_dim]; a token that sees nothing gets
     zeros.
     """
-    qs = _rows(q, "q", None, cache.head_dim)
-    T, H = int(q.shape[0]), int(q.shape[1])
+    dev, D = cache.device, cache.head_dim
+    qp, T, H, _, qs = _rows(q, "q", None, None, D, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch][width]")
-    B, W = int(block_table.shape[0]), int(block_table.shape[1])
-    _dev(block_table, "block_table", torch.int32)
-    _dev(kv_len, "kv_len", torch.int32, (B,))
-    if q_start is not None:
-        _dev(q_start, "q_start", torch.int32, (B + 1,))
+    B, W = block_table.shape
+    tp = _operand(block_table, "block_table", _I32, (B, W), dev)
+    lp = _operand(kv_len, "kv_len", _I32, (B,), dev)
+    sp = None if q_start is None else _operand(q_start, "q_start", _I32, (B + 1,), dev)
     if max_q_len is None:
         max_q_len = T if q_start is not None or B == 0 else T // B
     if max_kv_len is None:
         max_kv_len = min(W * cache.page_size, 2 ** 31 - 1)
     if scale is None:
-        scale = cache.head_dim ** -0.5
+        scale = D ** -0.5
     if out is None:
-        out = torch.empty((T, H, cache.head_dim), dtype=torch.float16, device=q.device)
-    _dev(out, "out", torch.float16, (T, H, cache.head_dim))
+        out = torch.empty((T, H, D), dtype=_F16, device=q.device)
+    op = _operand(out, "out", _F16, (T, H, D), dev)
     if workspace is None:
         workspace = paged_attention_workspace(cache, T, H, B, max_q_len, max_kv_len, q.device, window)
-    _dev(workspace, "workspace", torch.uint8)
-    _same_device(cache.k, q=q, block_table=block_table, kv_len=kv_len, q_start=q_start, out=out, workspace=workspace)
-    _check(lib().qlinear_paged_attention(cache.ref, _ptr(q), qs, T, H, B, _ptr(q_start), _ptr(kv_len),
-                                         _ptr(block_table), W, int(max_q_len), int(max_kv_len), float(scale),
-                                         int(window), _ptr(out), _ptr(workspace), workspace.numel(),
-                                         _stream(q.device)), "qlinear_paged_attention")
+    n = workspace.numel()
+    wp = _operand(workspace, "workspace", _U8, (n,), dev)
+    _check(lib().qlinear_paged_attention(cache.ref, qp, qs, T, H, B, sp, lp, tp, W, max_q_len, max_kv_len, scale,
+                                         window, op, wp, n, _stream(dev)), "qlinear_paged_attention")
     return out
 
 
@@ -301,15 +306,19 @@ def copy_pages(caches, pairs: torch.Tensor) -> None:
     """Page pairs[i][1] becomes a copy of page pairs[i][0] in every cache of
     `caches` (a model's layers, one shape); pairs int32 [moves][2]. No page may
     be a target and appear in another pair."""
-    caches = list(caches)
-    if pairs.dim() != 2 or pairs.shape[1] != 2:
+    dev = pairs.get_device()
+    if pairs.dim() != 2:
         raise ValueError("pairs must be [moves][2]")
-    _dev(pairs, "pairs", torch.int32)
+    moves = pairs.shape[0]
+    pp = _operand(pairs, "pairs", _I32, (moves, 2), dev)
+    caches = list(caches)
     for c in caches:
-        _same_device(c.k, pairs=pairs)
-    arr = (qlinear_kv_cache * max(1, len(caches)))(*[c.c for c in caches])
-    _check(lib().qlinear_copy_pages(arr, len(caches), _ptr(pairs), int(pairs.shape[0]), _stream(pairs.device)),
-           "qlinear_copy_pages")
+        if c.device != dev:
+            raise ValueError(f"pairs must be on the caches' GPU {c.device}, got {pairs.device}")
+    # The structs side by side (ctypes' own array constructor takes 0.3 us each).
+    arr = (qlinear_kv_cache * max(1, len(caches))).from_buffer_copy(
+        b"".join([c.raw for c in caches]) or bytes(ctypes.sizeof(qlinear_kv_cache)))
+    _check(lib().qlinear_copy_pages(arr, len(caches), pp, moves, _stream(dev)), "qlinear_copy_pages")
 
 
 # ---------------------------------------------------------------- norm
@@ -321,18 +330,15 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual:
     residual_out if it is given (it may be x or residual). out may be x."""
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
-    K = int(x.shape[-1])
-    _dev(x, "x", torch.float16)
-    _dev(weight, "weight", torch.float16, (K,))
-    if residual is not None:
-        _dev(residual, "residual", torch.float16, tuple(x.shape))
+    dev, shape = x.get_device(), x.shape
+    K = shape[-1]
+    xp = _operand(x, "x", _F16, shape, dev)
+    wp = _operand(weight, "weight", _F16, (K,), dev)
+    rp = None if residual is None else _operand(residual, "residual", _F16, shape, dev)
     if out is None:
         out = torch.empty_like(x)
-    _dev(out, "out", torch.float16, tuple(x.shape))
-    if residual_out is not None:
-        _dev(residual_out, "residual_out", torch.float16, tuple(x.shape))
-    _same_device(x, weight=weight, residual=residual, out=out, residual_out=residual_out)
+    op = _operand(out, "out", _F16, shape, dev)
+    hp = None if residual_out is None else _operand(residual_out, "residual_out", _F16, shape, dev)
     M = x.numel() // K if K else 0
-    _check(lib().qlinear_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), M, K, float(eps), _ptr(out),
-                                  _ptr(residual_out), _stream(x.device)), "qlinear_rms_norm")
+    _check(lib().qlinear_rms_norm(xp, rp, wp, M, K, eps, op, hp, _stream(dev)), "qlinear_rms_norm")
     return out
