@@ -61,78 +61,109 @@ __device__ __forceinline__ void encode8(const Half8& x, int u, uint32_t* words, 
 
 // B: 0 rotates q rows only, 16 appends to a float16 cache, 8 / 6 / 4 to a
 // quantized one with blocks of G. Rows of a token: q heads, k heads, v heads.
-template <int B, int G>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, qlinear_kv_cache c, int heads_per_thread) {
+// H: rows a thread goes over, all of them read before the first is written;
+// reads past the last row, or of a partner that is not needed, take an address
+// in reach instead of a branch.
+template <int B, int G, int H, bool HALF>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, qlinear_kv_cache c) {
   const int D = a.head_dim, U = D / 8;
   const int lane = threadIdx.x & 63;
-  const int rows_per_wave = 64 / U;
-  const int in_wave = lane / U, u = lane - in_wave * U;
+  // A cache's head widths are powers of two.
+  const int rows_per_wave = B == 0 ? 64 / U : 64 >> __builtin_ctz(U);
+  const int in_wave = B == 0 ? lane / U : lane >> __builtin_ctz(U), u = lane - in_wave * U;
   if (in_wave >= rows_per_wave) return;
   const int t = blockIdx.x;
   const int total = B == 0 ? a.q_heads : a.q_heads + 2 * c.kv_heads;
   const int wave = blockIdx.y * (kThreads / 64) + (threadIdx.x >> 6);
-  int row = wave * rows_per_wave * heads_per_thread + in_wave;
+  const int row0 = wave * rows_per_wave * H + in_wave;
 
   const bool rotated = u * 8 < a.rot_dim;
-  const bool interleaved = a.layout == QLINEAR_ROPE_INTERLEAVED;
   const int half_units = a.rot_dim / 16;
   const bool low = u < half_units;
-  float2 cs[8];
+  const int partner = !rotated ? u : low ? u + half_units : u - half_units;
+
+  const uint16_t* q = a.q + t * a.q_stride;
+  const uint16_t* k = a.k + t * a.k_stride;
+  const uint16_t* v = a.v + t * a.v_stride;
+  Half8 x[H], o[H];      // the row's 8 elements, and in the half layout their partners
+#pragma unroll
+  for (int n = 0; n < H; ++n) {
+    const int row = min(row0 + n * rows_per_wave, total - 1);
+    const uint16_t* src = q + (int64_t)row * D;
+    if constexpr (B != 0) {
+      const int kv = row - a.q_heads;
+      if (kv >= 0) src = kv < c.kv_heads ? k + (int64_t)kv * D : v + (int64_t)(kv - c.kv_heads) * D;
+    }
+    x[n].v = *reinterpret_cast<const uint4*>(src + u * 8);
+    if constexpr (HALF) o[n].v = *reinterpret_cast<const uint4*>(src + partner * 8);
+  }
+
+  // (cos, sin) of the lane's pairs: 8 in the half layout, 4 else.
+  constexpr int kPairs = HALF ? 8 : 4;
+  float cs[2 * kPairs];
   if (rotated) {
     const int p = a.positions[t];
     const bool known = (unsigned)p < (unsigned)a.table_rows;
-    const float2* src = reinterpret_cast<const float2*>(a.table) + (int64_t)(known ? p : 0) * (a.rot_dim / 2) +
-                        (interleaved ? u * 4 : (low ? u : u - half_units) * 8);
+    const float4* src = reinterpret_cast<const float4*>(a.table + (int64_t)(known ? p : 0) * a.rot_dim) +
+                        (HALF ? (low ? u : u - half_units) * 4 : u * 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (interleaved && i >= 4) break;
-      cs[i] = known ? src[i] : make_float2(__builtin_nanf(""), __builtin_nanf(""));
+    for (int i = 0; i < kPairs / 2; ++i) {
+      const float4 w = src[i];
+      cs[4 * i] = w.x;
+      cs[4 * i + 1] = w.y;
+      cs[4 * i + 2] = w.z;
+      cs[4 * i + 3] = w.w;
     }
+#pragma unroll
+    for (int i = 0; i < 2 * kPairs; ++i) cs[i] = known ? cs[i] : __builtin_nanf("");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * kPairs; ++i) cs[i] = 0.0f;
   }
-  int64_t slot = -1;
-  if constexpr (B != 0) slot = a.slots[t];
+  int slot = -1, slots = 0;
+  if constexpr (B != 0) {
+    slot = a.slots[t];
+    slots = c.num_pages * c.page_size;
+  }
 
-  for (int n = 0; n < heads_per_thread; ++n, row += rows_per_wave) {
+#pragma unroll
+  for (int n = 0; n < H; ++n) {
+    const int row = row0 + n * rows_per_wave;
     if (row >= total) break;
     const bool is_q = B == 0 || row < a.q_heads;
     const bool is_v = B != 0 && row >= a.q_heads + c.kv_heads;
-    const int head = is_q ? row : row - a.q_heads - (is_v ? c.kv_heads : 0);
-    const uint16_t* src = is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride;
-    src += (int64_t)head * D;
-    Half8 x;
-    x.v = *reinterpret_cast<const uint4*>(src + u * 8);
     if (rotated && !is_v) {
 #pragma clang fp contract(off)
       Half8 r;
-      if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = half_value(x.b[2 * i]), q = half_value(x.b[2 * i + 1]);
-          r.b[2 * i] = __builtin_bit_cast(uint16_t, (_Float16)(p * cs[i].x - q * cs[i].y));
-          r.b[2 * i + 1] = __builtin_bit_cast(uint16_t, (_Float16)(q * cs[i].x + p * cs[i].y));
-        }
-      } else {
-        Half8 o;
-        o.v = *reinterpret_cast<const uint4*>(src + (low ? u + half_units : u - half_units) * 8);
+      if constexpr (HALF) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p = half_value(x.b[i]) * cs[i].x, q = half_value(o.b[i]) * cs[i].y;
-          r.b[i] = __builtin_bit_cast(uint16_t, (_Float16)(low ? p - q : p + q));
+          const float p = half_value(x[n].b[i]) * cs[2 * i], s = half_value(o[n].b[i]) * cs[2 * i + 1];
+          r.b[i] = __builtin_bit_cast(uint16_t, (_Float16)(p + (low ? -s : s)));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = half_value(x[n].b[2 * i]), s = half_value(x[n].b[2 * i + 1]);
+          r.b[2 * i] = __builtin_bit_cast(uint16_t, (_Float16)(p * cs[2 * i] - s * cs[2 * i + 1]));
+          r.b[2 * i + 1] = __builtin_bit_cast(uint16_t, (_Float16)(s * cs[2 * i] + p * cs[2 * i + 1]));
         }
       }
-      x = r;
+      x[n] = r;
     }
     if (is_q) {
-      *reinterpret_cast<uint4*>(a.q_out + t * a.out_stride + (int64_t)head * D + u * 8) = x.v;
+      *reinterpret_cast<uint4*>(a.q_out + t * a.out_stride + (int64_t)row * D + u * 8) = x[n].v;
     } else if constexpr (B != 0) {
-      if (slot < 0 || slot >= (int64_t)c.num_pages * c.page_size) continue;
+      if ((unsigned)slot >= (unsigned)slots) continue;
       // Row of (page, head, slot in page) in the pools.
-      const int64_t r = ((slot / c.page_size) * c.kv_heads + head) * c.page_size + slot % c.page_size;
+      const int head = row - a.q_heads - (is_v ? c.kv_heads : 0);
+      const int page = slot >> __builtin_ctz(c.page_size), place = slot & (c.page_size - 1);
+      const int64_t r = ((int64_t)page * c.kv_heads + head) * c.page_size + place;
       void* pool = is_v ? c.v : c.k;
       if constexpr (B == 16)
-        reinterpret_cast<uint4*>(pool)[r * U + u] = x.v;
+        reinterpret_cast<uint4*>(pool)[r * U + u] = x[n].v;
       else
-        encode8<B, G>(x, u, reinterpret_cast<uint32_t*>(pool) + r * (D * B / 32),
+        encode8<B, G>(x[n], u, reinterpret_cast<uint32_t*>(pool) + r * (D * B / 32),
                       (is_v ? c.v_scales : c.k_scales) + r * (D / G));
     }
   }
@@ -142,10 +173,14 @@ template <int B, int G>
 hipError_t launch(const RopeArgs& a, const qlinear_kv_cache& c, hipStream_t stream) {
   const int rows_per_group = 64 / (a.head_dim / 8) * (kThreads / 64);
   const int total = B == 0 ? a.q_heads : a.q_heads + 2 * c.kv_heads;
-  const int heads_per_thread = a.tokens >= 256 ? 4 : 1;
-  const int per = rows_per_group * heads_per_thread;
-  hipLaunchKernelGGL((rope_kernel<B, G>), dim3((unsigned)a.tokens, (unsigned)((total + per - 1) / per)),
-                     dim3(kThreads), 0, stream, a, c, heads_per_thread);
+  // Several rows a thread once there are tokens enough to fill the chip.
+  const int rows = a.tokens >= 256 ? 4 : 1;
+  const int per = rows_per_group * rows;
+  const bool half = a.layout == QLINEAR_ROPE_HALF;
+  auto kernel = rows == 4 ? (half ? rope_kernel<B, G, 4, true> : rope_kernel<B, G, 4, false>)
+                          : (half ? rope_kernel<B, G, 1, true> : rope_kernel<B, G, 1, false>);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)a.tokens, (unsigned)((total + per - 1) / per)), dim3(kThreads), 0, stream,
+                     a, c);
   return hipGetLastError();
 }
 
