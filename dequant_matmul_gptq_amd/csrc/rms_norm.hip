@@ -8,6 +8,8 @@
 // element. A row stays in registers between the sum and the scaling (up to
 // 32768 elements, kRegRow); longer rows, and rows whose length is not a
 // multiple of 8 (their 16-byte loads would not be aligned), are read again.
+#include <type_traits>
+
 #include "qlinear_kernels.hpp"
 
 namespace qlinear {
@@ -21,11 +23,24 @@ union Half8 {
   _Float16 h[8];
 };
 
-// Sum over the T threads that share a row (T == 64: one wave).
+// PAST: stores that leave no lines in the caches, which hold less than what a
+// large call writes, and then keep its inputs instead (8192 x 8192 with a
+// residual: 102.8 us with plain stores, 79.9 us; 100000 x 512: 71.7, 57.8 us).
+// What a small call writes is read from the caches next.
+template <bool PAST>
+__device__ __forceinline__ void store8(uint16_t* p, const uint4& v) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  if constexpr (PAST)
+    __builtin_nontemporal_store(__builtin_bit_cast(u4, v), reinterpret_cast<u4*>(p));
+  else
+    *reinterpret_cast<uint4*>(p) = v;
+}
+
+// Sum over the T threads that share a row (neighbours in a wave, or waves).
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
-  for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k);
+  for (int k = 1; k < (T < 64 ? T : 64); k <<= 1) v += __shfl_xor(v, k);
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -36,15 +51,15 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-// T threads a row, NC 16-byte chunks a thread; T == 64 puts four rows in a workgroup.
-template <int T, int NC>
-__global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(
+// T threads a row, NC 16-byte chunks a thread; T <= 64 puts 256 / T rows in a workgroup.
+template <int T, int NC, bool PAST>
+__global__ __launch_bounds__(T <= 64 ? 256 : T) void rms_norm_kernel(
     const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, int M, int K, float eps,
     uint16_t* y, uint16_t* residual_out) {
-  __shared__ float part[T / 64];
+  __shared__ float part[T < 64 ? 1 : T / 64];
   const int t = threadIdx.x % T;
-  const int m = T == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  if (m >= M) return;   // whole waves only (T == 64), which meet no barrier
+  const int m = T <= 64 ? blockIdx.x * (256 / T) + threadIdx.x / T : blockIdx.x;
+  if (m >= M) return;   // whole rows (T <= 64), which meet no barrier
   const int64_t row = (int64_t)m * K;
   Half8 h[NC];
   float sum = 0.0f;
@@ -59,7 +74,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[c].h[i] = (_Float16)((float)h[c].h[i] + (float)r.h[i]);
     }
-    if (residual_out) *reinterpret_cast<uint4*>(residual_out + row + k) = h[c].v;
+    if (residual_out) store8<PAST>(residual_out + row + k, h[c].v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += (float)h[c].h[i] * (float)h[c].h[i];
   }
@@ -72,7 +87,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(
     w.v = *reinterpret_cast<const uint4*>(weight + k);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[c].h[i] = (_Float16)((float)h[c].h[i] * inv * (float)w.h[i]);
-    *reinterpret_cast<uint4*>(y + row + k) = h[c].v;
+    store8<PAST>(y + row + k, h[c].v);
   }
 }
 
@@ -107,21 +122,30 @@ __global__ __launch_bounds__(256) void rms_norm_any_kernel(const uint16_t* x, co
 
 hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int M, int K,
                            float eps, uint16_t* y, uint16_t* residual_out, hipStream_t stream) {
-  auto go = [&](auto kernel, int threads, int rows) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((M + rows - 1) / rows)), dim3(threads), 0, stream, x, residual, weight,
-                       M, K, eps, y, residual_out);
-    return hipGetLastError();
-  };
   if (K % 8 != 0 || K > kRegRow) {
     hipLaunchKernelGGL(rms_norm_any_kernel, dim3((unsigned)M), dim3(256), 0, stream, x, residual, weight, K, eps, y,
                        residual_out);
     return hipGetLastError();
   }
-  if (K <= 512) return go(rms_norm_kernel<64, 1>, 256, 4);
-  if (K <= 2048) return go(rms_norm_kernel<256, 1>, 256, 1);
-  if (K <= 4096) return go(rms_norm_kernel<256, 2>, 256, 1);
-  if (K <= 8192) return go(rms_norm_kernel<256, 4>, 256, 1);
-  return go(rms_norm_kernel<1024, 4>, 1024, 1);
+  const bool past = (int64_t)M * K >= 1 << 19;      // outputs of a MiB
+  auto go = [&](auto threads, auto chunks) {
+    constexpr int T = decltype(threads)::value, NC = decltype(chunks)::value;
+    constexpr int kRows = T <= 64 ? 256 / T : 1;
+    auto kernel = past ? rms_norm_kernel<T, NC, true> : rms_norm_kernel<T, NC, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((M + kRows - 1) / kRows)), dim3(T <= 64 ? 256 : T), 0, stream, x,
+                       residual, weight, M, K, eps, y, residual_out);
+    return hipGetLastError();
+  };
+  std::integral_constant<int, 1> one;
+  std::integral_constant<int, 4> four;
+  std::integral_constant<int, 256> group;
+  if (K <= 64) return go(std::integral_constant<int, 8>{}, one);
+  if (K <= 128) return go(std::integral_constant<int, 16>{}, one);
+  if (K <= 512) return go(std::integral_constant<int, 64>{}, one);
+  if (K <= 2048) return go(group, one);
+  if (K <= 4096) return go(group, std::integral_constant<int, 2>{});
+  if (K <= 8192) return go(group, four);
+  return go(std::integral_constant<int, 1024>{}, four);
 }
 
 }  // namespace qlinear
