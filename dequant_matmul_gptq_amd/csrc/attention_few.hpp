@@ -30,6 +30,7 @@ namespace qlinear {
 namespace attn {
 
 constexpr int kFewWaves = 4;
+constexpr int kAllButVmem = 0x78F;     // what may move across a scheduling barrier
 
 // Raw registers of one step.
 template <int D, int B>
@@ -334,20 +335,24 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
   bool nonfinite = false;      // this wave's rows of join hold what infinities and NaN add
   KeyRaw<D, B> kr;
   VR vr;
-  auto row_of = [&](int t) {
-    return pool_row(c, page_of(c, table, page_shift, last_page, t), page_shift, head, t);
+  // Pool rows of a step's two tiles; their pages are looked up a step ahead.
+  int pages[2];
+  int64_t rows[2];
+  auto look_up = [&](int step) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pages[i] = page_of(c, table, page_shift, last_page, step * kStep + 16 * i);
   };
   auto keys = [&](int step) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      load_keys<D, B, ONCE>(kr, i, c, group_shift,
-                      row_of(step * kStep + 16 * i), col, g);
+    for (int i = 0; i < 2; ++i) {
+      rows[i] = pool_row(c, pages[i], page_shift, head, step * kStep + 16 * i);
+      load_keys<D, B, ONCE>(kr, i, c, group_shift, rows[i], col, g);
+    }
   };
   auto values = [&](int step) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      load_values<D, B, ONCE>(vr, i, c, group_shift,
-                        row_of(step * kStep + 16 * i), col, g);
+    for (int i = 0; i < 2; ++i) load_values<D, B, ONCE>(vr, i, c, group_shift, rows[i], col, g);
+    look_up(step + kFewWaves);
   };
 
   // One step; kind: see StepKind. False: an edge step has infinities or NaN
@@ -355,7 +360,9 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
   auto one_step = [&](auto kind, int step) __attribute__((always_inline)) -> bool {
     constexpr bool kEdge = decltype(kind)::value != kWhole, kSplit = decltype(kind)::value == kCareful;
     const int t0 = step * kStep;
-    const bool more = step + kFewWaves < end;
+    // Whole steps are never the wave's last (see below): their loads stand
+    // in no branch, which would make the waits for them whole.
+    const bool more = !kEdge || step + kFewWaves < end;
     // S^T: tile i, row 4 g + r of it in register r.
     float4v s[NT][2];
 #pragma unroll
@@ -371,6 +378,8 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
       }
     }
     if (more) keys(step + kFewWaves);
+    // Memory loads stay in this order: keys are waited for first.
+    __builtin_amdgcn_sched_barrier(kAllButVmem);
 
     half8 p[NT];
 #pragma unroll
@@ -475,6 +484,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
     }
     step = begin + wave;
     if (step < end) {
+      look_up(step);
       keys(step);
       values(step);
     }
@@ -490,7 +500,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
   const int whole_lo = (w.lo_max + kStep - 1) / kStep, whole_hi = max((w.p_min + 1) / kStep, whole_lo);
   bool done = true;
   for (int round = 0; round < 2 && done; ++round) {
-    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end));
+    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end - kFewWaves));
     done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
   }
   if (!done) {
