@@ -21,6 +21,9 @@ constexpr int kMaxRows = (1 << 22) - 1;
 // Query rows of one attention call (a workgroup of 256 threads takes 128 rows
 // of a sequence and key/value head, or fewer where a sequence ends).
 constexpr int64_t kMaxQueryRows = (int64_t)1 << 29;
+// Token slots that a call's block tables name: its steps (32 tokens, four row
+// tiles at most) are counted in 32 bits.
+constexpr int64_t kMaxTableSlots = (int64_t)1 << 33;
 
 int check_cache(const qlinear_kv_cache* c) {
   if (!c || !c->k || !c->v || c->num_pages < 1 || c->kv_heads < 1) return QLINEAR_ERR_INVALID_ARGUMENT;
@@ -174,6 +177,7 @@ int qlinear_paged_attention(const qlinear_kv_cache* cache, const uint16_t* q, in
   if (tokens == 0 || batch == 0) return QLINEAR_OK;
   if (table_width < 1 || !isfinite(scale)) return QLINEAR_ERR_INVALID_ARGUMENT;
   if (!q_start && tokens % batch != 0) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if ((int64_t)batch * table_width > kMaxTableSlots / cache->page_size) return QLINEAR_ERR_UNSUPPORTED;
   st = check_rows(q, q_stride, q_heads, cache->head_dim);
   if (st != QLINEAR_OK) return st;
   if (!kv_len || !block_table || !out) return QLINEAR_ERR_INVALID_ARGUMENT;

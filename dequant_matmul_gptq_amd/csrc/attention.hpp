@@ -32,14 +32,19 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.4028234663852886e38f;
 
-// A launch's plan: row tiles of `rows` (token, head of the group) pairs, each
-// tile's visible tokens cut into `splits` ranges of `chunk` steps (the last
-// range takes what is left). It serves the sequences whose rows per
-// key/value head number min_rows to max_rows.
+// A launch's plan. It serves the sequences whose rows per key/value head,
+// (token, head of the group) pairs, number min_rows to max_rows, in tiles of
+// `rows`.
+//   Chunk kernel: each tile's visible tokens are cut into `splits` ranges of
+//   `chunk` steps (the last range takes what is left).
+//   Few-row kernel, workers == 0: a workgroup per tile. Else the tiles' steps
+//   stand one after another, sequence by sequence, and each key/value head's
+//   `workers` workgroups take equal spans of them (see Spans).
 struct Plan {
   int rows;
   int splits;
   int chunk;
+  int workers;
   int min_rows, max_rows;
 };
 constexpr int kStep = 32;          // tokens of a step, few-row kernel
@@ -52,14 +57,14 @@ inline int64_t chunk_tiles(const AttentionArgs& a, int group) {
   return ((int64_t)a.tokens * group + (kChunkRows - 1) * (int64_t)a.batch) / kChunkRows;
 }
 
-// Partial results of a split launch, float32: o [splits][rows][D] and (m, l)
-// [splits][rows]. Rows: those of the output (chunk kernel), or `cap` for each
-// sequence and key/value head (few-row kernel, whose sequences have no more).
+// Partial results, float32: o [.][rows][D] and (m, l) [.][rows]. Chunk kernel:
+// [splits][rows of the output]. Few-row kernel: a worker's span starts and
+// ends inside a tile, and what is between are whole tiles, so a worker has two
+// partial results at most: [workers][kv_heads][2][plan.rows].
 struct Partials {
   float* o;
   float2* ml;
   int64_t rows;
-  int cap;
 };
 
 // The kernels' loops come in kinds of step: whole ones that all rows see all
@@ -164,6 +169,87 @@ __device__ __forceinline__ bool find_tile(const AttentionArgs& a, const qlinear_
     y -= __builtin_amdgcn_readlane(upto, 63);
   }
   return false;
+}
+
+// ---- the few-row kernel's spans
+// A sequence's row tiles, and the steps counted for each (from the first token
+// that its first new token sees; 1 where none sees any, for the zeros).
+struct Item {
+  int tiles, steps, first_step;
+};
+__device__ __forceinline__ Item few_item(const AttentionArgs& a, const Plan& plan, int group, const Work& w) {
+  const int rows = w.n * group;
+  Item it;
+  it.tiles = rows > plan.max_rows ? 0 : (rows + plan.rows - 1) >> __builtin_ctz(plan.rows);
+  it.first_step = first_seen(w.len - w.n, a.window) / kStep;
+  it.steps = max((w.len - 1) / kStep - it.first_step, 0) + 1;
+  return it;
+}
+// Steps of the 64 sequences from b0 on, one per lane, with their running sum.
+// (The entry point bounds the slots of all tables, so that the sums fit.)
+struct Costs {
+  int own, upto;
+};
+__device__ __forceinline__ Costs few_costs(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                           int group, int b0) {
+  const int lane = threadIdx.x & 63;
+  Costs k = {0, 0};
+  if (b0 + lane < a.batch) {
+    Work w;
+    sequence(a, c, b0 + lane, w);
+    const Item it = few_item(a, plan, group, w);
+    k.own = it.tiles * it.steps;
+  }
+  k.upto = k.own;
+#pragma unroll
+  for (int n = 1; n < 64; n <<= 1) {
+    const int o = __shfl_up(k.upto, n);
+    if (lane >= n) k.upto += o;
+  }
+  return k;
+}
+// The steps of all sequences, and each worker's: whole turns of its four
+// waves, one at least. costs: of the first 64.
+struct Spans {
+  Costs costs;
+  int total, quota;
+};
+__device__ __forceinline__ Spans few_spans(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                           int group) {
+  Spans s;
+  s.costs = few_costs(a, c, plan, group, 0);
+  s.total = __builtin_amdgcn_readlane(s.costs.upto, 63);
+  for (int b0 = 64; b0 < a.batch; b0 += 64)
+    s.total += __builtin_amdgcn_readlane(few_costs(a, c, plan, group, b0).upto, 63);
+  s.quota = (int)((((unsigned)s.total + plan.workers - 1) / (unsigned)plan.workers + 3) & ~3u);
+  return s;
+}
+// The sequence that holds step `at` (below the total), and the steps before it.
+__device__ __forceinline__ int few_find(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan, int group,
+                                        const Spans& s, int at, int& before) {
+  Costs k = s.costs;
+  before = 0;
+  for (int b0 = 0;; b0 += 64, k = few_costs(a, c, plan, group, b0)) {
+    const uint64_t past = __ballot(before + k.upto > at);
+    if (past || b0 + 64 >= a.batch) {
+      const int i = past ? __builtin_ctzll(past) : 0;
+      before += __builtin_amdgcn_readlane(k.upto - k.own, i);
+      return b0 + i;
+    }
+    before += __builtin_amdgcn_readlane(k.upto, 63);
+  }
+}
+// The steps before sequence b.
+__device__ __forceinline__ int few_before(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                          int group, const Spans& s, int b) {
+  Costs k = s.costs;
+  int before = 0;
+  for (int b0 = 0; b >= 64; b -= 64) {
+    before += __builtin_amdgcn_readlane(k.upto, 63);
+    b0 += 64;
+    k = few_costs(a, c, plan, group, b0);
+  }
+  return before + __builtin_amdgcn_readlane(k.upto - k.own, b);
 }
 
 // Lane swaps: both halves' (rows of 16 lanes', pairwise) values of x in every lane.

@@ -3,9 +3,9 @@
 // up to 16 NT (token, head of the group) pairs, are the columns of 16-wide
 // matrix-core tiles, so that the cache is read once for all of them.
 //
-// A workgroup takes a range of the sequence's tokens; its four waves take
-// steps of 32 tokens in turn, each with its own running maximum and sums,
-// and join at the end. Keys and values go from memory straight into matrix
+// A workgroup takes a span of steps of 32 tokens, of one sequence or several;
+// its four waves take steps in turn, each with its own running maximum and
+// sums, and join at the end of each sequence. Keys and values go from memory straight into matrix
 // fragments, with no LDS between:
 //   - S^T tile i (16 tokens): lane (c, g) = (l % 16, l / 16) holds key c's
 //     elements of k-group g. float16: 8 elements at 32 f + 8 g for fragment
@@ -32,14 +32,16 @@ namespace attn {
 constexpr int kFewWaves = 4;
 constexpr int kAllButVmem = 0x78F;     // what may move across a scheduling barrier
 
-// Raw registers of one step.
+// Raw registers of one step. Scales have a register each: two 16-bit values
+// that live across the loop would be packed into one where they are loaded,
+// which waits for them there.
 template <int D, int B>
 struct KeyRaw {
   static constexpr int kScales = D == 256 ? 2 : 1;
   // words of a lane's row part (D / 4 codes, or D / 32 fragments of float16)
   static constexpr int kWords = B == 16 ? D / 8 : D / 4 * B / 32;
   uint32_t w[2][kWords];
-  uint16_t s[2][kScales];
+  uint32_t s[2][kScales];
 };
 
 template <int D, int B>
@@ -48,7 +50,7 @@ struct ValueRaw {
   static constexpr int U = D / (16 * W);        // parts (128 elements apart)
   static constexpr int kWords = B == 16 ? W / 2 : B == 6 ? 2 : (W * B + 31) / 32;
   uint32_t w[8][U][kWords];
-  uint16_t s[8][U];
+  uint32_t s[8][U];
 };
 
 // A load of what this workgroup alone reads, once (ONCE): past the caches,
@@ -147,7 +149,7 @@ __device__ __forceinline__ half8 key_fragment(const KeyRaw<D, B>& k, int i, int 
 #pragma unroll
     for (int e = 0; e < 4; ++e) r[e] = k.w[i][4 * f + e];
   } else {
-    const _Float16 s = __builtin_bit_cast(_Float16, k.s[i][KeyRaw<D, B>::kScales == 1 ? 0 : f / 4]);
+    const _Float16 s = __builtin_bit_cast(_Float16, (uint16_t)k.s[i][KeyRaw<D, B>::kScales == 1 ? 0 : f / 4]);
     const half2v s2 = {s, s};
     if constexpr (B == 8) {          // 2 words, byte order
 #pragma unroll
@@ -203,7 +205,7 @@ __device__ __forceinline__ void value_fragments(const ValueRaw<D, B>& v, int u, 
         r[2 * j + 1][t] = hi_halves(a[j], b[j]);
       }
     } else {
-      const half2v s = {__builtin_bit_cast(_Float16, v.s[2 * t][u]), __builtin_bit_cast(_Float16, v.s[2 * t + 1][u])};
+      const half2v s = as_half2(lo_halves(v.s[2 * t][u], v.s[2 * t + 1][u]));
       if constexpr (B == 8) {
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -261,8 +263,8 @@ __device__ __forceinline__ void add_nonfinite(const u32x4& v, const u32x4& sees,
 }
 
 template <int D, int B, int NT, bool ONCE>
-__global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
-                                                                       Partials part) {
+__global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_few_kernel(
+    AttentionArgs a, qlinear_kv_cache c, Plan plan, Partials part) {
   typedef ValueRaw<D, B> VR;
   constexpr int W = VR::W, U = VR::U, kTiles = D / 16, kFrags = D / 32;
   constexpr int kRow = D + 4;     // LDS row of the join, in floats
@@ -272,28 +274,41 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int group = a.q_heads / c.kv_heads;
-  const int split = blockIdx.z, head = blockIdx.x % c.kv_heads, tile = blockIdx.x / c.kv_heads;
+  const int head = blockIdx.x % c.kv_heads, worker = blockIdx.x / c.kv_heads;
   const int page_shift = __builtin_ctz(c.page_size);
   const int group_shift = B == 16 ? 0 : __builtin_ctz(c.group);
 
+  // This workgroup's steps: `at` to `stop` of all, from step i0 of tile `tile`.
   Work w;
-  sequence(a, c, blockIdx.y, w);
-  const int64_t seq_rows = (int64_t)w.n * group;
-  if (tile * 16 * NT >= seq_rows || seq_rows > plan.max_rows) return;
-  row_tile(a, group, tile * 16 * NT, 16 * NT, w);
-
-  // Steps of the tile and this workgroup's share of them.
-  const int step_lo = w.lo_min / kStep;
-  const int step_end = w.p_max < 0 ? 0 : w.p_max / kStep + 1;
-  const int begin = step_lo + split * plan.chunk;
-  const int end = split == plan.splits - 1 ? step_end : min(begin + plan.chunk, step_end);
-
-  const int64_t part_row0 = ((int64_t)w.b * c.kv_heads + head) * part.cap + w.row0;
-  if (begin >= end && plan.splits > 1) {   // nothing in this range
-    for (int r = threadIdx.x; r < w.rows; r += 64 * kFewWaves)
-      part.ml[split * part.rows + part_row0 + r] = make_float2(-INFINITY, 0.0f);
-    return;
+  Item it;
+  int tile, i0 = 0, at, stop;
+  if (plan.workers == 0) {
+    sequence(a, c, blockIdx.y, w);
+    it = few_item(a, plan, group, w);
+    tile = worker;
+    if (tile >= it.tiles) return;
+    at = 0;
+    stop = it.steps;
+  } else {
+    const Spans sp = few_spans(a, c, plan, group);
+    if ((int64_t)worker * sp.quota >= sp.total) return;
+    at = worker * sp.quota;
+    stop = min(at + sp.quota, sp.total);
+    int before;
+    sequence(a, c, few_find(a, c, plan, group, sp, at, before), w);
+    it = few_item(a, plan, group, w);
+    tile = (unsigned)(at - before) / (unsigned)it.steps;
+    i0 = at - before - tile * it.steps;
   }
+  int slot = 0;                // of a partial result
+
+  for (;;) {
+  const int taken = min(it.steps - i0, stop - at);
+  const bool alone = taken == it.steps;
+  row_tile(a, group, tile * 16 * NT, 16 * NT, w);
+  const int begin = max(it.first_step + i0, w.lo_min / kStep);
+  const int end = min(it.first_step + i0 + taken, w.p_max < 0 ? 0 : w.p_max / kStep + 1);
+  const int64_t part_row0 = (((int64_t)worker * c.kv_heads + head) * 2 + slot) * (16 * NT);
 
   // Rows: column col of tile nt is row row0 + 16 nt + col of the sequence.
   int pos[NT], first[NT];
@@ -490,6 +505,10 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
     }
   };
   auto steps_to = [&](auto kind, int to) __attribute__((always_inline)) -> bool {
+    // With nothing pending at its entry (vmcnt 0, the other counters open), a
+    // loop's waits are counted from its own loads alone, and leave those of
+    // the next step in flight.
+    if (step < to) __builtin_amdgcn_s_waitcnt(0x0F70);
     for (; step < to; step += kFewWaves)
       if (!one_step(kind, step)) return false;
     return true;
@@ -546,7 +565,6 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
       const int tok = (w.row0 + rr) / group, h = head * group + (w.row0 + rr) % group;
       const int pr = w.len - w.n + tok, fr = first_seen(pr, a.window);
       const int64_t out_row = (int64_t)(w.q0 + tok) * a.q_heads + h;
-      const bool alone = plan.splits == 1;
       const float inv = pr < fr ? 0.0f : 1.0f / total;
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
@@ -563,16 +581,29 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_fe
           for (int e = 0; e < 4; ++e) y[e] = (_Float16)(pr < fr ? 0.0f : v[e] * inv);
           *reinterpret_cast<half4*>(a.out + out_row * D + d * 64 + d0) = y;
         } else {
-          *reinterpret_cast<float4v*>(part.o + (split * part.rows + part_row0 + rr) * D + d * 64 + d0) = v;
+          *reinterpret_cast<float4v*>(part.o + (part_row0 + rr) * D + d * 64 + d0) = v;
         }
       }
       if (!alone && d0 == 0) {
         // A range that the row sees part of, all of it at -infinity, is not an empty one.
         const bool sees = max(fr, begin * kStep) <= min(pr, end * kStep - 1);
-        part.ml[split * part.rows + part_row0 + rr] =
-            make_float2(top == -INFINITY && sees ? kLowest : top, total);
+        part.ml[part_row0 + rr] = make_float2(top == -INFINITY && sees ? kLowest : top, total);
       }
     }
+  }
+
+  at += taken;
+  if (at >= stop) break;
+  slot = 1;                    // a second partial result is the span's end
+  i0 = 0;
+  if (++tile == it.tiles) {
+    do {
+      sequence(a, c, w.b + 1, w);
+      it = few_item(a, plan, group, w);
+    } while (it.tiles == 0);
+    tile = 0;
+  }
+  __syncthreads();             // the join's rows have been read
   }
 }
 
@@ -582,9 +613,8 @@ hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const P
   const int group = a.q_heads / c.kv_heads;
   const int64_t most = (int64_t)a.max_q_len * group;
   const int tiles = (int)(((most < p.max_rows ? most : p.max_rows) + p.rows - 1) / p.rows);
-  // Ranges vary slowest: those past a sequence's end are then neighbours in the
-  // grid, and what work there is goes to all XCDs alike.
-  const dim3 grid((unsigned)(c.kv_heads * tiles), (unsigned)a.batch, (unsigned)p.splits);
+  const dim3 grid = p.workers ? dim3((unsigned)(c.kv_heads * p.workers))
+                              : dim3((unsigned)(c.kv_heads * tiles), (unsigned)a.batch);
   // One tile per sequence and key/value head reads each cache row once, more of
   // them share it through L2 (both sides measured, cold: 64 sequences of 2048
   // tokens, 64/8 heads, one tile 98.2 us with plain loads, 87.4 us past the

@@ -9,72 +9,98 @@ namespace {
 
 using namespace attn;
 
-// The row of a join's workgroup: FEW, row r of (key/value head, sequence) in
-// the grid's y and z; else row r of the tile and head in y. False: no such row.
-struct JoinRow {
-  int64_t out, part;     // row of the output, of the partial results
-};
+// A row of the output and its partial results.
 template <bool FEW>
-__device__ __forceinline__ bool join_row(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
-                                         const Partials& part, int r, JoinRow& j) {
+struct JoinRow {
+  int64_t out;       // row of the output
+  int parts;
+  int64_t row;       // chunk kernel: row in each range's results
+  int worker, head;  // few-row kernel: the first worker of the row's tile, ...
+  bool tail;         // ... whose span ends in the tile (its second result, if it starts before)
+  int in_tile;
+  __device__ __forceinline__ int64_t part(int i, const qlinear_kv_cache& c, const Plan& plan,
+                                          const Partials& p) const {
+    if constexpr (!FEW) return i * p.rows + row;
+    return (((int64_t)(worker + i) * c.kv_heads + head) * 2 + (i == 0 && tail ? 1 : 0)) * plan.rows + in_tile;
+  }
+};
+
+// FEW: row r of the (key/value head, sequence) in the grid's y and z; else row
+// r of the tile and head in y. False: no such row, or nothing to join.
+template <bool FEW>
+__device__ __forceinline__ bool join_row(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan, int r,
+                                         JoinRow<FEW>& j) {
   const int group = a.q_heads / c.kv_heads;
   Work w;
-  int head;
   if constexpr (FEW) {
-    head = blockIdx.y;
+    j.head = blockIdx.y;
     sequence(a, c, blockIdx.z, w);
-    const int64_t seq_rows = (int64_t)w.n * group;
-    if (r >= seq_rows || seq_rows > plan.max_rows) return false;
+    const Item it = few_item(a, plan, group, w);
+    const int tile = r >> __builtin_ctz(plan.rows);
+    if (tile >= it.tiles || r >= w.n * group) return false;
+    const Spans sp = few_spans(a, c, plan, group);
+    const unsigned start = few_before(a, c, plan, group, sp, w.b) + tile * it.steps, last = start + it.steps - 1;
+    j.worker = (int)(start / (unsigned)sp.quota);
+    j.parts = (int)(last / (unsigned)sp.quota) - j.worker + 1;
+    if (j.parts == 1) return false;      // one worker had the whole tile
+    j.tail = start > (unsigned)j.worker * sp.quota;
+    j.in_tile = r & (plan.rows - 1);
   } else {
     int tile = 0;
-    head = blockIdx.y % c.kv_heads;
+    j.head = blockIdx.y % c.kv_heads;
     if (!find_tile(a, c, plan, group, blockIdx.y / c.kv_heads, w, tile)) return false;
     r += tile * kChunkRows;
     if (r >= w.n * group) return false;
+    j.parts = plan.splits;
   }
-  j.out = (int64_t)(w.q0 + r / group) * a.q_heads + head * group + r % group;
-  j.part = FEW ? ((int64_t)w.b * c.kv_heads + head) * part.cap + r : j.out;
+  j.out = (int64_t)(w.q0 + r / group) * a.q_heads + j.head * group + r % group;
+  if constexpr (!FEW) j.row = j.out;
   return true;
 }
 
-// Joins the partial results of a split launch: o = sum_s f_s o_s / sum_s f_s
-// l_s with f_s = 2^(m_s - max m), an empty range (m = -infinity, o not
-// written) left out. Bound by the latency of its reads, so few of them wait
-// for one another. Up to kJoinFew ranges: one wave a row, all reads at once.
-constexpr int kJoinFew = 16;
+// Joins partial results: o = sum_i f_i o_i / sum_i f_i l_i with f_i =
+// 2^(m_i - max m), an empty range (m = -infinity) left out. One wave a row,
+// kJoinAtOnce results at a time in a fixed order: bound by the latency of its
+// reads, which do not wait for one another.
+constexpr int kJoinAtOnce = 16;
 template <int D, bool FEW>
-__global__ __launch_bounds__(256) void attention_join_few_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
-                                                                 Partials part) {
-  constexpr int kLanes = D / 4, kSide = 64 / kLanes;     // lanes to a range, ranges at a time
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
+                                                             Partials part) {
+  constexpr int kLanes = D / 4, kSide = 64 / kLanes;     // lanes to a result, results side by side
   const int lane = threadIdx.x & 63, side = lane / kLanes, d = lane % kLanes;
-  JoinRow row;
-  if (!join_row<FEW>(a, c, plan, part, blockIdx.x * 4 + (threadIdx.x >> 6), row)) return;
-  const int splits = plan.splits;
-  float2 ml = make_float2(-INFINITY, 0.0f);
-  if (lane < splits) ml = part.ml[lane * part.rows + row.part];
-  const float4v* p = reinterpret_cast<const float4v*>(part.o) + row.part * kLanes + d;
-  float4v x[kJoinFew / kSide];
-#pragma unroll
-  for (int i = 0; i < kJoinFew / kSide; ++i) {
-    const int s = i * kSide + side;
-    x[i] = p[(s < splits ? s : 0) * part.rows * kLanes];
-  }
-  float top = ml.x;
-#pragma unroll
-  for (int k = 1; k < kJoinFew; k <<= 1) top = fmaxf(top, __shfl_xor(top, k, kJoinFew));
-  top = __shfl(top, 0);
-  const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-  float total = f * ml.y;
-#pragma unroll
-  for (int k = 1; k < kJoinFew; k <<= 1) total += __shfl_xor(total, k, kJoinFew);
-  total = __shfl(total, 0);
+  JoinRow<FEW> row;
+  if (!join_row<FEW>(a, c, plan, blockIdx.x * 4 + (threadIdx.x >> 6), row)) return;
+  float top = -INFINITY, total = 0.0f;
   float4v o = {0, 0, 0, 0};
+  for (int i0 = 0; i0 < row.parts; i0 += kJoinAtOnce) {
+    const int n = min(kJoinAtOnce, row.parts - i0);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < n) ml = part.ml[row.part(i0 + lane, c, plan, part)];
+    float4v x[kJoinAtOnce / kSide];
 #pragma unroll
-  for (int i = 0; i < kJoinFew / kSide; ++i) {
-    const int s = i * kSide + side;
-    const float fs = __shfl(f, s), ms = __shfl(ml.x, s);
+    for (int k = 0; k < kJoinAtOnce / kSide; ++k) {
+      const int i = k * kSide + side;
+      x[k] = reinterpret_cast<const float4v*>(part.o)[row.part(i0 + (i < n ? i : 0), c, plan, part) * kLanes + d];
+    }
+    float most = ml.x;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += ms == -INFINITY ? 0.0f : fs * x[i][e];
+    for (int k = 1; k < kJoinAtOnce; k <<= 1) most = fmaxf(most, __shfl_xor(most, k, kJoinAtOnce));
+    most = fmaxf(top, __shfl(most, 0));
+    const float keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - most);
+    const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - most);
+    top = most;
+    float sum = f * ml.y;
+#pragma unroll
+    for (int k = 1; k < kJoinAtOnce; k <<= 1) sum += __shfl_xor(sum, k, kJoinAtOnce);
+    total = total * keep + __shfl(sum, 0);
+    o *= keep;
+#pragma unroll
+    for (int k = 0; k < kJoinAtOnce / kSide; ++k) {
+      const int i = k * kSide + side;
+      const float fi = __shfl(f, i), mi = __shfl(ml.x, i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += mi == -INFINITY ? 0.0f : fi * x[k][e];
+    }
   }
 #pragma unroll
   for (int k = kLanes; k < 64; k <<= 1)
@@ -87,82 +113,20 @@ __global__ __launch_bounds__(256) void attention_join_few_kernel(AttentionArgs a
   *reinterpret_cast<half4*>(a.out + row.out * D + 4 * d) = y;
 }
 
-// More ranges: a workgroup a row, the weights kJoinBatch at a time in LDS,
-// then D / 4 threads to a range and several loads in flight. Threads and
-// ranges are added in a fixed order.
-constexpr int kJoinBatch = 256;
-template <int D, bool FEW>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
-                                                             Partials part) {
-  constexpr int kSide = 256 / (D / 4);    // ranges at a time
-  __shared__ float weight[kJoinBatch];
-  __shared__ float tops[4], sums[4];
-  __shared__ float4v o_part[kSide][D / 4];
-  JoinRow at;
-  if (!join_row<FEW>(a, c, plan, part, blockIdx.x, at)) return;
-  const int64_t row = at.part, rows = part.rows;
-  const int splits = plan.splits;
-  const int t = threadIdx.x, side = t / (D / 4), d = t % (D / 4);
-  float top = -INFINITY;
-  for (int s = t; s < splits; s += 256) top = fmaxf(top, part.ml[s * rows + row].x);
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
-  if ((t & 63) == 0) tops[t >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-
-  float total = 0.0f;
-  float4v o = {0, 0, 0, 0};
-  for (int s0 = 0; s0 < splits; s0 += kJoinBatch) {
-    const int n = min(kJoinBatch, splits - s0);
-    if (s0) __syncthreads();
-    if (t < n) {
-      const float2 ml = part.ml[(s0 + t) * rows + row];
-      const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-      weight[t] = ml.x == -INFINITY ? -1.0f : f;       // -1: left out
-      total += f * ml.y;
-    }
-    __syncthreads();
-    const float4v* p = reinterpret_cast<const float4v*>(part.o) + (s0 * rows + row) * (D / 4) + d;
-#pragma unroll 4
-    for (int s = side; s < n; s += kSide) {
-      const float f = weight[s];
-      if (f >= 0.0f || f != f) o += f * p[s * rows * (D / 4)];
-    }
-  }
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k);
-  if ((t & 63) == 0) sums[t >> 6] = total;
-  o_part[side][d] = o;
-  __syncthreads();
-  if (side != 0) return;
-  total = sums[0] + sums[1] + sums[2] + sums[3];
-#pragma unroll
-  for (int i = 1; i < kSide; ++i) o += o_part[i][d];
-  half4 y;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = (_Float16)(top == -INFINITY ? 0.0f : o[e] / total);
-  *reinterpret_cast<half4*>(a.out + at.out * D + 4 * d) = y;
-}
-
-template <int D, bool FEW>
-hipError_t launch_join_width(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
-                             int rows, dim3 grid, hipStream_t stream) {
-  const bool few = p.splits <= kJoinFew;
-  grid.x = (unsigned)(few ? (rows + 3) / 4 : rows);
-  auto kernel = few ? attention_join_few_kernel<D, FEW> : attention_join_kernel<D, FEW>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, c, p, part);
-  return hipGetLastError();
-}
-
 // `rows` rows for each place of the grid's y and z.
 template <bool FEW>
 hipError_t launch_join(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
                        int rows, dim3 grid, hipStream_t stream) {
-  if (c.head_dim == 64) return launch_join_width<64, FEW>(c, a, p, part, rows, grid, stream);
-  if (c.head_dim == 128) return launch_join_width<128, FEW>(c, a, p, part, rows, grid, stream);
-  return launch_join_width<256, FEW>(c, a, p, part, rows, grid, stream);
+  grid.x = (unsigned)((rows + 3) / 4);
+  auto kernel = c.head_dim == 64    ? attention_join_kernel<64, FEW>
+                : c.head_dim == 128 ? attention_join_kernel<128, FEW>
+                                    : attention_join_kernel<256, FEW>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, c, p, part);
+  return hipGetLastError();
 }
+
+// Up to this many steps a workgroup takes a tile whole, and nothing is joined.
+constexpr int kWholeSteps = 8;
 
 // Steps of `tokens` tokens that a row tile spans at most.
 int64_t plan_steps(const AttentionArgs& a, int tokens) {
@@ -193,24 +157,16 @@ Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
     p.rows = r.few_cap <= 16 || c.head_dim == 256 ? 16 : 32;
     p.min_rows = 1;
     p.max_rows = kFewRows;
-    p.splits = 1;
-    p.chunk = INT32_MAX;
-    const int64_t tiles = (int64_t)(r.few_cap + p.rows - 1) / p.rows * c.kv_heads * a.batch;
+    const int64_t tiles = (int64_t)(r.few_cap + p.rows - 1) / p.rows * a.batch;
     const int64_t steps = plan_steps(a, kStep);
-    // Ranges for two workgroups per CU (what their registers allow), of 4 to
-    // 64 steps: shorter ones cost more in partial results than they spread
-    // (64 sequences of 2048 tokens, 64/8 heads: 96.8 us whole, 102.6, 107, 123
-    // us in ranges of 64, 16, 4 steps), longer ones leave CUs idle at the end
-    // (one of 32768: 31.0, 31.1, 40.1 us in ranges of 16, 64, 96).
-    int64_t chunk = (tiles * steps + 511) / 512;
-    if (chunk < 4) chunk = 4;
-    if (chunk > 64) chunk = 64;
-    if (getenv("QL_CHUNK")) chunk = atoi(getenv("QL_CHUNK"));
-    p.splits = (int)((steps + chunk - 1) / chunk);
-    if (p.splits < 1) p.splits = 1;
-    if (p.splits > 1) {
-      p.chunk = (int)chunk;
-      r.few_rows = (int64_t)a.batch * c.kv_heads * r.few_cap;
+    if (steps > kWholeSteps) {
+      // As many workgroups as the chip holds at once, two to a CU by their
+      // registers (one for 256 wide heads), of four steps at least.
+      int64_t workers = (c.head_dim == 256 ? 256 : 512) / c.kv_heads;
+      const int64_t quarter = (tiles * steps + 3) / 4;
+      if (workers > quarter) workers = quarter;
+      p.workers = workers > 1 ? (int)workers : 1;
+      r.few_rows = (int64_t)p.workers * c.kv_heads * 2 * p.rows;
     }
   }
   if (r.chunk) {
@@ -235,15 +191,15 @@ Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
   return r;
 }
 
-size_t partial_bytes(const Plan& p, int64_t rows, int D) { return (size_t)p.splits * rows * (D + 2) * sizeof(float); }
+// `ranges` results of `rows` rows each.
+size_t partial_bytes(int64_t ranges, int64_t rows, int D) { return (size_t)(ranges * rows * (D + 2)) * sizeof(float); }
 
-Partials partials(void* ws, const Plan& p, int64_t rows, int cap, int D) {
+Partials partials(void* ws, int64_t ranges, int64_t rows, int D) {
   Partials part = {};
   if (rows == 0) return part;
   part.o = (float*)ws;
-  part.ml = (float2*)(part.o + (int64_t)p.splits * rows * D);
+  part.ml = (float2*)(part.o + ranges * rows * D);
   part.rows = rows;
-  part.cap = cap;
   return part;
 }
 
@@ -252,8 +208,8 @@ Partials partials(void* ws, const Plan& p, int64_t rows, int cap, int D) {
 // The two kernels' launches follow one another on the stream and share the workspace.
 size_t paged_attention_workspace_bytes(const qlinear_kv_cache& cache, const AttentionArgs& a) {
   const Route r = make_route(cache, a);
-  const size_t few = partial_bytes(r.few_plan, r.few_rows, cache.head_dim);
-  const size_t chunk = partial_bytes(r.chunk_plan, r.chunk_rows, cache.head_dim);
+  const size_t few = partial_bytes(1, r.few_rows, cache.head_dim);
+  const size_t chunk = partial_bytes(r.chunk_plan.splits, r.chunk_rows, cache.head_dim);
   return few > chunk ? few : chunk;
 }
 
@@ -263,7 +219,7 @@ hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const Attention
   const int D = cache.head_dim, group = a.q_heads / cache.kv_heads;
   if (r.chunk) {
     const Plan& p = r.chunk_plan;
-    const Partials part = partials(ws, p, r.chunk_rows, 0, D);
+    const Partials part = partials(ws, p.splits, r.chunk_rows, D);
     const hipError_t e = D == 64    ? launch_attention_chunk_64(cache, a, p, part, stream)
                          : D == 128 ? launch_attention_chunk_128(cache, a, p, part, stream)
                                     : launch_attention_chunk_256(cache, a, p, part, stream);
@@ -278,7 +234,7 @@ hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const Attention
   // Without q_start all sequences have the same length.
   if (r.few && (!r.chunk || a.q_start || (int64_t)(a.tokens / a.batch) * group <= kFewRows)) {
     const Plan& p = r.few_plan;
-    const Partials part = partials(ws, p, r.few_rows, r.few_cap, D);
+    const Partials part = partials(ws, 1, r.few_rows, D);
     const hipError_t e = D == 64    ? launch_attention_few_64(cache, a, p, part, stream)
                          : D == 128 ? launch_attention_few_128(cache, a, p, part, stream)
                                     : launch_attention_few_256(cache, a, p, part, stream);

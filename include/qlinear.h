@@ -510,7 +510,7 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
  * < 1, q_stride < q_heads * head_dim, tokens % batch without q_start, a scale
  * that is not finite), UNSUPPORTED (q_heads not a multiple of kv_heads,
  * q_heads > 65535, batch > 65535, q_stride % 8 != 0, tokens * q_heads > 2^29,
- * batch * kv_heads > 2^22), MISALIGNED (q, out, workspace 16 bytes; the int32 arrays
+ * batch * kv_heads > 2^22, batch * table_width * page_size > 2^33), MISALIGNED (q, out, workspace 16 bytes; the int32 arrays
  * 4), WORKSPACE.
  */
 int qlinear_paged_attention_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,
