@@ -217,8 +217,16 @@ struct Spans {
 __device__ __forceinline__ Spans few_spans(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
                                            int group) {
   Spans s;
-  s.costs = few_costs(a, c, plan, group, 0);
-  s.total = __builtin_amdgcn_readlane(s.costs.upto, 63);
+  if (a.batch == 1) {      // no lane work on the way to the first load
+    Work w;
+    sequence(a, c, 0, w);
+    const Item it = few_item(a, plan, group, w);
+    s.costs.own = s.costs.upto = it.tiles * it.steps;
+    s.total = __builtin_amdgcn_readfirstlane(s.costs.upto);
+  } else {
+    s.costs = few_costs(a, c, plan, group, 0);
+    s.total = __builtin_amdgcn_readlane(s.costs.upto, 63);
+  }
   for (int b0 = 64; b0 < a.batch; b0 += 64)
     s.total += __builtin_amdgcn_readlane(few_costs(a, c, plan, group, b0).upto, 63);
   s.quota = (int)((((unsigned)s.total + plan.workers - 1) / (unsigned)plan.workers + 3) & ~3u);

@@ -1,6 +1,9 @@
 // Attention over a paged cache: the launch plan, the join of split calls, and
 // the choice between the two kernels (attention_few.hpp, attention_chunk.hpp).
 #include <stdlib.h>
+
+#include <type_traits>
+
 #include "attention.hpp"
 
 namespace qlinear {
@@ -59,20 +62,23 @@ __device__ __forceinline__ bool join_row(const AttentionArgs& a, const qlinear_k
 }
 
 // Joins partial results: o = sum_i f_i o_i / sum_i f_i l_i with f_i =
-// 2^(m_i - max m), an empty range (m = -infinity) left out. One wave a row,
-// kJoinAtOnce results at a time in a fixed order: bound by the latency of its
-// reads, which do not wait for one another.
+// 2^(m_i - max m), an empty range (m = -infinity) left out. A wave takes
+// kJoinAtOnce results at a time: bound by the latency of its reads, which do
+// not wait for one another. WAVES waves to a row take turns, and their sums are
+// joined the same way; all in a fixed order.
 constexpr int kJoinAtOnce = 16;
-template <int D, bool FEW>
+template <int D, bool FEW, int WAVES>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, qlinear_kv_cache c, Plan plan,
                                                              Partials part) {
   constexpr int kLanes = D / 4, kSide = 64 / kLanes;     // lanes to a result, results side by side
-  const int lane = threadIdx.x & 63, side = lane / kLanes, d = lane % kLanes;
+  __shared__ float4v o_all[4][kLanes];
+  __shared__ float2 ml_all[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, side = lane / kLanes, d = lane % kLanes;
   JoinRow<FEW> row;
-  if (!join_row<FEW>(a, c, plan, blockIdx.x * 4 + (threadIdx.x >> 6), row)) return;
+  if (!join_row<FEW>(a, c, plan, blockIdx.x * (4 / WAVES) + wave / WAVES, row)) return;
   float top = -INFINITY, total = 0.0f;
   float4v o = {0, 0, 0, 0};
-  for (int i0 = 0; i0 < row.parts; i0 += kJoinAtOnce) {
+  for (int i0 = wave % WAVES * kJoinAtOnce; i0 < row.parts; i0 += WAVES * kJoinAtOnce) {
     const int n = min(kJoinAtOnce, row.parts - i0);
     float2 ml = make_float2(-INFINITY, 0.0f);
     if (lane < n) ml = part.ml[row.part(i0 + lane, c, plan, part)];
@@ -106,6 +112,22 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, ql
   for (int k = kLanes; k < 64; k <<= 1)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], k);
+  if constexpr (WAVES > 1) {     // the whole workgroup is on one row
+    if (side == 0) o_all[wave][d] = o;
+    if (lane == 0) ml_all[wave] = make_float2(top, total);
+    __syncthreads();
+    if (wave != 0) return;
+    top = fmaxf(fmaxf(ml_all[0].x, ml_all[1].x), fmaxf(ml_all[2].x, ml_all[3].x));
+    total = 0.0f;
+    o = float4v{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (ml_all[i].x == -INFINITY) continue;
+      const float f = __builtin_amdgcn_exp2f(ml_all[i].x - top);
+      total += f * ml_all[i].y;
+      o += f * o_all[i][d];
+    }
+  }
   if (side != 0) return;
   half4 y;
 #pragma unroll
@@ -113,16 +135,24 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, ql
   *reinterpret_cast<half4*>(a.out + row.out * D + 4 * d) = y;
 }
 
-// `rows` rows for each place of the grid's y and z.
+// `rows` rows for each place of the grid's y and z, of about `parts` results.
 template <bool FEW>
 hipError_t launch_join(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
-                       int rows, dim3 grid, hipStream_t stream) {
-  grid.x = (unsigned)((rows + 3) / 4);
-  auto kernel = c.head_dim == 64    ? attention_join_kernel<64, FEW>
-                : c.head_dim == 128 ? attention_join_kernel<128, FEW>
-                                    : attention_join_kernel<256, FEW>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, c, p, part);
-  return hipGetLastError();
+                       int rows, dim3 grid, int64_t parts, hipStream_t stream) {
+  auto go = [&](auto kernel, int waves) {
+    grid.x = (unsigned)((rows * waves + 3) / 4);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, c, p, part);
+    return hipGetLastError();
+  };
+  auto width = [&](auto waves) {
+    constexpr int W = decltype(waves)::value;
+    if (c.head_dim == 64) return go(attention_join_kernel<64, FEW, W>, W);
+    if (c.head_dim == 128) return go(attention_join_kernel<128, FEW, W>, W);
+    return go(attention_join_kernel<256, FEW, W>, W);
+  };
+  // Four waves to a row if one would make several turns (64 results: 10.2 us
+  // with one wave, 5.1 us with four).
+  return parts > kJoinAtOnce ? width(std::integral_constant<int, 4>{}) : width(std::integral_constant<int, 1>{});
 }
 
 // Up to this many steps a workgroup takes a tile whole, and nothing is joined.
@@ -227,7 +257,7 @@ hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const Attention
     if (r.chunk_rows > 0) {
       // Splitting needs few workgroups, so the grid's y holds them.
       const hipError_t j = launch_join<false>(cache, a, p, part, kChunkRows,
-                                              dim3(1, (unsigned)(chunk_tiles(a, group) * cache.kv_heads)), stream);
+                                              dim3(1, (unsigned)(chunk_tiles(a, group) * cache.kv_heads)), p.splits, stream);
       if (j != hipSuccess) return j;
     }
   }
@@ -241,7 +271,7 @@ hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const Attention
     if (e != hipSuccess) return e;
     if (r.few_rows > 0)
       return launch_join<true>(cache, a, p, part, r.few_cap,
-                               dim3(1, (unsigned)cache.kv_heads, (unsigned)a.batch), stream);
+                               dim3(1, (unsigned)cache.kv_heads, (unsigned)a.batch), p.workers / a.batch, stream);
   }
   return hipSuccess;
 }
