@@ -52,6 +52,16 @@ constexpr int kChunkRows = 128;    // rows of a tile, chunk kernel
 constexpr int kFewRows = 64;       // most rows of a sequence per key/value head in the few-row kernel
 __host__ __device__ constexpr int chunk_step(int D) { return D == 256 ? 32 : 64; }   // tokens of its step
 
+// Workgroups of the few-row kernel that a CU holds, by their registers: one of
+// 256 wide heads or of 32 rows by 128, else two. With codes two of 32 by 128 are
+// taken as well: they spill outside the loop of whole steps, and the unpacking
+// wants the waves (8 sequences of 8192 tokens, 64/8 heads, 7 new tokens each, in
+// us with one and two: float16 68 and 79, Q8 72 and 62, Q6 82 and 70, Q4 71 and
+// 60; 4 new tokens: float16 53 and 70, Q8 44 and 49, Q6 50 and 51).
+constexpr int few_per_cu(int head_dim, int rows, int bits) {
+  return head_dim == 256 || (head_dim == 128 && rows == 32 && bits == 16) ? 1 : 2;
+}
+
 // Row tiles of the chunk kernel, at most, whatever the sequences' lengths.
 inline int64_t chunk_tiles(const AttentionArgs& a, int group) {
   return ((int64_t)a.tokens * group + (kChunkRows - 1) * (int64_t)a.batch) / kChunkRows;

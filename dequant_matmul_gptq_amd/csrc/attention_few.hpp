@@ -263,7 +263,7 @@ __device__ __forceinline__ void add_nonfinite(const u32x4& v, const u32x4& sees,
 }
 
 template <int D, int B, int NT, bool ONCE>
-__global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attention_few_kernel(
+__global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void attention_few_kernel(
     AttentionArgs a, qlinear_kv_cache c, Plan plan, Partials part) {
   typedef ValueRaw<D, B> VR;
   constexpr int W = VR::W, U = VR::U, kTiles = D / 16, kFrags = D / 32;
@@ -618,7 +618,7 @@ hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const P
   // One tile per sequence and key/value head reads each cache row once, more of
   // them share it through L2 (both sides measured, cold: 64 sequences of 2048
   // tokens, 64/8 heads, one tile 98.2 us with plain loads, 87.4 us past the
-  // caches; 8 of 8192 with 7 drafts each, two tiles, 72.2 and 86.1 us).
+  // caches; 8 of 8192 with 7 new tokens each, two tiles, 69.3 and 76.7 us).
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kFewWaves), 0, stream, a, c, p, part);
     return hipGetLastError();

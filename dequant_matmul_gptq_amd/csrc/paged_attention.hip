@@ -1,7 +1,5 @@
 // Attention over a paged cache: the launch plan, the join of split calls, and
 // the choice between the two kernels (attention_few.hpp, attention_chunk.hpp).
-#include <stdlib.h>
-
 #include <type_traits>
 
 #include "attention.hpp"
@@ -190,9 +188,8 @@ Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
     const int64_t tiles = (int64_t)(r.few_cap + p.rows - 1) / p.rows * a.batch;
     const int64_t steps = plan_steps(a, kStep);
     if (steps > kWholeSteps) {
-      // As many workgroups as the chip holds at once, two to a CU by their
-      // registers (one for 256 wide heads), of four steps at least.
-      int64_t workers = (c.head_dim == 256 ? 256 : 512) / c.kv_heads;
+      // As many workgroups as the chip holds at once, of four steps at least.
+      int64_t workers = 256 * few_per_cu(c.head_dim, p.rows, c.bits) / c.kv_heads;
       const int64_t quarter = (tiles * steps + 3) / 4;
       if (workers > quarter) workers = quarter;
       p.workers = workers > 1 ? (int)workers : 1;
@@ -211,7 +208,6 @@ Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
     const int64_t steps = plan_steps(a, chunk_step(c.head_dim));
     int64_t splits = 512 / groups;
     if (splits > steps / 8) splits = steps / 8;
-    if (getenv("QL_SPLITS")) splits = atoi(getenv("QL_SPLITS"));
     if (splits > 1) {
       p.chunk = (int)((steps + splits - 1) / splits);
       p.splits = (int)((steps + p.chunk - 1) / p.chunk);
