@@ -348,3 +348,19 @@ def test_oracle_rms_norm_pins():
     assert np.allclose(y, [[3 / r, 8 / r]]) and h.dtype == np.float16
     y, h = od.rms_norm(np.array([[2.0, 5.0]]), np.array([1.0, 2.0]), 0.0, np.array([[1.0, -1.0]]))
     assert np.allclose(y, [[3 / r, 8 / r]]) and h.tolist() == [[3.0, 4.0]]
+
+
+@pytest.mark.parametrize("cache,change", [
+    (dict(kv_heads=4097), dict(q_heads=4097, q_stride=4097 * 128)),
+    ({}, dict(tokens=(1 << 26) + 1)),                                  # tokens * q_heads past 2^29
+    (dict(kv_heads=128), dict(q_heads=128, q_stride=128 * 128, batch=32769)),   # batch * kv_heads past 2^22
+    ({}, dict(batch=8193, table_width=32768))])                        # slots of all tables past 2^33
+def test_attention_refuses_what_its_indexes_cannot_hold(cache, change):
+    assert _attention(cache=_cache(**cache), **change) == UNS
+
+
+@pytest.mark.parametrize("change", [dict(M=1 << 22), dict(K=(1 << 24) + 8)])
+def test_rms_norm_refuses_what_its_indexes_cannot_hold(change):
+    a = dict(x=FAKE, residual=None, weight=FAKE, M=1, K=64, eps=1e-5, out=FAKE, residual_out=None)
+    a.update(change)
+    assert dq.lib().qlinear_rms_norm(*a.values(), None) == UNS

@@ -348,3 +348,89 @@ def test_binding_refuses_wrong_tensors():
     assert e.value.status == dq._lib.ERR_UNSUPPORTED
     with pytest.raises(dq.QlinearError):
         dq.paged_attention(b.cache, q, table, kv, scale=float("inf"))
+
+
+@pytest.mark.parametrize("bits,group,D,Hq,Hk", [(16, 64, 64, 8, 2), (4, 32, 64, 4, 4), (8, 64, 128, 8, 1),
+                                                (16, 64, 256, 4, 2)])
+def test_more_sequences_than_lanes(bits, group, D, Hq, Hk):
+    """Batches past 64 and 128 sequences of all kinds: without new tokens,
+    without cached ones, with few rows and with many."""
+    say(f"attention many sequences bits={bits} D={D}")
+    rng = np.random.default_rng(bits + D)
+    for B in (64, 65, 150):
+        n = rng.choice([0, 1, 1, 1, 2, 5], B)
+        L = np.where(rng.random(B) < 0.1, 0, n + rng.integers(0, 90, B))
+        n[B - 1], L[B - 1] = 1, 700
+        n[3], L[3] = 40, 333
+        n[B // 2], L[B // 2] = 2, 450
+        b = Batch(Hq, Hk, D, 16, bits, group, n, L, seed=B)
+        b.check(b.run(), what=f"B={B}")
+        b.check(b.run(window=40, max_kv_len=700), window=40, what=f"B={B}")
+
+
+@pytest.mark.parametrize("where", (0, 63, 64, 129))
+def test_one_long_sequence_among_short_ones(where):
+    """Its steps are shared out over workgroups that also have whole sequences."""
+    say(f"attention one long at {where}")
+    for lens, n in ((1, 1), (40, 1), (0, 1), (9, 3)):
+        L = [lens] * 130
+        L[where] = 6000
+        b = Batch(4, 2, 64, 64, 16, 64, [n] * 130, L, seed=where)
+        b.check(b.run(), what=f"lens={lens}")
+
+
+@pytest.mark.parametrize("D,bits", [(64, 16), (128, 16), (128, 4), (256, 8)])
+def test_drafts_over_long_caches(D, bits):
+    """One to four row tiles per sequence, lengths off the step, tile and span edges."""
+    say(f"attention drafts D={D} bits={bits}")
+    for Hq, n in ((8, 2), (8, 3), (8, 4), (8, 5), (8, 8), (16, 4), (5, 7)):
+        b = Batch(Hq, 1, D, 32, bits, 64, [n] * 5, [2049, 700, 3001, n, 1500], seed=Hq + n)
+        b.check(b.run(), what=f"{Hq} heads, {n} tokens")
+        b.check(b.run(window=900), window=900, what=f"{Hq} heads, {n} tokens")
+
+
+@pytest.mark.parametrize("n", (1, 6, 130))
+@pytest.mark.parametrize("bits", (8, 6, 4))
+def test_unseen_quantized_nan_stays_out(n, bits):
+    """A quantized row of NaN has a NaN scale: the rows that see it are NaN, the others untouched."""
+    say(f"attention NaN scales n={n} bits={bits}")
+    window = 50
+    b = Batch(4, 2, 128, 32, bits, 32, [n], [n + 400], seed=n + bits)
+    hidden, last = 400 - window + 1, n + 399       # the first is seen by row 0 alone, one more by none
+    for t in (hidden - 1, hidden, last):
+        b.k[0][t] = b.v[0][t] = np.nan
+    b.fill()
+    o = b.run(window=window)
+    for i in range(n):
+        p = 400 + i
+        lo = p - window + 1
+        if lo <= hidden or p == last:
+            assert np.isnan(o[i]).all(), i
+            continue
+        ref, w, _ = oracle.decoder.attention(b.q[0][i:i + 1], b.kv[0][0][lo:p + 1], b.kv[1][0][lo:p + 1], 128 ** -0.5)
+        bound = 2.0 ** -11 * np.abs(ref[0]) + (2.0 ** -11 + 2.0 ** -12) * w[0] + 2.0 ** -25 * (1 + (p + 1) * 5)
+        assert np.isfinite(o[i]).all() and (np.abs(o[i] - ref[0]) <= bound).all(), i
+
+
+@pytest.mark.parametrize("n", (1, 100))
+def test_pools_past_32_bit_offsets(n):
+    """Appended to, copied within and read from pages that lie more than 2^32 bytes and elements into a pool."""
+    say(f"attention large pool n={n}")
+    dev = device()
+    D, P, Hk, pages = 128, 64, 2, 270000       # 2^32 elements of a pool are 262144 pages
+    cache = dq.KVCache.empty(pages, Hk, D, page_size=P)
+    rng = np.random.default_rng(n)
+    L = 150
+    q, k, v = (rng.standard_normal((m, h, D)).astype(np.float16) for m, h in ((n, 4), (L, Hk), (L, Hk)))
+    held, first = [269999, 131073, 262145], [269990, 131070, 262140]
+    slots = [first[t // P] * P + t % P for t in range(L)]
+    dq.rope_append(cache, None, torch.from_numpy(k).to(dev), torch.from_numpy(v).to(dev), None,
+                   torch.tensor(slots, dtype=torch.int32, device=dev), None)
+    dq.copy_pages([cache], torch.tensor(list(zip(first, held)), dtype=torch.int32, device=dev))
+    o = dq.paged_attention(cache, torch.from_numpy(q).to(dev), torch.tensor([held], dtype=torch.int32, device=dev),
+                           torch.tensor([L], dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    ref, w, total = oracle.decoder.attention(q, k.astype(np.float64), v.astype(np.float64), D ** -0.5)
+    err = np.abs(o.double().cpu().numpy() - ref)
+    tiny = L * np.abs(v).max() / np.maximum(total, 1.0)
+    assert (err <= 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * w + 2.0 ** -25 * (1 + tiny[..., None])).all()
