@@ -39,12 +39,14 @@ constexpr float kLowest = -3.4028234663852886e38f;
 //   `chunk` steps (the last range takes what is left).
 //   Few-row kernel, workers == 0: a workgroup per tile. Else the tiles' steps
 //   stand one after another, sequence by sequence, and each key/value head's
-//   `workers` workgroups take equal spans of them (see Spans).
+//   `workers` workgroups take equal spans of them (see Spans), or whole tiles
+//   as well, if the launch has `whole` of them for each sequence (0: it has
+//   not). `slots`: workgroups of a head that the chip holds at once.
 struct Plan {
   int rows;
   int splits;
   int chunk;
-  int workers;
+  int workers, slots, whole;
   int min_rows, max_rows;
 };
 constexpr int kStep = 32;          // tokens of a step, few-row kernel
@@ -58,7 +60,7 @@ __host__ __device__ constexpr int chunk_step(int D) { return D == 256 ? 32 : 64;
 // wants the waves (8 sequences of 8192 tokens, 64/8 heads, 7 new tokens each, in
 // us with one and two: float16 68 and 79, Q8 72 and 62, Q6 82 and 70, Q4 71 and
 // 60; 4 new tokens: float16 53 and 70, Q8 44 and 49, Q6 50 and 51).
-constexpr int few_per_cu(int head_dim, int rows, int bits) {
+__host__ __device__ constexpr int few_per_cu(int head_dim, int rows, int bits) {
   return head_dim == 256 || (head_dim == 128 && rows == 32 && bits == 16) ? 1 : 2;
 }
 
@@ -199,18 +201,32 @@ __device__ __forceinline__ Item few_item(const AttentionArgs& a, const Plan& pla
 // (The entry point bounds the slots of all tables, so that the sums fit.)
 struct Costs {
   int own, upto;
+  int q0, n, len, tiles, steps;     // the lane's sequence, each of its tiles' steps
+  // Sequence b, from the lane that holds it.
+  __device__ __forceinline__ void get(int b, Work& w) const {
+    w.b = b;
+    w.q0 = __builtin_amdgcn_readlane(q0, b & 63);
+    w.n = __builtin_amdgcn_readlane(n, b & 63);
+    w.len = __builtin_amdgcn_readlane(len, b & 63);
+  }
+  __device__ __forceinline__ void set(const Work& w, const Item& it) {
+    q0 = w.q0;
+    n = w.n;
+    len = w.len;
+    tiles = it.tiles;
+    steps = it.tiles > 0 ? it.steps : 0;
+    own = upto = it.tiles * it.steps;
+  }
 };
 __device__ __forceinline__ Costs few_costs(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
                                            int group, int b0) {
   const int lane = threadIdx.x & 63;
-  Costs k = {0, 0};
+  Costs k = {};
   if (b0 + lane < a.batch) {
     Work w;
     sequence(a, c, b0 + lane, w);
-    const Item it = few_item(a, plan, group, w);
-    k.own = it.tiles * it.steps;
+    k.set(w, few_item(a, plan, group, w));
   }
-  k.upto = k.own;
 #pragma unroll
   for (int n = 1; n < 64; n <<= 1) {
     const int o = __shfl_up(k.upto, n);
@@ -220,31 +236,64 @@ __device__ __forceinline__ Costs few_costs(const AttentionArgs& a, const qlinear
 }
 // The steps of all sequences, and each worker's: whole turns of its four
 // waves, one at least. costs: of the first 64.
+//
+// whole: every workgroup takes one tile, and nothing is joined. A span that
+// cuts tiles pays for its second start and the join, about as much as 13 steps
+// of a lone workgroup; a whole tile's workgroup pays by being the last one. A
+// full chip's step takes about 1.25 times a lone workgroup's for each one that
+// a CU holds, a partly full one's less in proportion. So tiles are taken whole
+// if the longest, at the load of all of them, is done within 13 lone steps of
+// what the spans take. Both sides measured, us, spans and whole, 64/8 heads of
+// 128: float16: 16 sequences of 700 tokens 22.1 and 19.6, of 2100 36.1 and 40.9;
+// 64 of 1100 59.9 and 52.9; 48 of 1 to 4000 73.3 and 114; Q4: 64 of 1100 38.3 and
+// 28.8, of 2100 54.8 and 45.6, 128 of 1100 66.9 and 56.8, of 700 42.0 and 44.6.
 struct Spans {
   Costs costs;
-  int total, quota;
+  int total, quota, tiles;
+  bool whole;
 };
+__device__ __forceinline__ int few_tiles(const Costs& k) {
+  static_assert(kFewRows <= 4 * 16, "four tiles of a sequence at most");
+  int tiles = 0;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) tiles += __builtin_popcountll(__ballot(k.tiles > n));
+  return tiles;
+}
 __device__ __forceinline__ Spans few_spans(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
                                            int group) {
   Spans s;
   if (a.batch == 1) {      // no lane work on the way to the first load
     Work w;
     sequence(a, c, 0, w);
-    const Item it = few_item(a, plan, group, w);
-    s.costs.own = s.costs.upto = it.tiles * it.steps;
+    s.costs.set(w, few_item(a, plan, group, w));
     s.total = __builtin_amdgcn_readfirstlane(s.costs.upto);
+    s.tiles = __builtin_amdgcn_readfirstlane(s.costs.tiles);
   } else {
     s.costs = few_costs(a, c, plan, group, 0);
     s.total = __builtin_amdgcn_readlane(s.costs.upto, 63);
+    s.tiles = few_tiles(s.costs);
   }
-  for (int b0 = 64; b0 < a.batch; b0 += 64)
-    s.total += __builtin_amdgcn_readlane(few_costs(a, c, plan, group, b0).upto, 63);
+  for (int b0 = 64; b0 < a.batch; b0 += 64) {
+    const Costs k = few_costs(a, c, plan, group, b0);
+    s.total += __builtin_amdgcn_readlane(k.upto, 63);
+    s.tiles += few_tiles(k);
+  }
   s.quota = (int)((((unsigned)s.total + plan.workers - 1) / (unsigned)plan.workers + 3) & ~3u);
+  if (plan.whole > 0) {
+    // In a lone workgroup's steps; full: what one is worth on a full chip.
+    const float full = 1.25f * (float)few_per_cu(c.head_dim, plan.rows, c.bits) / (float)plan.slots;
+    const float spans = fmaxf((float)s.quota, full * (float)s.total) + 13.0f;
+    const int most = (int)(spans / fmaxf(1.0f, full * (float)s.tiles));
+    s.whole = !__any(s.costs.steps > most);
+    for (int b0 = 64; b0 < a.batch && s.whole; b0 += 64) s.whole = !__any(few_costs(a, c, plan, group, b0).steps > most);
+  } else {
+    s.whole = false;
+  }
   return s;
 }
-// The sequence that holds step `at` (below the total), and the steps before it.
-__device__ __forceinline__ int few_find(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan, int group,
-                                        const Spans& s, int at, int& before) {
+// The sequence w that holds step `at` (below the total), and the steps before it.
+__device__ __forceinline__ void few_find(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan, int group,
+                                        const Spans& s, int at, int& before, Work& w) {
   Costs k = s.costs;
   before = 0;
   for (int b0 = 0;; b0 += 64, k = few_costs(a, c, plan, group, b0)) {
@@ -252,7 +301,8 @@ __device__ __forceinline__ int few_find(const AttentionArgs& a, const qlinear_kv
     if (past || b0 + 64 >= a.batch) {
       const int i = past ? __builtin_ctzll(past) : 0;
       before += __builtin_amdgcn_readlane(k.upto - k.own, i);
-      return b0 + i;
+      k.get(b0 + i, w);
+      return;
     }
     before += __builtin_amdgcn_readlane(k.upto, 63);
   }

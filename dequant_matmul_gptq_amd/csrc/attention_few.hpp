@@ -313,14 +313,28 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
     stop = it.steps;
   } else {
     const Spans sp = few_spans(a, c, plan, group);
-    if ((int64_t)worker * sp.quota >= sp.total) return;
-    at = worker * sp.quota;
-    stop = min(at + sp.quota, sp.total);
-    int before;
-    sequence(a, c, few_find(a, c, plan, group, sp, at, before), w);
-    it = few_item(a, plan, group, w);
-    tile = (unsigned)(at - before) / (unsigned)it.steps;
-    i0 = at - before - tile * it.steps;
+    if (sp.whole) {
+      const int b = worker / plan.whole;
+      if (b >= a.batch) return;
+      if (b < 64)
+        sp.costs.get(b, w);
+      else
+        sequence(a, c, b, w);
+      it = few_item(a, plan, group, w);
+      tile = worker - b * plan.whole;
+      if (tile >= it.tiles) return;
+      at = 0;
+      stop = it.steps;
+    } else {
+      if (worker >= plan.workers || (int64_t)worker * sp.quota >= sp.total) return;
+      at = worker * sp.quota;
+      stop = min(at + sp.quota, sp.total);
+      int before;
+      few_find(a, c, plan, group, sp, at, before, w);
+      it = few_item(a, plan, group, w);
+      tile = (unsigned)(at - before) / (unsigned)it.steps;
+      i0 = at - before - tile * it.steps;
+    }
   }
   int slot = 0;                // of a partial result
 
@@ -635,7 +649,8 @@ hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const P
   const int group = a.q_heads / c.kv_heads;
   const int64_t most = (int64_t)a.max_q_len * group;
   const int tiles = (int)(((most < p.max_rows ? most : p.max_rows) + p.rows - 1) / p.rows);
-  const dim3 grid = p.workers ? dim3((unsigned)(c.kv_heads * p.workers))
+  const int workgroups = p.whole * a.batch > p.workers ? p.whole * a.batch : p.workers;
+  const dim3 grid = p.workers ? dim3((unsigned)(c.kv_heads * workgroups))
                               : dim3((unsigned)(c.kv_heads * tiles), (unsigned)a.batch);
   // One tile per sequence and key/value head reads each cache row once, more of
   // them share it through L2 (both sides measured, cold: 64 sequences of 2048

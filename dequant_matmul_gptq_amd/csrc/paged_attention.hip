@@ -40,6 +40,7 @@ __device__ __forceinline__ bool join_row(const AttentionArgs& a, const qlinear_k
     const int tile = r >> __builtin_ctz(plan.rows);
     if (tile >= it.tiles || r >= w.n * group) return false;
     const Spans sp = few_spans(a, c, plan, group);
+    if (sp.whole) return false;
     const unsigned start = few_before(a, c, plan, group, sp, w.b) + tile * it.steps, last = start + it.steps - 1;
     j.worker = (int)(start / (unsigned)sp.quota);
     j.parts = (int)(last / (unsigned)sp.quota) - j.worker + 1;
@@ -153,8 +154,11 @@ hipError_t launch_join(const qlinear_kv_cache& c, const AttentionArgs& a, const 
   return parts > kJoinAtOnce ? width(std::integral_constant<int, 4>{}) : width(std::integral_constant<int, 1>{});
 }
 
-// Up to this many steps a workgroup takes a tile whole, and nothing is joined.
-constexpr int kWholeSteps = 8;
+// Up to this many steps a workgroup takes a tile whole, and nothing is joined
+// (us, split and whole: one sequence of 400 tokens 10.3 and 10.6 (32/32 heads),
+// 8.1 and 5.9 (32/8 heads of 64); of 1000 11.0 and 18.4; 64 of 400, 64/8 heads,
+// 35.6 and 21.9). Past it the lengths decide on the device (see Spans).
+constexpr int kWholeSteps = 16;
 
 // Steps of `tokens` tokens that a row tile spans at most.
 int64_t plan_steps(const AttentionArgs& a, int tokens) {
@@ -191,8 +195,12 @@ Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
       // As many workgroups as the chip holds at once, of four steps at least.
       int64_t workers = 256 * few_per_cu(c.head_dim, p.rows, c.bits) / c.kv_heads;
       const int64_t quarter = (tiles * steps + 3) / 4;
+      p.slots = workers > 1 ? (int)workers : 1;
       if (workers > quarter) workers = quarter;
       p.workers = workers > 1 ? (int)workers : 1;
+      // One sequence this long is always cut. Past twice the slots spans hold
+      // several tiles each, and whole ones would gain little.
+      if (a.batch > 1 && tiles <= 2 * p.slots) p.whole = (int)(tiles / a.batch);
       r.few_rows = (int64_t)p.workers * c.kv_heads * 2 * p.rows;
     }
   }

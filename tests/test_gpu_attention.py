@@ -412,6 +412,22 @@ def test_unseen_quantized_nan_stays_out(n, bits):
         assert np.isfinite(o[i]).all() and (np.abs(o[i] - ref[0]) <= bound).all(), i
 
 
+@pytest.mark.parametrize("D,bits,Hq,Hk", [(128, 16, 8, 8), (64, 4, 16, 8), (256, 8, 8, 8)])
+def test_batches_of_near_equal_lengths(D, bits, Hq, Hk):
+    """Fewer and more tiles than the chip holds workgroups of a head, in lengths
+    near one another, with one much longer, and with some sequences without new tokens."""
+    say(f"attention near-equal lengths D={D} bits={bits}")
+    rng = np.random.default_rng(D + bits)
+    for B, n in ((2, 1), (20, 2), (65, 1)):
+        L = rng.integers(560, 640, B)
+        q = np.full(B, n)
+        b = Batch(Hq, Hk, D, 64, bits, 64, q, L, seed=B)
+        b.check(b.run(), what=f"B={B}")
+        q[B // 2], L[B // 3] = 0, 2500
+        b = Batch(Hq, Hk, D, 64, bits, 64, q, L, seed=B + 1)
+        b.check(b.run(), what=f"B={B}, one long")
+
+
 @pytest.mark.parametrize("n", (1, 100))
 def test_pools_past_32_bit_offsets(n):
     """Appended to, copied within and read from pages that lie more than 2^32 bytes and elements into a pool."""
