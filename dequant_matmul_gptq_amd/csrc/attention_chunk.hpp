@@ -5,9 +5,13 @@
 // where two steps of 64 would not leave room for a second workgroup in LDS).
 //
 // A step's keys and values are staged in LDS as float16 [token][D], two steps
-// deep: the next step's come in (float16: straight from memory to LDS;
-// quantized: through registers, dequantized by all waves together) while this
-// one is multiplied, with one barrier per step. The 32 x 32 x 16 products:
+// deep, with one barrier per step: the next step's are asked for before this
+// one is multiplied (float16: straight from memory to LDS; quantized: through
+// registers, dequantized by all waves together after this step's products).
+// The barrier does not wait for loads to LDS, so each wave waits for its own
+// before it. At D = 64 and 128 the compiler waits for them already before this
+// step's first LDS read, so that there a second workgroup on the CU covers
+// their latency, not this one's products. The 32 x 32 x 16 products:
 //   - S^T = K Q^T: keys are rows (A: 16-byte LDS reads), q stays in registers.
 //     Accumulator register r of lane (n, h) = (l % 32, l / 32) is token
 //     8 (r / 4) + 4 h + r % 4 and query row n.
@@ -17,14 +21,15 @@
 // 16-byte pieces of a row sit at places exclusive-or-ed with the row number,
 // so that the lanes of one LDS cycle hit different banks.
 //
-// Measured: a prompt of 8192 tokens, 64/8 heads of 128, float16: 1140 us, 965
-// TFLOP/s of the visible pairs, 73% of what a library product of 8192 cubed
+// Measured: a prompt of 8192 tokens, 64/8 heads of 128, float16: 1160 us, 948
+// TFLOP/s of the visible pairs, 72% of what a library product of 8192 cubed
 // reaches when warm (1325). Its cycles are half matrix products, half softmax
 // and waits, at a clock that the power limit holds near 1.8 GHz: the same call on
 // zeros takes 870 us. Tiles of 32 tokens with the next one's products in
 // between this one's exponentials, ordered by hand, took as many cycles (1160
 // to 1190 us). 511 tokens at 16384 over Q8, 40/40 heads: 237 us, 15 of them the
 // join; its unpacking is hidden (a third fewer instructions there changed nothing).
+// 4096 tokens of 16/4 heads of 256, one workgroup per CU: 261 us, 527 TFLOP/s.
 #pragma once
 
 #include <type_traits>
@@ -270,8 +275,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   float16v o[kOutTiles];
   float m, l;
 
-  // One step: rows in kc, vc; the next step's go to kn, vn. That the two pairs
-  // are apart (restrict) lets the reads of one pass the writes of the other.
+  // One step: rows in kc, vc; the next step's go to kn, vn, which are apart (restrict).
   // kind: see StepKind. False: an edge step has infinities or NaN that only
   // some rows see.
   auto one_step = [&](auto kind, int step, Lds __restrict__ kc, Lds __restrict__ vc, Lds __restrict__ kn,
@@ -451,11 +455,22 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     }
   };
   int step = begin, buf = 0;
+  // Everyone's rows are in LDS and nobody reads the others any more. A barrier
+  // does not wait for loads from memory to LDS, so each wave waits for its own
+  // first (vmcnt 0, the other counters open); the compiler's waits are for its
+  // own reads alone, and not at every width.
+  auto meet = [&]() __attribute__((always_inline)) {
+    if constexpr (B == 16) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0F70);
+    }
+    __syncthreads();
+  };
   // Steps of one kind up to `to`; each turns the buffers.
   auto steps_to = [&](auto kind, int to) __attribute__((always_inline)) -> bool {
     while (step < to) {
       for (; step < to; ++step, buf ^= 1) {
-        __syncthreads();     // this step's rows are in LDS; the other buffers are free
+        meet();
         if (!one_step(kind, step, (Lds)ks[buf], (Lds)vs[buf], (Lds)ks[buf ^ 1], (Lds)vs[buf ^ 1])) break;
       }
       if constexpr (decltype(kind)::value == kWhole) {
@@ -481,7 +496,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
   }
   if (!done) {
-    __syncthreads();       // the staging under way has ended
+    meet();                // the staging under way ends before the first step's starts again
     step = begin;
     buf = 0;
     start();

@@ -450,3 +450,23 @@ def test_pools_past_32_bit_offsets(n):
     err = np.abs(o.double().cpu().numpy() - ref)
     tiny = L * np.abs(v).max() / np.maximum(total, 1.0)
     assert (err <= 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * w + 2.0 ** -25 * (1 + tiny[..., None])).all()
+
+
+@pytest.mark.parametrize("D", (64, 128, 256))
+def test_long_chunks_from_memory(D):
+    """Many whole steps, rows staged from memory rather than from a cache, one
+    range of steps and several: no step may use rows that have not arrived."""
+    say(f"attention long chunk D={D}")
+    n, past = 150, 5000
+    b = Batch(4, 2, D, 64, 16, 64, [n], [n + past], seed=D)
+    ref, w, total = oracle.decoder.attention(b.q[0], b.kv[0][0], b.kv[1][0], D ** -0.5)
+    tiny = (n + past) * np.abs(b.kv[1][0]).max() / np.maximum(total, 1.0)
+    bound = 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * w + 2.0 ** -25 * (1 + tiny[..., None])
+    other = torch.empty(1 << 30, dtype=torch.uint8, device=device())
+    # a small length bound plans one range
+    assert dq.paged_attention_workspace_bytes(b.cache, n, 4, 1, n, n + past) > 0
+    for kw in (dict(max_kv_len=n), dict(max_kv_len=n + past)):
+        for _ in range(3):
+            other.add_(1)          # what the caches hold now
+            o = b.run(**kw)
+            assert (np.abs(o - ref) <= bound).all(), (kw, (np.abs(o - ref) / bound).max())
