@@ -30,6 +30,14 @@ def _stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
 
 
+def _gpu_of(t: torch.Tensor, name: str) -> int:
+    """The GPU that the call runs on, that of its operand t."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return device
+
+
 def _operand(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
     """Check a contiguous operand on GPU `device` and return its pointer."""
     if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
@@ -197,7 +205,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
          out: torch.Tensor | None = None) -> torch.Tensor:
     """x float16 [tokens][heads][head_dim] (token stride free) rotated to the
     positions (int32 [tokens]) by the table of rope_table. out may be x."""
-    dev = x.get_device()
+    dev = _gpu_of(x, "x")
     xp, T, H, D, xs = _rows(x, "x", None, None, None, dev)
     pos, tab, rows, rot = _rope_operands(table, positions, T, dev)
     if out is None:
@@ -330,7 +338,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual:
     residual_out if it is given (it may be x or residual). out may be x."""
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
-    dev, shape = x.get_device(), x.shape
+    dev, shape = _gpu_of(x, "x"), x.shape
     K = shape[-1]
     xp = _operand(x, "x", _F16, shape, dev)
     wp = _operand(weight, "weight", _F16, (K,), dev)

@@ -7,6 +7,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 import dequant_matmul_gptq_amd as dq
 from dequant_matmul_gptq_amd import _lib
@@ -364,3 +365,14 @@ def test_rms_norm_refuses_what_its_indexes_cannot_hold(change):
     a = dict(x=FAKE, residual=None, weight=FAKE, M=1, K=64, eps=1e-5, out=FAKE, residual_out=None)
     a.update(change)
     assert dq.lib().qlinear_rms_norm(*a.values(), None) == UNS
+
+
+def test_binding_refuses_host_tensors():
+    """Calls whose operands are all in host memory, so that their devices agree."""
+    x, w = torch.zeros((4, 2, 64), dtype=torch.float16), torch.ones(64, dtype=torch.float16)
+    pos, table = torch.zeros(4, dtype=torch.int32), dq.rope_table(8, 64)
+    for call in (lambda: dq.rms_norm(x, w), lambda: dq.rms_norm(x, w, residual=x, out=x, residual_out=x.clone()),
+                 lambda: dq.rope(x, pos, table), lambda: dq.rope(x[:0], pos[:0], table),
+                 lambda: dq.rope(x.to("meta"), pos, table), lambda: dq.KVCache(x[None], x[None])):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
