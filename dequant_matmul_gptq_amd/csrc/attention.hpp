@@ -111,10 +111,12 @@ __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_k
   w.len = (int)min((int64_t)max(a.kv_len[b], 0), cap);
 }
 
-__device__ __forceinline__ int first_seen(int p, int window) { return window > 0 ? max(0, p - window + 1) : 0; }
+__host__ __device__ __forceinline__ int first_seen(int p, int window) {
+  return window > 0 && p >= window ? p - window + 1 : 0;     // no difference of a negative p and any window
+}
 
 // The tile of `tile_rows` rows from row0 on (group rows per token).
-__device__ __forceinline__ void row_tile(const AttentionArgs& a, int group, int row0, int tile_rows, Work& w) {
+__host__ __device__ __forceinline__ void row_tile(const AttentionArgs& a, int group, int row0, int tile_rows, Work& w) {
   w.row0 = row0;
   w.rows = min(tile_rows, w.n * group - row0);
   w.p_min = w.len - w.n + row0 / group;
@@ -189,7 +191,7 @@ __device__ __forceinline__ bool find_tile(const AttentionArgs& a, const qlinear_
 struct Item {
   int tiles, steps, first_step;
 };
-__device__ __forceinline__ Item few_item(const AttentionArgs& a, const Plan& plan, int group, const Work& w) {
+__host__ __device__ __forceinline__ Item few_item(const AttentionArgs& a, const Plan& plan, int group, const Work& w) {
   const int rows = w.n * group;
   Item it;
   it.tiles = rows > plan.max_rows ? 0 : (rows + plan.rows - 1) >> __builtin_ctz(plan.rows);

@@ -1,0 +1,33 @@
+// Host-side probe of what the attention kernels' workgroups work out about
+// their rows and steps. Reads lines of
+//   rows <new tokens> <length> <group> <window> <row0> <tile rows>
+// and prints the positions and first tokens seen of that row tile, and the
+// steps that the few-row kernel counts for the sequence. Runs on the CPU only;
+// calls no HIP runtime function.
+#include <cstdio>
+#include <cstring>
+
+#include "attention.hpp"
+
+using namespace qlinear;
+
+int main() {
+  char what[16];
+  while (scanf("%15s", what) == 1) {
+    if (!strcmp(what, "rows")) {
+      attn::Work w = {};
+      AttentionArgs a = {};
+      attn::Plan plan = {};
+      int group, row0, tile_rows;
+      if (scanf("%d %d %d %d %d %d", &w.n, &w.len, &group, &a.window, &row0, &tile_rows) != 6) return 1;
+      plan.rows = 16;
+      plan.max_rows = INT32_MAX;
+      const attn::Item it = attn::few_item(a, plan, group, w);
+      attn::row_tile(a, group, row0, tile_rows, w);
+      printf("%d %d %d %d %d %d\n", w.p_min, w.p_max, w.lo_min, w.lo_max, it.first_step, it.steps);
+    } else {
+      return 1;
+    }
+  }
+  return 0;
+}

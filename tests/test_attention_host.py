@@ -1,0 +1,50 @@
+"""The attention kernels' arithmetic on rows, steps and pages, compiled for the
+host, against the same in whole numbers without a limit (no GPU)."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def probe(tmp_path_factory):
+    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not available")
+    exe = str(tmp_path_factory.mktemp("probe") / "attention_probe")
+    cmd = [hipcc, "-std=c++20", "-O1", "-x", "hip", "--offload-arch=gfx950", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(ROOT, "dequant_matmul_gptq_amd", "csrc"),
+           os.path.join(ROOT, "tests", "host", "attention_probe.cpp"), "-o", exe]
+    subprocess.run(cmd, check=True, capture_output=True)
+
+    def ask(what, cases):
+        text = "\n".join(" ".join(map(str, (what, *c))) for c in cases)
+        out = subprocess.run([exe], input=text, check=True, capture_output=True, text=True).stdout
+        got = [tuple(map(int, line.split())) for line in out.splitlines()]
+        assert len(got) == len(cases)
+        return got
+
+    return ask
+
+
+def _first(p, window):
+    return max(0, p - window + 1) if window else 0
+
+
+def test_rows_see_what_the_window_says(probe):
+    """Windows up to the largest number, rows before the first token among them."""
+    cases = [(n, L, group, window, row0, 16)
+             for n, L in ((1, 1), (5, 3), (100, 40), (300, 0), (40, 5000), (64, 2000000000))
+             for group in (1, 4) for window in (0, 1, 33, 4096, INT_MAX - 1, INT_MAX)
+             for row0 in range(0, n * group, 16)]
+    for (n, L, group, window, row0, rows), got in zip(cases, probe("rows", cases)):
+        last = min(row0 + rows, n * group) - 1
+        lo, hi = L - n + row0 // group, L - n + last // group
+        first = _first(L - n, window) // 32
+        steps = max((L - 1) // 32 - first, 0) + 1
+        assert got == (lo, hi, _first(lo, window), _first(hi, window), first, steps), (n, L, group, window, row0)

@@ -470,3 +470,13 @@ def test_long_chunks_from_memory(D):
             other.add_(1)          # what the caches hold now
             o = b.run(**kw)
             assert (np.abs(o - ref) <= bound).all(), (kw, (np.abs(o - ref) / bound).max())
+
+
+@pytest.mark.parametrize("n,L", [(5, 3), (100, 40), (3, 0)])
+def test_windows_that_end_nowhere(n, L):
+    """The largest windows hide nothing, also from rows before the first token."""
+    say(f"attention window 2^31 - 1 n={n} L={L}")
+    for D in (64, 128):
+        b = Batch(4, 2, D, 16, 16, 64, [n, 1], [L, 700], seed=n)
+        for window in (2 ** 31 - 1, 2 ** 31 - n):
+            b.check(b.run(window=window), what=f"window={window}")
