@@ -96,6 +96,18 @@ struct Work {
   int lo_min, lo_max;  // first tokens they see
 };
 
+// A sequence's length as its table bounds it, and so far below 2^31 that the
+// tokens whose pages are looked up ahead have numbers too (kLookAhead past the
+// last one at most: a step of 64, and the two after it).
+constexpr int kLookAhead = 256;
+constexpr int kMaxLength = INT32_MAX - 1023;
+static_assert(kMaxLength <= INT32_MAX - kLookAhead);
+__host__ __device__ __forceinline__ int bounded_length(int kv_len, int table_width, int page_size) {
+  const int64_t cap = (int64_t)table_width * page_size;
+  const int most = cap < kMaxLength ? (int)cap : kMaxLength;
+  return kv_len < 0 ? 0 : kv_len < most ? kv_len : most;
+}
+
 // Sequence b's rows and length, bounded by what the buffers hold.
 __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
   w.b = b;
@@ -107,8 +119,7 @@ __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_k
     w.n = a.tokens / a.batch;
     w.q0 = b * w.n;
   }
-  const int64_t cap = (int64_t)a.table_width * c.page_size;
-  w.len = (int)min((int64_t)max(a.kv_len[b], 0), cap);
+  w.len = bounded_length(a.kv_len[b], a.table_width, c.page_size);
 }
 
 __host__ __device__ __forceinline__ int first_seen(int p, int window) {

@@ -494,7 +494,7 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
  *   kv_len    : int32 [batch]
  *   block_table : int32 [batch][table_width], see qlinear_kv_cache; entries
  *               past a sequence's pages are not read. A length is taken to be
- *               at most table_width * page_size.
+ *               at most table_width * page_size, and 2^31 - 1024.
  *   max_q_len : upper bound of n; a sequence with more may be left out
  *   max_kv_len : upper bound of L, for the launch plan only (too small a one
  *               costs speed)

@@ -2,8 +2,10 @@
 // their rows and steps. Reads lines of
 //   rows <new tokens> <length> <group> <window> <row0> <tile rows>
 // and prints the positions and first tokens seen of that row tile, and the
-// steps that the few-row kernel counts for the sequence. Runs on the CPU only;
-// calls no HIP runtime function.
+// steps that the few-row kernel counts for the sequence; and lines of
+//   length <length> <table width> <page size>
+// and prints the length that the kernels take. Runs on the CPU only; calls no
+// HIP runtime function.
 #include <cstdio>
 #include <cstring>
 
@@ -25,6 +27,10 @@ int main() {
       const attn::Item it = attn::few_item(a, plan, group, w);
       attn::row_tile(a, group, row0, tile_rows, w);
       printf("%d %d %d %d %d %d\n", w.p_min, w.p_max, w.lo_min, w.lo_max, it.first_step, it.steps);
+    } else if (!strcmp(what, "length")) {
+      int len, width, page;
+      if (scanf("%d %d %d", &len, &width, &page) != 3) return 1;
+      printf("%d\n", attn::bounded_length(len, width, page));
     } else {
       return 1;
     }

@@ -48,3 +48,14 @@ def test_rows_see_what_the_window_says(probe):
         first = _first(L - n, window) // 32
         steps = max((L - 1) // 32 - first, 0) + 1
         assert got == (lo, hi, _first(lo, window), _first(hi, window), first, steps), (n, L, group, window, row0)
+
+
+def test_lengths_leave_room_to_look_ahead(probe):
+    """Lengths bounded by the table, and the tokens looked up two steps past the last one below 2^31."""
+    cases = [(L, width, page) for page in (16, 256) for width in (1, 3, 4000, 2 ** 23 - 1, 2 ** 23, 2 ** 27, 2 ** 29)
+             for L in (INT_MAX, INT_MAX - 200, INT_MAX - 1500, 5000, 700, 1, 0, -1, -INT_MAX)]
+    for (L, width, page), (got,) in zip(cases, probe("length", cases)):
+        assert got == max(0, min(L, width * page, INT_MAX - 1023))
+        for step in (32, 64):       # of the two kernels: the few-row one looks four turns of a wave ahead
+            ahead = 4 if step == 32 else 2
+            assert (got // step + 1 + ahead) * step <= INT_MAX
