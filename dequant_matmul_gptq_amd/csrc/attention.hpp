@@ -108,13 +108,18 @@ __host__ __device__ __forceinline__ int bounded_length(int kv_len, int table_wid
   return kv_len < 0 ? 0 : kv_len < most ? kv_len : most;
 }
 
+// Rows q0 .. q1 - 1 of q, as far as there are such.
+__host__ __device__ __forceinline__ void bounded_rows(int q0, int q1, int tokens, Work& w) {
+  w.q0 = q0 > 0 ? q0 : 0;
+  const int end = q1 < tokens ? q1 : tokens;
+  w.n = end > w.q0 ? end - w.q0 : 0;
+}
+
 // Sequence b's rows and length, bounded by what the buffers hold.
 __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
   w.b = b;
   if (a.q_start) {
-    const int q0 = max(a.q_start[b], 0), q1 = min(a.q_start[b + 1], a.tokens);
-    w.q0 = q0;
-    w.n = max(q1 - q0, 0);
+    bounded_rows(a.q_start[b], a.q_start[b + 1], a.tokens, w);
   } else {
     w.n = a.tokens / a.batch;
     w.q0 = b * w.n;

@@ -4,7 +4,9 @@
 // and prints the positions and first tokens seen of that row tile, and the
 // steps that the few-row kernel counts for the sequence; and lines of
 //   length <length> <table width> <page size>
-// and prints the length that the kernels take. Runs on the CPU only; calls no
+// and prints the length that the kernels take; and lines of
+//   start <first row> <row after the last> <tokens>
+// and prints the first row and the number of rows that they take. Runs on the CPU only; calls no
 // HIP runtime function.
 #include <cstdio>
 #include <cstring>
@@ -31,6 +33,12 @@ int main() {
       int len, width, page;
       if (scanf("%d %d %d", &len, &width, &page) != 3) return 1;
       printf("%d\n", attn::bounded_length(len, width, page));
+    } else if (!strcmp(what, "start")) {
+      attn::Work w = {};
+      int q0, q1, tokens;
+      if (scanf("%d %d %d", &q0, &q1, &tokens) != 3) return 1;
+      attn::bounded_rows(q0, q1, tokens, w);
+      printf("%d %d\n", w.q0, w.n);
     } else {
       return 1;
     }

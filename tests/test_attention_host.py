@@ -59,3 +59,12 @@ def test_lengths_leave_room_to_look_ahead(probe):
         for step in (32, 64):       # of the two kernels: the few-row one looks four turns of a wave ahead
             ahead = 4 if step == 32 else 2
             assert (got // step + 1 + ahead) * step <= INT_MAX
+
+
+def test_rows_stay_inside_q(probe):
+    """Any two numbers in q_start, also ones that are not those of rows."""
+    values = (-2 ** 31, -5, 0, 1, 7, 40, 41, 5000, INT_MAX)
+    cases = [(q0, q1, tokens) for q0 in values for q1 in values for tokens in (1, 40, 1 << 29)]
+    for (q0, q1, tokens), (first, n) in zip(cases, probe("start", cases)):
+        want = range(max(q0, 0), max(min(q1, tokens), max(q0, 0)))
+        assert (first, n) == (want.start, len(want)) and (n == 0 or first + n <= tokens)
