@@ -155,13 +155,14 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   half8 q[kFrags];
   {
     const uint16_t* p = a.q + (w.q0 + tok) * a.q_stride + (int64_t)qh * D + 8 * h;
-    // The kernel's scale is positive: a negative one turns q, 0 makes it 0.
-    const uint32_t flip = a.scale < 0.0f ? kTops : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
+    // The kernel's scale is positive: a negative one turns q, 0 makes it 0 (NaN
+    // where it is not finite).
+    const uint32_t flip = a.scale < 0.0f ? kTops : 0u;
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
       u32x4 v = *reinterpret_cast<const u32x4*>(p + 16 * f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (v[e] ^ flip) & keep;
+      for (int e = 0; e < 4; ++e) v[e] = a.scale == 0.0f ? spread_top(nonfinite_halves(v[e])) : v[e] ^ flip;
       const half8 x = __builtin_bit_cast(half8, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) q[f][e] = x[unpacked<B>(e)];

@@ -480,3 +480,23 @@ def test_windows_that_end_nowhere(n, L):
         b = Batch(4, 2, D, 16, 16, 64, [n, 1], [L, 700], seed=n)
         for window in (2 ** 31 - 1, 2 ** 31 - n):
             b.check(b.run(window=window), what=f"window={window}")
+
+
+@pytest.mark.parametrize("n", (3, 150))
+@pytest.mark.parametrize("value", (np.nan, np.inf))
+def test_non_finite_queries(n, value):
+    """A NaN or infinity in a head's query makes that row NaN (its scores are, or
+    their differences), at any scale, zero among them, and leaves the others."""
+    say(f"attention non-finite query n={n} {value}")
+    b = Batch(4, 2, 64, 32, 16, 64, [n], [n + 90], seed=n)
+    b.q[0][1, 2, 5] = b.q[0][n - 1, 3, 63] = value
+    hit = np.zeros((n, 4), bool)
+    hit[1, 2] = hit[n - 1, 3] = True
+    finite = np.where(hit[..., None], 0, b.q[0])
+    for scale in (0.0, 0.1, -0.1):
+        o = b.run(scale=scale)
+        ref, w, total = oracle.decoder.attention(finite, b.kv[0][0], b.kv[1][0], scale)
+        tiny = (n + 90) * np.abs(b.kv[1][0]).max() / np.maximum(total, 1.0)
+        bound = 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * w + 2.0 ** -25 * (1 + tiny[..., None])
+        assert np.isnan(o[hit]).all(), scale
+        assert (np.abs(o - ref)[~hit] <= bound[~hit]).all(), scale
