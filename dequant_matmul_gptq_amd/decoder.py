@@ -30,6 +30,17 @@ def _stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _int32(*numbers):
+    """The numbers as the C calls take them. ctypes would cut them to 32 bits; a
+    bound (of a length, a window) past those is as good as the largest one, and
+    a size or a negative number past them is refused as the largest or -1 is.
+    Callers come here if the numbers' or, shifted by 31, is not 0."""
+    return tuple(max(-1, min(n, _INT_MAX)) for n in numbers)
+
+
 def _gpu_of(t: torch.Tensor, name: str) -> int:
     """The GPU that the call runs on, that of its operand t."""
     device = t.get_device()
@@ -211,6 +222,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
     if out is None:
         out = torch.empty((T, H, D), dtype=_F16, device=x.device)
     op, _, _, _, ost = _rows(out, "out", T, H, D, dev)
+    if (T | H | D | rows | rot) >> 31:
+        T, H, D, rows, rot = _int32(T, H, D, rows, rot)
     _check(lib().qlinear_rope(xp, xs, T, H, D, pos, tab, rows, rot, layout, op, ost, _stream(dev)), "qlinear_rope")
     return out
 
@@ -240,6 +253,8 @@ def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torc
         op, _, _, _, ost = _rows(q_out, "q_out", T, heads, D, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    if (T | heads | rows | rot) >> 31:
+        T, heads, rows, rot = _int32(T, heads, rows, rot)
     _check(lib().qlinear_rope_append(cache.ref, qp, qs, heads, kp, ks, vp, vs, op, ost, T, pos, sp, tab, rows, rot,
                                      layout, _stream(dev)), "qlinear_rope_append")
     return q_out
@@ -250,9 +265,8 @@ def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torc
 def paged_attention_workspace_bytes(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int,
                                     max_kv_len: int, window: int = 0) -> int:
     n = ctypes.c_size_t(0)
-    _check(lib().qlinear_paged_attention_workspace_bytes(cache.ref, int(tokens), int(q_heads), int(batch),
-                                                         int(max_q_len), int(max_kv_len), int(window),
-                                                         ctypes.byref(n)),
+    sizes = _int32(int(tokens), int(q_heads), int(batch), int(max_q_len), int(max_kv_len), int(window))
+    _check(lib().qlinear_paged_attention_workspace_bytes(cache.ref, *sizes, ctypes.byref(n)),
            "qlinear_paged_attention_workspace_bytes")
     return int(n.value)
 
@@ -293,7 +307,7 @@ def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, 
     if max_q_len is None:
         max_q_len = T if q_start is not None or B == 0 else T // B
     if max_kv_len is None:
-        max_kv_len = min(W * cache.page_size, 2 ** 31 - 1)
+        max_kv_len = W * cache.page_size
     if scale is None:
         scale = D ** -0.5
     if out is None:
@@ -303,6 +317,8 @@ def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, 
         workspace = paged_attention_workspace(cache, T, H, B, max_q_len, max_kv_len, q.device, window)
     n = workspace.numel()
     wp = _operand(workspace, "workspace", _U8, (n,), dev)
+    if (T | H | B | W | max_q_len | max_kv_len | window) >> 31:
+        T, H, B, W, max_q_len, max_kv_len, window = _int32(T, H, B, W, max_q_len, max_kv_len, window)
     _check(lib().qlinear_paged_attention(cache.ref, qp, qs, T, H, B, sp, lp, tp, W, max_q_len, max_kv_len, scale,
                                          window, op, wp, n, _stream(dev)), "qlinear_paged_attention")
     return out
@@ -326,6 +342,8 @@ def copy_pages(caches, pairs: torch.Tensor) -> None:
     # The structs side by side (ctypes' own array constructor takes 0.3 us each).
     arr = (qlinear_kv_cache * max(1, len(caches))).from_buffer_copy(
         b"".join([c.raw for c in caches]) or bytes(ctypes.sizeof(qlinear_kv_cache)))
+    if moves >> 31:
+        moves, = _int32(moves)
     _check(lib().qlinear_copy_pages(arr, len(caches), pp, moves, _stream(dev)), "qlinear_copy_pages")
 
 
@@ -348,5 +366,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual:
     op = _operand(out, "out", _F16, shape, dev)
     hp = None if residual_out is None else _operand(residual_out, "residual_out", _F16, shape, dev)
     M = x.numel() // K if K else 0
+    if (M | K) >> 31:
+        M, K = _int32(M, K)
     _check(lib().qlinear_rms_norm(xp, rp, wp, M, K, eps, op, hp, _stream(dev)), "qlinear_rms_norm")
     return out

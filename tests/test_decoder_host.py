@@ -4,6 +4,7 @@ oracle's functions. No GPU needed."""
 
 import ctypes
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -376,3 +377,19 @@ def test_binding_refuses_host_tensors():
                  lambda: dq.rope(x.to("meta"), pos, table), lambda: dq.KVCache(x[None], x[None])):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_binding_passes_no_number_cut_to_32_bits():
+    """Past 32 bits a bound counts as the largest one and a size is refused."""
+    cache = SimpleNamespace(ref=ctypes.byref(_cache()))
+    need = lambda *sizes: dq.paged_attention_workspace_bytes(cache, *sizes)      # noqa: E731
+    top = 2 ** 31 - 1
+    assert need(8, 8, 2, 4, 2 ** 32, 0) == need(8, 8, 2, 4, top, 0) > 0
+    assert need(8, 8, 2, 2 ** 32 + 1, 5000, 0) == need(8, 8, 2, top, 5000, 0)
+    assert need(8, 8, 2, 4, 5000, 2 ** 32 + 64) == need(8, 8, 2, 4, 5000, top) != need(8, 8, 2, 4, 5000, 64)
+    for sizes, status in (((2 ** 32 + 8, 8, 2, 4, 5000), UNS), ((8, 2 ** 32 + 8, 2, 4, 5000), UNS),
+                          ((8, 8, 2 ** 32 + 2, 4, 5000), UNS), ((8, 8, 2, -2 ** 32, 5000), INV),
+                          ((8, 8, 2, 4, 5000, 1 - 2 ** 32), INV)):
+        with pytest.raises(dq.QlinearError) as e:
+            need(*sizes)
+        assert e.value.status == status, sizes

@@ -500,3 +500,13 @@ def test_non_finite_queries(n, value):
         bound = 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * w + 2.0 ** -25 * (1 + tiny[..., None])
         assert np.isnan(o[hit]).all(), scale
         assert (np.abs(o - ref)[~hit] <= bound[~hit]).all(), scale
+
+
+def test_sizes_past_32_bits():
+    say("attention sizes past 32 bits")
+    b = Batch(4, 2, 64, 32, 16, 64, [3, 70], [200, 90], seed=3)
+    o = b.run()
+    for kw in (dict(window=2 ** 32 + 1), dict(max_kv_len=2 ** 32 + 1), dict(max_q_len=2 ** 32 + 1)):
+        assert np.array_equal(b.run(**kw), o), kw
+    with pytest.raises(dq.QlinearError):
+        b.run(window=1 - 2 ** 32)

@@ -253,3 +253,12 @@ def test_binding_refuses_wrong_tensors():
         dq.rope_append(c, None, x[:, :1], x, pos, pos, table)
     with pytest.raises(ValueError):
         dq.rope_append(c, None, x, x, None, pos, table)
+
+
+def test_rms_norm_refuses_rows_past_32_bits():
+    say("rms_norm rows past 32 bits")
+    x = torch.empty((2 ** 32 + 5, 1), dtype=torch.float16, device=device())
+    out = torch.empty_like(x)
+    with pytest.raises(dq.QlinearError) as e:
+        dq.rms_norm(x, torch.ones(1, dtype=torch.float16, device=device()), out=out)
+    assert e.value.status == dq._lib.ERR_UNSUPPORTED
