@@ -192,7 +192,7 @@ int qlinear_paged_attention(const qlinear_kv_cache* cache, const uint16_t* q, in
   a.table_width = table_width;
   a.scale = scale;
   a.out = out;
-  const size_t need = paged_attention_workspace_bytes(*cache, a);
+  const size_t need = paged_attention_workspace_need(*cache, a);
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLINEAR_ERR_WORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return QLINEAR_ERR_MISALIGNED;
   return hip_status(launch_paged_attention(*cache, a, workspace, (hipStream_t)stream));

@@ -167,6 +167,20 @@ int64_t plan_steps(const AttentionArgs& a, int tokens) {
   return (a.max_kv_len + (int64_t)tokens - 1) / tokens;
 }
 
+// Workgroups of a key/value head that the chip holds at once, and as many of
+// them as get four steps each at least; rows of their partial results.
+int few_slots(const qlinear_kv_cache& c, int rows) {
+  const int slots = 256 * few_per_cu(c.head_dim, rows, c.bits) / c.kv_heads;
+  return slots > 1 ? slots : 1;
+}
+int few_workers(const qlinear_kv_cache& c, int rows, int64_t tiles, int64_t steps) {
+  const int64_t slots = few_slots(c, rows), quarter = (tiles * steps + 3) / 4;
+  return (int)(slots < quarter ? slots : quarter > 1 ? quarter : 1);
+}
+int64_t few_partial_rows(const qlinear_kv_cache& c, int rows, int workers) {
+  return (int64_t)workers * c.kv_heads * 2 * rows;
+}
+
 // The sequences of a call are served by their number of rows per key/value
 // head: up to kFewRows by the few-row kernel, more by the chunk kernel. A call
 // launches the kernels that it may need.
@@ -192,16 +206,12 @@ Route make_route(const qlinear_kv_cache& c, const AttentionArgs& a) {
     const int64_t tiles = (int64_t)(r.few_cap + p.rows - 1) / p.rows * a.batch;
     const int64_t steps = plan_steps(a, kStep);
     if (steps > kWholeSteps) {
-      // As many workgroups as the chip holds at once, of four steps at least.
-      int64_t workers = 256 * few_per_cu(c.head_dim, p.rows, c.bits) / c.kv_heads;
-      const int64_t quarter = (tiles * steps + 3) / 4;
-      p.slots = workers > 1 ? (int)workers : 1;
-      if (workers > quarter) workers = quarter;
-      p.workers = workers > 1 ? (int)workers : 1;
+      p.slots = few_slots(c, p.rows);
+      p.workers = few_workers(c, p.rows, tiles, steps);
       // One sequence this long is always cut. Past twice the slots spans hold
       // several tiles each, and whole ones would gain little.
       if (a.batch > 1 && tiles <= 2 * p.slots) p.whole = (int)(tiles / a.batch);
-      r.few_rows = (int64_t)p.workers * c.kv_heads * 2 * p.rows;
+      r.few_rows = few_partial_rows(c, p.rows, p.workers);
     }
   }
   if (r.chunk) {
@@ -240,11 +250,45 @@ Partials partials(void* ws, int64_t ranges, int64_t rows, int D) {
 }  // namespace
 
 // The two kernels' launches follow one another on the stream and share the workspace.
-size_t paged_attention_workspace_bytes(const qlinear_kv_cache& cache, const AttentionArgs& a) {
+size_t paged_attention_workspace_need(const qlinear_kv_cache& cache, const AttentionArgs& a) {
   const Route r = make_route(cache, a);
   const size_t few = partial_bytes(1, r.few_rows, cache.head_dim);
   const size_t chunk = partial_bytes(r.chunk_plan.splits, r.chunk_rows, cache.head_dim);
   return few > chunk ? few : chunk;
+}
+
+// Smaller calls may need more (fewer rows are split further), so this goes over
+// the kinds of plan that a call of at most these sizes may have, each at its most.
+size_t paged_attention_workspace_bytes(const qlinear_kv_cache& c, const AttentionArgs& a) {
+  const int64_t group = a.q_heads / c.kv_heads, most = a.max_q_len * group;
+  const int64_t cap = most < kFewRows ? most : kFewRows;
+  // A window's steps are one more where fewer new tokens reach less far than the length bound.
+  auto steps_of = [&](int tokens) {
+    const int64_t reach = (int64_t)a.window + a.max_q_len, all = a.max_kv_len;
+    const int64_t seen = a.window > 0 && reach < all ? reach : all;
+    return (seen + tokens - 1) / tokens + (a.window > 0 ? 1 : 0);
+  };
+  int64_t rows = 0;
+  auto few = [&](int tile_rows, int64_t most_rows) {
+    const int64_t tiles = (most_rows + tile_rows - 1) / tile_rows * a.batch;
+    const int64_t r = few_partial_rows(c, tile_rows, few_workers(c, tile_rows, tiles, steps_of(kStep)));
+    if (r > rows) rows = r;
+  };
+  if ((group <= kFewRows || a.batch > 1) && steps_of(kStep) > kWholeSteps) {
+    if (c.head_dim == 256)
+      few(16, cap);
+    else if (group <= 16)
+      few(16, cap < 16 ? cap : 16);
+    if (c.head_dim != 256 && cap > 16) few(32, cap);
+  }
+  const int64_t ranges = steps_of(chunk_step(c.head_dim)) / 8;
+  if (most > kFewRows && ranges > 1 && 512 / c.kv_heads > 1) {
+    // Ranges times tiles times heads are 512 at most, of kChunkRows rows each.
+    const int64_t all = ranges * a.tokens * a.q_heads;
+    const int64_t r = all < 512 * kChunkRows ? all : 512 * kChunkRows;
+    if (r > rows) rows = r;
+  }
+  return partial_bytes(1, rows, c.head_dim);
 }
 
 hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const AttentionArgs& a, void* ws,

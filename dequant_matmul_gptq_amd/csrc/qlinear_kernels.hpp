@@ -129,6 +129,9 @@ struct AttentionArgs {
   float scale;
   uint16_t* out;
 };
+// What a call takes of its workspace, and what is enough for it and for all
+// smaller ones.
+size_t paged_attention_workspace_need(const qlinear_kv_cache& cache, const AttentionArgs& a);
 size_t paged_attention_workspace_bytes(const qlinear_kv_cache& cache, const AttentionArgs& a);
 hipError_t launch_paged_attention(const qlinear_kv_cache& cache, const AttentionArgs& a, void* ws,
                                   hipStream_t stream);

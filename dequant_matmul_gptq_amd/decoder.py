@@ -273,8 +273,9 @@ def paged_attention_workspace_bytes(cache: KVCache, tokens: int, q_heads: int, b
 
 def paged_attention_workspace(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int, max_kv_len: int,
                               device, window: int = 0) -> torch.Tensor:
-    """A paged_attention workspace for calls of these sizes (scratch: needs no
-    initialization; calls that may overlap in time must not share one)."""
+    """A paged_attention workspace for calls of up to these sizes with the same
+    q_heads and window (scratch: needs no initialization; calls that may overlap
+    in time must not share one)."""
     n = paged_attention_workspace_bytes(cache, tokens, q_heads, batch, max_q_len, max_kv_len, window)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 

@@ -500,8 +500,10 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
  *               costs speed)
  *   window    : 0 = none
  *   out       : float16 [tokens][q_heads][head_dim], contiguous; not q
- *   workspace : qlinear_paged_attention_workspace_bytes of the same sizes;
- *               scratch, as for qlinear_qgemv
+ *   workspace : qlinear_paged_attention_workspace_bytes of the same sizes, or
+ *               of larger tokens, batch, max_q_len and max_kv_len: its answer
+ *               is enough for all calls up to them with the same cache shape,
+ *               q_heads and window. Scratch, as for qlinear_qgemv
  * Cache slots that no new token of the sequence sees never reach its result,
  * whatever they hold; nor do tokens that other rows see reach a row that does
  * not see them. A page number outside the pool reads some page inside it.

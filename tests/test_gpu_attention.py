@@ -510,3 +510,16 @@ def test_sizes_past_32_bits():
         assert np.array_equal(b.run(**kw), o), kw
     with pytest.raises(dq.QlinearError):
         b.run(window=1 - 2 ** 32)
+
+
+def test_one_workspace_for_the_chunks_of_a_prompt():
+    say("attention workspace")
+    dev = device()
+    top = 700
+    cache = None
+    for n, past in ((top, 0), (300, 4000), (33, 9000), (3, 9000), (1, 9000)):
+        b = Batch(8, 2, 64, 64, 16, 64, [n], [n + past], seed=n)
+        if cache is None:
+            cache = b.cache
+            ws = dq.paged_attention_workspace(cache, top, 8, 1, top, 10000, dev)
+        b.check(b.run(max_q_len=n, max_kv_len=10000, workspace=ws), what=f"n={n}")
