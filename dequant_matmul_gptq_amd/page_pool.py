@@ -14,7 +14,7 @@ class PagePool:
     A sequence is a key the caller picks; its page list is `pages(seq)` and its
     token count `length(seq)`. A page held by several sequences is full and
     never appended to: fork gives the copy its own last page if that one is
-    only partly filled.
+    only partly filled, or cut.
     """
 
     def __init__(self, num_pages: int, page_size: int):
@@ -70,38 +70,39 @@ class PagePool:
         return [pages[t // P] * P + t % P for t in range(at, at + tokens)]
 
     def truncate(self, seq, length: int) -> None:
-        """Forget the tokens from `length` on (rejected drafts). Not past what
-        the sequence shares: a shared page that would become partly filled
-        cannot be appended to, so that is refused (fork instead)."""
+        """Forget the tokens from `length` on (rejected drafts). A shared page
+        that would become partly filled cannot be appended to, so that is
+        refused: fork the sequence up to `length` and free it instead."""
         if not 0 <= length <= self._length[seq]:
             raise ValueError("length must be between 0 and the sequence's own")
         pages, P = self._pages[seq], self.page_size
         keep = -(-length // P)
         if length % P and self._refs[pages[keep - 1]] > 1:
-            raise ValueError("the sequence would end inside a shared page")
+            raise ValueError("the sequence would end inside a shared page: fork it up to that length")
         for p in pages[keep:]:
             self._drop(p)
         del pages[keep:]
         self._length[seq] = length
 
-    def fork(self, seq, new) -> list[tuple[int, int]]:
-        """`new` starts as a copy of `seq`: full pages are shared, a partly
-        filled last page is copied. Returns the copies to run (none or one)."""
+    def fork(self, seq, new, length: int | None = None) -> list[tuple[int, int]]:
+        """`new` starts as a copy of the first `length` tokens of `seq` (None:
+        all): full pages are shared, a page that they fill in part is copied.
+        Returns the copies to run (none or one)."""
         if new in self._pages:
             raise ValueError(f"sequence {new!r} is already in the pool")
-        pages = list(self._pages[seq])
+        length = self._length[seq] if length is None else length
+        if not 0 <= length <= self._length[seq]:
+            raise ValueError("length must be between 0 and the sequence's own")
+        full, part = divmod(length, self.page_size)
+        pages = self._pages[seq][:full]
         copies = []
-        if self._length[seq] % self.page_size:
+        if part:
             if not self._free:
                 raise MemoryError("1 page needed, 0 free")
-            copies.append((pages[-1], self._take()))
-            pages[-1] = copies[0][1]
-            shared = pages[:-1]
-        else:
-            shared = pages
-        for p in shared:
+            copies.append((self._pages[seq][full], self._take()))
+        for p in pages:
             self._refs[p] += 1
-        self._pages[new], self._length[new] = pages, self._length[seq]
+        self._pages[new], self._length[new] = pages + [p for _, p in copies], length
         return copies
 
     def free(self, seq) -> None:

@@ -393,3 +393,72 @@ def test_binding_passes_no_number_cut_to_32_bits():
         with pytest.raises(dq.QlinearError) as e:
             need(*sizes)
         assert e.value.status == status, sizes
+
+
+def test_page_pool_rolls_back_inside_a_shared_page():
+    """Drafts rejected just after a fork at a page boundary: what the fork shares cannot be cut, but forked up to a length."""
+    pool = dq.PagePool(6, 4)
+    mem = {}
+    pool.add("a")
+    for i, s in enumerate(pool.extend("a", 8)):
+        mem[s] = i
+    assert pool.fork("a", "b") == []
+    with pytest.raises(ValueError, match="fork"):
+        pool.truncate("b", 6)
+    copies = pool.fork("b", "c", 6)
+    assert len(copies) == 1 and copies[0][0] == pool.pages("a")[1] and pool.length("c") == 6
+    for src, dst in copies:
+        mem.update({dst * 4 + i: mem[src * 4 + i] for i in range(4)})
+    pool.free("b")
+    new = pool.extend("c", 3)
+    for i, s in enumerate(new):
+        mem[s] = 100 + i
+    read = lambda seq: [mem.get(p * 4 + i) for p in pool.pages(seq) for i in range(4)][:pool.length(seq)]    # noqa: E731
+    assert read("c") == [0, 1, 2, 3, 4, 5, 100, 101, 102] and read("a") == list(range(8))
+    assert pool.pages("c")[0] == pool.pages("a")[0]
+    # at a boundary nothing is copied; up to nothing, nothing is held
+    assert pool.fork("c", "d", 8) == [] and pool.pages("d") == pool.pages("c")[:2]
+    assert pool.fork("c", "e", 0) == [] and pool.pages("e") == [] and pool.length("e") == 0
+    assert pool.fork("c", "f", 9) and pool.length("f") == 9
+    used = pool.num_pages - pool.free_pages
+    assert used == len({p for s in pool.sequences() for p in pool.pages(s)}) == 5
+    for length in (10, -1):
+        with pytest.raises(ValueError):
+            pool.fork("c", "g", length)
+    assert "g" not in pool.sequences() and pool.num_pages - pool.free_pages == used
+    for s in pool.sequences():
+        pool.free(s)
+    assert pool.free_pages == 6
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_page_pool_forks_of_any_length_against_a_model(seed):
+    rng = np.random.default_rng(seed)
+    P, N, token, names = int(rng.integers(1, 6)), 30, 0, 1
+    pool, mem, seqs = dq.PagePool(N, P), [[None] * P for _ in range(N)], {0: []}
+    pool.add(0)
+    for _ in range(300):
+        s = list(seqs)[int(rng.integers(len(seqs)))]
+        op = rng.choice(["extend", "fork", "free", "compact"])
+        copies = []
+        try:
+            if op == "extend":
+                for x in pool.extend(s, int(rng.integers(0, 2 * P))):
+                    mem[x // P][x % P] = token
+                    seqs[s].append(token)
+                    token += 1
+            elif op == "fork" and len(seqs) < 8:
+                n = int(rng.integers(0, len(seqs[s]) + 1))
+                copies = pool.fork(s, names, n)
+                seqs[names] = seqs[s][:n]
+                names += 1
+            elif op == "free" and len(seqs) > 1:
+                pool.free(s)
+                del seqs[s]
+            elif op == "compact":
+                copies = pool.compact()
+        except MemoryError:
+            pass
+        for src, dst in copies:
+            mem[dst] = list(mem[src])
+        _model_check(pool, mem, seqs)
