@@ -89,12 +89,18 @@ class Decoder:
 
     # ---- one step
     def step(self, batch: list[tuple[object, list[int]]]) -> torch.Tensor:
-        """Append each sequence's new tokens; logits float16 [tokens][vocab] of all of them."""
+        """Append each sequence's new tokens; logits float16 [tokens][vocab] of all of them.
+        Raises MemoryError, changing nothing, if the pool has too few free pages."""
         ints = lambda x: torch.tensor(x, dtype=torch.int32, device=self.device)    # noqa: E731
         tokens, positions, slots, starts, lens = [], [], [], [0], []
         for seq, new in batch:
             at = self.pool.length(seq)
-            slots += self.pool.extend(seq, len(new))
+            try:
+                slots += self.pool.extend(seq, len(new))
+            except MemoryError:
+                for (done, taken) in reversed(batch[:len(lens)]):
+                    self.pool.truncate(done, self.pool.length(done) - len(taken))
+                raise
             positions += range(at, at + len(new))
             tokens += new
             starts.append(len(tokens))
