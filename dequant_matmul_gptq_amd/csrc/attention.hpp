@@ -103,9 +103,8 @@ constexpr int kLookAhead = 256;
 constexpr int kMaxLength = INT32_MAX - 1023;
 static_assert(kMaxLength <= INT32_MAX - kLookAhead);
 __host__ __device__ __forceinline__ int bounded_length(int kv_len, int table_width, int page_size) {
-  const int64_t cap = (int64_t)table_width * page_size;
-  const int most = cap < kMaxLength ? (int)cap : kMaxLength;
-  return kv_len < 0 ? 0 : kv_len < most ? kv_len : most;
+  const int64_t len = max(kv_len, 0), cap = (int64_t)table_width * page_size;
+  return min((int)(len < cap ? len : cap), kMaxLength);
 }
 
 // Rows q0 .. q1 - 1 of q, as far as there are such.
@@ -128,7 +127,8 @@ __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_k
 }
 
 __host__ __device__ __forceinline__ int first_seen(int p, int window) {
-  return window > 0 && p >= window ? p - window + 1 : 0;     // no difference of a negative p and any window
+  // Below -1 all p see nothing; their differences to the largest windows would not fit.
+  return window > 0 ? max(0, max(p, -1) - window + 1) : 0;
 }
 
 // The tile of `tile_rows` rows from row0 on (group rows per token).
