@@ -24,12 +24,15 @@
 // Measured: a prompt of 8192 tokens, 64/8 heads of 128, float16: 1160 us, 948
 // TFLOP/s of the visible pairs, 72% of what a library product of 8192 cubed
 // reaches when warm (1325). Its cycles are half matrix products, half softmax
-// and waits, at a clock that the power limit holds near 1.8 GHz: the same call on
-// zeros takes 870 us. Tiles of 32 tokens with the next one's products in
-// between this one's exponentials, ordered by hand, took as many cycles (1160
-// to 1190 us). 511 tokens at 16384 over Q8, 40/40 heads: 237 us, 15 of them the
-// join; its unpacking is hidden (a third fewer instructions there changed nothing).
-// 4096 tokens of 16/4 heads of 256, one workgroup per CU: 261 us, 527 TFLOP/s.
+// and waits, those for the next step's rows (see above) among them, at a clock
+// that the power limit holds near 1.8 GHz: the same call on zeros takes 870 us.
+// Tiles of 32 tokens with the next one's products in between this one's
+// exponentials, ordered by hand, took as many cycles (1160 to 1190 us). 511
+// tokens at 16384 over Q8, 40/40 heads: 235 us, 15 of them the join; its
+// unpacking is hidden (a third fewer instructions there changed nothing). 4096
+// tokens of 16/4 heads of 256, one workgroup per CU by its registers (32 to 57 of
+// them spilled, outside the loops of whole steps but for one): 258 us, 533
+// TFLOP/s; over Q8 / Q6 / Q4 242, 268, 255 us.
 #pragma once
 
 #include <type_traits>
@@ -157,12 +160,12 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     const uint16_t* p = a.q + (w.q0 + tok) * a.q_stride + (int64_t)qh * D + 8 * h;
     // The kernel's scale is positive: a negative one turns q, 0 makes it 0 (NaN
     // where it is not finite).
-    const uint32_t flip = a.scale < 0.0f ? kTops : 0u;
+    const uint32_t flip = a.scale < 0.0f ? kTops : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
       u32x4 v = *reinterpret_cast<const u32x4*>(p + 16 * f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = a.scale == 0.0f ? spread_top(nonfinite_halves(v[e])) : v[e] ^ flip;
+      for (int e = 0; e < 4; ++e) v[e] = ((v[e] ^ flip) & keep) | (spread_top(nonfinite_halves(v[e])) & ~keep);
       const half8 x = __builtin_bit_cast(half8, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) q[f][e] = x[unpacked<B>(e)];
