@@ -265,6 +265,13 @@ __device__ __forceinline__ Costs few_costs(const AttentionArgs& a, const qlinear
 // 128: float16: 16 sequences of 700 tokens 22.1 and 19.6, of 2100 36.1 and 40.9;
 // 64 of 1100 59.9 and 52.9; 48 of 1 to 4000 73.3 and 114; Q4: 64 of 1100 38.3 and
 // 28.8, of 2100 54.8 and 45.6, 128 of 1100 66.9 and 56.8, of 700 42.0 and 44.6.
+//
+// Every workgroup, and every one of the join, goes over all sequences for this,
+// 64 at a time: work that grows with the square of the batch. Single tokens over
+// 600 cached ones, 64/8 heads of 128, float16, us (and the cache's bytes at a
+// large copy's rate): 512 sequences 266 (245), 1024 594 (489), 2048 1417 (979);
+// 8/1 heads: 1024 101 (61), 16384 4933 (979). Batches past a thousand sequences
+// are better cut by the caller.
 struct Spans {
   Costs costs;
   int total, quota, tiles;
