@@ -30,6 +30,11 @@ def _stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
 
 
+# A call's GPU has to be the current one: a default stream's handle is 0 on all
+# GPUs and means that of the current one. Where it is not, the call is made again
+# with it.
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
 _INT_MAX = 2 ** 31 - 1
 
 
@@ -217,6 +222,9 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
     """x float16 [tokens][heads][head_dim] (token stride free) rotated to the
     positions (int32 [tokens]) by the table of rope_table. out may be x."""
     dev = _gpu_of(x, "x")
+    if _current_gpu() != dev:
+        with torch.cuda.device(dev):
+            return rope(x, positions, table, layout, out)
     xp, T, H, D, xs = _rows(x, "x", None, None, None, dev)
     pos, tab, rows, rot = _rope_operands(table, positions, T, dev)
     if out is None:
@@ -237,6 +245,9 @@ def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torc
     negative = not appended). table None: no rotation. q None: only the append.
     """
     dev, D, Hk = cache.device, cache.head_dim, cache.kv_heads
+    if _current_gpu() != dev:
+        with torch.cuda.device(dev):
+            return rope_append(cache, q, k, v, positions, slots, table, layout, q_out)
     kp, T, _, _, ks = _rows(k, "k", None, Hk, D, dev)
     vp, _, _, _, vs = _rows(v, "v", T, Hk, D, dev)
     sp = _operand(slots, "slots", _I32, (T,), dev)
@@ -298,6 +309,10 @@ def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, 
     zeros.
     """
     dev, D = cache.device, cache.head_dim
+    if _current_gpu() != dev:
+        with torch.cuda.device(dev):
+            return paged_attention(cache, q, block_table, kv_len, q_start, max_q_len, max_kv_len, scale, window, out,
+                                   workspace)
     qp, T, H, _, qs = _rows(q, "q", None, None, D, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch][width]")
@@ -340,6 +355,9 @@ def copy_pages(caches, pairs: torch.Tensor) -> None:
     for c in caches:
         if c.device != dev:
             raise ValueError(f"pairs must be on the caches' GPU {c.device}, got {pairs.device}")
+    if caches and _current_gpu() != dev:
+        with torch.cuda.device(dev):
+            return copy_pages(caches, pairs)
     # The structs side by side (ctypes' own array constructor takes 0.3 us each).
     arr = (qlinear_kv_cache * max(1, len(caches))).from_buffer_copy(
         b"".join([c.raw for c in caches]) or bytes(ctypes.sizeof(qlinear_kv_cache)))
@@ -358,6 +376,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual:
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
     dev, shape = _gpu_of(x, "x"), x.shape
+    if _current_gpu() != dev:
+        with torch.cuda.device(dev):
+            return rms_norm(x, weight, eps, residual, out, residual_out)
     K = shape[-1]
     xp = _operand(x, "x", _F16, shape, dev)
     wp = _operand(weight, "weight", _F16, (K,), dev)

@@ -462,3 +462,60 @@ def test_page_pool_forks_of_any_length_against_a_model(seed):
         for src, dst in copies:
             mem[dst] = list(mem[src])
         _model_check(pool, mem, seqs)
+
+
+def test_calls_run_with_their_tensors_gpu_as_the_current_one(monkeypatch):
+    """Also where another one is: the default stream's handle is 0 on every GPU. (No GPU: the library and the
+    device calls stand-ins.)"""
+    from dequant_matmul_gptq_amd import decoder
+    state = dict(current=0, calls=[])
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, state["current"] = state["current"], self.device
+
+        def __exit__(self, *_):
+            state["current"] = self.before
+
+    class Tensor:
+        dtype, shape = torch.float16, torch.Size((3, 64))
+
+        def __init__(self, *shape):
+            self.shape = torch.Size(shape)
+
+        def get_device(self):
+            return 2
+
+        def is_contiguous(self):
+            return True
+
+        def dim(self):
+            return len(self.shape)
+
+        def numel(self):
+            return self.shape.numel()
+
+        def data_ptr(self):
+            return FAKE
+
+    def norm(*args):
+        state["calls"].append((state["current"], args[-1]))
+        return state.get("status", 0)
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(decoder, "_current_gpu", lambda: state["current"], raising=False)
+    monkeypatch.setattr(decoder, "_raw_stream", lambda device: 1000 + device)
+    monkeypatch.setattr(decoder, "lib", lambda: SimpleNamespace(qlinear_rms_norm=norm))
+    x, w, y = Tensor(3, 64), Tensor(64), Tensor(3, 64)
+    assert dq.rms_norm(x, w, out=y) is y
+    assert state["calls"] == [(2, 1002)] and state["current"] == 0
+    state["status"] = INV
+    with pytest.raises(dq.QlinearError):
+        dq.rms_norm(x, w, out=y)
+    assert state["calls"][1:] == [(2, 1002)] and state["current"] == 0
+    state.update(status=0, current=2)
+    dq.rms_norm(x, w, out=y)
+    assert state["calls"][2:] == [(2, 1002)] and state["current"] == 2
