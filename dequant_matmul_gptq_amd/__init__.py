@@ -1,7 +1,8 @@
 """MI355X (gfx950) quantized linear layer: GPTQ 4-bit and EXL2 mixed-bit codes
 unpacked, scaled and fused into the matmul against float16 activations; and the
 operators between a decoder's linear layers: rotary positions, a paged
-key/value cache, attention over it, and the root-mean-square norm.
+key/value cache, attention over it, the root-mean-square norm, and log
+probabilities from the head's logits.
 
 The compute lives in libqlinear.so (hand-written HIP, C ABI in
 include/qlinear.h); this package is its thin Python binding. PyTorch provides
@@ -43,9 +44,11 @@ from ._lib import (  # noqa: F401
     kv_dequant,
 )
 from .decoder import (  # noqa: F401
+    MAX_TOP,
     ROPE_HALF,
     ROPE_INTERLEAVED,
     KVCache,
+    TokenLogprobs,
     copy_pages,
     paged_attention,
     paged_attention_workspace,
@@ -54,5 +57,8 @@ from .decoder import (  # noqa: F401
     rope,
     rope_append,
     rope_table,
+    token_logprobs,
+    token_logprobs_workspace,
+    token_logprobs_workspace_bytes,
 )
 from .page_pool import PagePool  # noqa: F401

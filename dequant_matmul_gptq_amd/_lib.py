@@ -55,10 +55,14 @@ EXPORTS = (
     "qlinear_kv_dequant",
     "qlinear_rope",
     "qlinear_rope_append",
+    "qlinear_norm_rope",
+    "qlinear_norm_rope_append",
     "qlinear_paged_attention_workspace_bytes",
     "qlinear_paged_attention",
     "qlinear_copy_pages",
     "qlinear_rms_norm",
+    "qlinear_token_logprobs_workspace_bytes",
+    "qlinear_token_logprobs",
 )
 
 ACT_NONE = 0
@@ -159,6 +163,11 @@ def lib() -> ctypes.CDLL:
                                               sz, vp]
         L.qlinear_copy_pages.argtypes = [cp, i32, vp, i32, vp]
         L.qlinear_rms_norm.argtypes = [vp, vp, vp, i32, i32, f32, vp, vp, vp]
+        L.qlinear_norm_rope.argtypes = [vp, i64, i32, i32, i32, vp, i32, f32, vp, vp, i32, i32, i32, vp, i64, vp]
+        L.qlinear_norm_rope_append.argtypes = [cp, vp, i64, i32, vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, i32, f32,
+                                               vp, vp, vp, i32, i32, i32, vp]
+        L.qlinear_token_logprobs_workspace_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.qlinear_token_logprobs.argtypes = [vp, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp]
         for name in EXPORTS[1:]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L

@@ -25,6 +25,10 @@ constexpr int64_t kMaxQueryRows = (int64_t)1 << 29;
 // tiles at most) are counted in 32 bits.
 constexpr int64_t kMaxTableSlots = (int64_t)1 << 33;
 
+// Logits of one call: with at most kMaxRows rows its parts (16384 elements at
+// least where there are several) are a grid below 2^24 workgroups.
+constexpr int64_t kMaxLogits = (int64_t)1 << 37;
+
 int check_cache(const qlinear_kv_cache* c) {
   if (!c || !c->k || !c->v || c->num_pages < 1 || c->kv_heads < 1) return QLINEAR_ERR_INVALID_ARGUMENT;
   const int P = c->page_size, D = c->head_dim;
@@ -73,6 +77,18 @@ int check_attention(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_hea
   return QLINEAR_OK;
 }
 
+int check_logprob(int32_t rows, int32_t vocab, int32_t logit_bits, int32_t top, LogprobArgs& a) {
+  if (rows < 0 || vocab < 1 || top < 0 || top > vocab) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if ((logit_bits != 16 && logit_bits != 32) || vocab > QLINEAR_MAX_VOCAB || top > QLINEAR_MAX_TOP ||
+      rows > kMaxRows || (int64_t)rows * vocab > kMaxLogits)
+    return QLINEAR_ERR_UNSUPPORTED;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.f32 = logit_bits == 32;
+  a.top = top;
+  return QLINEAR_OK;
+}
+
 AttentionArgs attention_sizes(int32_t tokens, int32_t q_heads, int32_t batch, int32_t max_q_len, int32_t max_kv_len,
                               int32_t window) {
   AttentionArgs a = {};
@@ -85,21 +101,40 @@ AttentionArgs attention_sizes(int32_t tokens, int32_t q_heads, int32_t batch, in
   return a;
 }
 
-}  // namespace
+// Norm weights of q and k heads: one for all heads, or one a head; NULL: no norm.
+struct Norms {
+  const uint16_t* q = nullptr;
+  int32_t q_heads = 1;
+  const uint16_t* k = nullptr;
+  int32_t k_heads = 1;
+  float eps = 0.0f;
+};
+int set_norms(const Norms& n, int32_t q_heads, int32_t kv_heads, int32_t head_dim, RopeArgs& a) {
+  if (!(n.eps >= 0.0f) || !isfinite(n.eps)) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if ((n.q && n.q_heads != 1 && n.q_heads != q_heads) || (n.k && n.k_heads != 1 && n.k_heads != kv_heads))
+    return QLINEAR_ERR_INVALID_ARGUMENT;
+  if (!aligned(n.q, 16) || !aligned(n.k, 16)) return QLINEAR_ERR_MISALIGNED;
+  a.q_norm = n.q;
+  a.k_norm = n.k;
+  a.q_norm_stride = n.q_heads == 1 ? 0 : head_dim;
+  a.k_norm_stride = n.k_heads == 1 ? 0 : head_dim;
+  a.eps = n.eps;
+  return QLINEAR_OK;
+}
 
-extern "C" {
-
-int qlinear_rope(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t heads, int32_t head_dim,
-                 const int32_t* positions, const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout,
-                 uint16_t* out, int64_t out_stride, void* stream) {
-  if (tokens < 0 || heads < 0 || head_dim < 1 || rot_dim < 1) return QLINEAR_ERR_INVALID_ARGUMENT;
+// rot_dim == 0 needs no positions or table.
+int rotate(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t heads, int32_t head_dim, const Norms& norms,
+           const int32_t* positions, const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout,
+           uint16_t* out, int64_t out_stride, void* stream) {
+  if (tokens < 0 || heads < 0 || head_dim < 1 || rot_dim < 0) return QLINEAR_ERR_INVALID_ARGUMENT;
   if (heads > 65535 || tokens > kMaxRows) return QLINEAR_ERR_UNSUPPORTED;
   if (tokens == 0 || heads == 0) return QLINEAR_OK;
+  RopeArgs a = {};
   int st = check_rotation(head_dim, rot_dim, layout, positions, table, table_rows);
   if (st == QLINEAR_OK) st = check_rows(x, x_stride, heads, head_dim);
   if (st == QLINEAR_OK) st = check_rows(out, out_stride, heads, head_dim);
+  if (st == QLINEAR_OK) st = set_norms(norms, heads, 0, head_dim, a);
   if (st != QLINEAR_OK) return st;
-  RopeArgs a = {};
   a.q = x;
   a.q_stride = x_stride;
   a.q_out = out;
@@ -115,10 +150,10 @@ int qlinear_rope(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t he
   return hip_status(launch_rope(a, (hipStream_t)stream));
 }
 
-int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t q_heads,
-                        const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out,
-                        int64_t q_out_stride, int32_t tokens, const int32_t* positions, const int32_t* slots,
-                        const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout, void* stream) {
+int append(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t q_heads, const uint16_t* k,
+           int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out, int64_t q_out_stride, int32_t tokens,
+           const Norms& norms, const int32_t* positions, const int32_t* slots, const float* table, int32_t table_rows,
+           int32_t rot_dim, int32_t layout, void* stream) {
   int st = check_cache(cache);
   if (st != QLINEAR_OK) return st;
   if (tokens < 0 || q_heads < 0 || rot_dim < 0) return QLINEAR_ERR_INVALID_ARGUMENT;
@@ -130,10 +165,11 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
   if (st == QLINEAR_OK) st = check_rows(v, v_stride, cache->kv_heads, D);
   if (st == QLINEAR_OK && q_heads > 0) st = check_rows(q, q_stride, q_heads, D);
   if (st == QLINEAR_OK && q_heads > 0) st = check_rows(q_out, q_out_stride, q_heads, D);
+  RopeArgs a = {};
+  if (st == QLINEAR_OK) st = set_norms(norms, q_heads, cache->kv_heads, D, a);
   if (st != QLINEAR_OK) return st;
   if (!slots) return QLINEAR_ERR_INVALID_ARGUMENT;
   if (!aligned(slots, 4)) return QLINEAR_ERR_MISALIGNED;
-  RopeArgs a = {};
   a.q = q;
   a.k = k;
   a.v = v;
@@ -152,6 +188,46 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
   a.rot_dim = rot_dim;
   a.layout = layout;
   return hip_status(launch_rope_append(a, *cache, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlinear_rope(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t heads, int32_t head_dim,
+                 const int32_t* positions, const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout,
+                 uint16_t* out, int64_t out_stride, void* stream) {
+  if (rot_dim < 1) return QLINEAR_ERR_INVALID_ARGUMENT;
+  return rotate(x, x_stride, tokens, heads, head_dim, {}, positions, table, table_rows, rot_dim, layout, out,
+                out_stride, stream);
+}
+
+int qlinear_norm_rope(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t heads, int32_t head_dim,
+                      const uint16_t* weight, int32_t weight_heads, float eps, const int32_t* positions,
+                      const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout, uint16_t* out,
+                      int64_t out_stride, void* stream) {
+  if (tokens > 0 && heads > 0 && !weight) return QLINEAR_ERR_INVALID_ARGUMENT;
+  return rotate(x, x_stride, tokens, heads, head_dim, {weight, weight_heads, nullptr, 1, eps}, positions, table,
+                table_rows, rot_dim, layout, out, out_stride, stream);
+}
+
+int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t q_heads,
+                        const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out,
+                        int64_t q_out_stride, int32_t tokens, const int32_t* positions, const int32_t* slots,
+                        const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout, void* stream) {
+  return append(cache, q, q_stride, q_heads, k, k_stride, v, v_stride, q_out, q_out_stride, tokens, {}, positions,
+                slots, table, table_rows, rot_dim, layout, stream);
+}
+
+int qlinear_norm_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t q_heads,
+                             const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out,
+                             int64_t q_out_stride, int32_t tokens, const uint16_t* q_norm, int32_t q_norm_heads,
+                             const uint16_t* k_norm, int32_t k_norm_heads, float eps, const int32_t* positions,
+                             const int32_t* slots, const float* table, int32_t table_rows, int32_t rot_dim,
+                             int32_t layout, void* stream) {
+  return append(cache, q, q_stride, q_heads, k, k_stride, v, v_stride, q_out, q_out_stride, tokens,
+                {q_norm, q_norm_heads, k_norm, k_norm_heads, eps}, positions, slots, table, table_rows, rot_dim, layout,
+                stream);
 }
 
 int qlinear_paged_attention_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,
@@ -227,6 +303,42 @@ int qlinear_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t
       !aligned(residual_out, 16))
     return QLINEAR_ERR_MISALIGNED;
   return hip_status(launch_rms_norm(x, residual, weight, M, K, eps, y, residual_out, (hipStream_t)stream));
+}
+
+int qlinear_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t logit_bits, int32_t top,
+                                           size_t* bytes) {
+  if (!bytes) return QLINEAR_ERR_INVALID_ARGUMENT;
+  LogprobArgs a = {};
+  const int st = check_logprob(rows, vocab, logit_bits, top, a);
+  if (st != QLINEAR_OK) return st;
+  *bytes = rows == 0 ? 0 : logprob_workspace_bytes(a);
+  return QLINEAR_OK;
+}
+
+int qlinear_token_logprobs(const void* logits, int64_t stride, int32_t rows, int32_t vocab, int32_t logit_bits,
+                           const int32_t* tokens, int32_t top, float* logprob, float* entropy, float* top_logprob,
+                           int32_t* top_id, void* workspace, size_t workspace_bytes, void* stream) {
+  LogprobArgs a = {};
+  const int st = check_logprob(rows, vocab, logit_bits, top, a);
+  if (st != QLINEAR_OK) return st;
+  if (rows == 0) return QLINEAR_OK;
+  if (!logits || stride < vocab || (logprob && !tokens) || (top > 0 && (!top_logprob || !top_id)))
+    return QLINEAR_ERR_INVALID_ARGUMENT;
+  if (!aligned(logits, logit_bits / 8) || !aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
+      !aligned(top_logprob, 4) || !aligned(top_id, 4))
+    return QLINEAR_ERR_MISALIGNED;
+  if (!logprob && !entropy && top == 0) return QLINEAR_OK;
+  a.logits = logits;
+  a.stride = stride;
+  a.tokens = tokens;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.top_logprob = top_logprob;
+  a.top_id = top_id;
+  const size_t need = logprob_workspace_need(a);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QLINEAR_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return QLINEAR_ERR_MISALIGNED;
+  return hip_status(launch_logprob(a, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

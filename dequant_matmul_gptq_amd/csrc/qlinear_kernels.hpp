@@ -115,6 +115,10 @@ struct RopeArgs {
   const int32_t *positions, *slots;
   const float* table;
   int table_rows, rot_dim, layout;
+  // Norm weights of q and k heads, one for all (stride 0) or one a head; NULL: no norm.
+  const uint16_t *q_norm, *k_norm;
+  int64_t q_norm_stride, k_norm_stride;
+  float eps;
 };
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_rope_append(const RopeArgs& a, const qlinear_kv_cache& cache, hipStream_t stream);
@@ -143,6 +147,21 @@ hipError_t launch_copy_pages(const qlinear_kv_cache* caches, int count, const in
 // Root-mean-square norm with the residual's addition (rms_norm.hip).
 hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int M, int K,
                            float eps, uint16_t* y, uint16_t* residual_out, hipStream_t stream);
+
+// Log probabilities of given tokens, entropy and top alternatives of logit rows (logprob.hip).
+struct LogprobArgs {
+  const void* logits;        // float16 or float32 [rows][vocab], row stride `stride`
+  int64_t stride;
+  int rows, vocab, f32, top;
+  const int32_t* tokens;
+  float *logprob, *entropy, *top_logprob;
+  int32_t* top_id;
+};
+// What a call takes of its workspace, and what is enough for it and for all
+// with fewer rows, shorter ones or fewer alternatives.
+size_t logprob_workspace_need(const LogprobArgs& a);
+size_t logprob_workspace_bytes(const LogprobArgs& a);
+hipError_t launch_logprob(const LogprobArgs& a, void* ws, hipStream_t stream);
 
 // Streaming-read floor (measurement helper): grid workgroups of 256 threads
 // read `bytes` (a multiple of 16) with `loads` (4, 8 or 16) 16-byte loads in

@@ -11,6 +11,11 @@
 // table's row is read once for them. A wave reads all of its rows' elements
 // before it writes any, so a row may be rotated in place. Quantized blocks
 // are groups of neighbouring lanes, whose maximum takes lane swaps.
+//
+// With norms (NORM), a q or k row is first scaled to x / sqrt(mean x^2 + eps) w:
+// the row's lanes add up its squares by lane swaps, and the scaled elements,
+// the partner's too, stay float32 up to the rotation's rounding. The weight's
+// elements are read along with the row's.
 #include <type_traits>
 
 #include "qlinear_kernels.hpp"
@@ -70,12 +75,27 @@ __device__ __forceinline__ void encode8(const Half8& x, int u, uint32_t* words, 
   if (u % (G / 8) == 0) scales[u / (G / 8)] = __builtin_bit_cast(uint16_t, s16);
 }
 
+// Sum over a row's U neighbouring lanes, u the lane's place among them.
+template <bool POW2>
+__device__ __forceinline__ float row_sum(float v, int u, int U) {
+  if constexpr (POW2) {
+    for (int k = 1; k < U; k <<= 1) v += __shfl_xor(v, k);
+    return v;
+  } else {         // lane u holds the sum of u .. u + 2 k - 1 after a turn
+    for (int k = 1; k < U; k <<= 1) {
+      const float o = __shfl_down(v, k);
+      v += u + k < U ? o : 0.0f;
+    }
+    return __shfl(v, (int)(threadIdx.x & 63) - u);
+  }
+}
+
 // B: 0 rotates q rows only, 16 appends to a float16 cache, 8 / 6 / 4 to a
 // quantized one with blocks of G. Rows of a token: q heads, k heads, v heads.
 // H: rows a thread goes over, all of them read before the first is written;
 // reads past the last row, or of a partner that is not needed, take an address
 // in reach instead of a branch.
-template <int B, int G, int H, bool HALF>
+template <int B, int G, int H, bool HALF, bool NORM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, qlinear_kv_cache c) {
   const int D = a.head_dim, U = D / 8;
   const int lane = threadIdx.x & 63;
@@ -97,6 +117,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, qlinear_kv_c
   const uint16_t* k = a.k + t * a.k_stride;
   const uint16_t* v = a.v + t * a.v_stride;
   Half8 x[H], o[H];      // the row's 8 elements, and in the half layout their partners
+  Half8 wx[H], wo[H];    // weights of both
+  bool normed[H];
 #pragma unroll
   for (int n = 0; n < H; ++n) {
     const int row = min(row0 + n * rows_per_wave, total - 1);
@@ -107,6 +129,14 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, qlinear_kv_c
     }
     x[n].v = *reinterpret_cast<const uint4*>(src + u * 8);
     if constexpr (HALF) o[n].v = *reinterpret_cast<const uint4*>(src + partner * 8);
+    if constexpr (NORM) {
+      const bool is_q = B == 0 || row < a.q_heads;
+      const uint16_t* w = is_q ? a.q_norm : row < a.q_heads + c.kv_heads ? a.k_norm : nullptr;
+      normed[n] = w != nullptr;
+      w = normed[n] ? w + (is_q ? row * a.q_norm_stride : (row - a.q_heads) * a.k_norm_stride) : src;
+      wx[n].v = *reinterpret_cast<const uint4*>(w + u * 8);
+      if constexpr (HALF) wo[n].v = *reinterpret_cast<const uint4*>(w + partner * 8);
+    }
   }
 
   // (cos, sin) of the lane's pairs: 8 in the half layout, 4 else.
@@ -137,13 +167,45 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, qlinear_kv_c
     slots = c.num_pages * c.page_size;
   }
 
+  float inv[H];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int n = 0; n < H; ++n) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += half_value(x[n].b[i]) * half_value(x[n].b[i]);
+      inv[n] = 1.0f / sqrtf(row_sum<B != 0>(sum, u, U) / (float)D + a.eps);
+    }
+  }
+
 #pragma unroll
   for (int n = 0; n < H; ++n) {
     const int row = row0 + n * rows_per_wave;
     if (row >= total) break;
     const bool is_q = B == 0 || row < a.q_heads;
     const bool is_v = B != 0 && row >= a.q_heads + c.kv_heads;
-    if (rotated && !is_v) {
+    if (NORM && normed[n]) {
+#pragma clang fp contract(off)
+      float f[8];
+      Half8 r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = half_value(x[n].b[i]) * inv[n] * half_value(wx[n].b[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float y = f[i];
+        if (rotated) {
+          if constexpr (HALF) {
+            const float s = half_value(o[n].b[i]) * inv[n] * half_value(wo[n].b[i]) * cs[2 * i + 1];
+            y = y * cs[2 * i] + (low ? -s : s);
+          } else {
+            const float s = f[i ^ 1] * cs[i / 2 * 2 + 1];
+            y = y * cs[i / 2 * 2] + (i % 2 ? s : -s);
+          }
+        }
+        r.b[i] = __builtin_bit_cast(uint16_t, (_Float16)y);
+      }
+      x[n] = r;
+    } else if (rotated && !is_v) {
 #pragma clang fp contract(off)
       Half8 r;
       if constexpr (HALF) {
@@ -192,10 +254,11 @@ hipError_t launch(const RopeArgs& a, const qlinear_kv_cache& c, hipStream_t stre
     rows = (total + rows_per_group * groups - 1) / (rows_per_group * groups);
   }
   const dim3 grid((unsigned)a.tokens, (unsigned)groups);
-  const bool half = a.layout == QLINEAR_ROPE_HALF;
+  const bool half = a.layout == QLINEAR_ROPE_HALF, norm = a.q_norm || a.k_norm;
   auto go = [&](auto h) {
     constexpr int H = decltype(h)::value;
-    auto kernel = half ? rope_kernel<B, G, H, true> : rope_kernel<B, G, H, false>;
+    auto kernel = norm ? (half ? rope_kernel<B, G, H, true, true> : rope_kernel<B, G, H, false, true>)
+                       : (half ? rope_kernel<B, G, H, true, false> : rope_kernel<B, G, H, false, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a, c);
     return hipGetLastError();
   };

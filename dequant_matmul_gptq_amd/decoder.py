@@ -1,14 +1,16 @@
 """Binding of the operators between a decoder's linear layers: the paged
-key/value cache, rotary positions, attention, page copies and the norm
-(argument marshalling; the one computation here is the host-made table of
-rotary angles). Checks, streams and errors are those of the other calls:
-wrong tensors raise ValueError, a non-zero status QlinearError.
+key/value cache, rotary positions, attention, page copies and the norm, and of
+what is read off the head's logits (argument marshalling; the one computation
+here is the host-made table of rotary angles). Checks, streams and errors are
+those of the other calls: wrong tensors raise ValueError, a non-zero status
+QlinearError.
 """
 
 from __future__ import annotations
 
 import ctypes
 import math
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -217,37 +219,64 @@ def _rope_operands(table: torch.Tensor, positions: torch.Tensor, tokens: int, de
             _operand(table, "table", _F32, (rows, half, 2), device), rows, 2 * half)
 
 
-def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: int = ROPE_HALF,
-         out: torch.Tensor | None = None) -> torch.Tensor:
+def _norm_weight(w: torch.Tensor | None, name: str, heads: int, dim: int, device: int):
+    """Pointer and number of rows of a norm's weight, [head_dim] or [heads][head_dim]."""
+    if w is None:
+        return None, 1
+    if w.dim() == 1:
+        return _operand(w, name, _F16, (dim,), device), 1
+    return _operand(w, name, _F16, (heads, dim), device), heads
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor | None, table: torch.Tensor | None, layout: int = ROPE_HALF,
+         out: torch.Tensor | None = None, norm: torch.Tensor | None = None, eps: float = 1e-6) -> torch.Tensor:
     """x float16 [tokens][heads][head_dim] (token stride free) rotated to the
-    positions (int32 [tokens]) by the table of rope_table. out may be x."""
+    positions (int32 [tokens]) by the table of rope_table. out may be x.
+
+    norm float16 [head_dim] or [heads][head_dim]: each head's row is first
+    x / sqrt(mean(x^2) + eps) * norm, in the same pass (table None: that alone).
+    """
     dev = _gpu_of(x, "x")
     if _current_gpu() != dev:
         with torch.cuda.device(dev):
-            return rope(x, positions, table, layout, out)
+            return rope(x, positions, table, layout, out, norm, eps)
     xp, T, H, D, xs = _rows(x, "x", None, None, None, dev)
-    pos, tab, rows, rot = _rope_operands(table, positions, T, dev)
+    pos = tab = None
+    rows = rot = 0
+    if table is not None:
+        if positions is None:
+            raise ValueError("a table needs positions")
+        pos, tab, rows, rot = _rope_operands(table, positions, T, dev)
+    elif norm is None:
+        raise ValueError("a call without a table needs a norm")
+    wp, wh = _norm_weight(norm, "norm", H, D, dev)
     if out is None:
         out = torch.empty((T, H, D), dtype=_F16, device=x.device)
     op, _, _, _, ost = _rows(out, "out", T, H, D, dev)
     if (T | H | D | rows | rot) >> 31:
-        T, H, D, rows, rot = _int32(T, H, D, rows, rot)
-    _check(lib().qlinear_rope(xp, xs, T, H, D, pos, tab, rows, rot, layout, op, ost, _stream(dev)), "qlinear_rope")
+        T, H, D, rows, rot, wh = _int32(T, H, D, rows, rot, wh)
+    if norm is None:
+        _check(lib().qlinear_rope(xp, xs, T, H, D, pos, tab, rows, rot, layout, op, ost, _stream(dev)), "qlinear_rope")
+    else:
+        _check(lib().qlinear_norm_rope(xp, xs, T, H, D, wp, wh, eps, pos, tab, rows, rot, layout, op, ost,
+                                       _stream(dev)), "qlinear_norm_rope")
     return out
 
 
 def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                 positions: torch.Tensor | None, slots: torch.Tensor, table: torch.Tensor | None,
-                layout: int = ROPE_HALF, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+                layout: int = ROPE_HALF, q_out: torch.Tensor | None = None, q_norm: torch.Tensor | None = None,
+                k_norm: torch.Tensor | None = None, eps: float = 1e-6) -> torch.Tensor | None:
     """Rotate q [tokens][q_heads][head_dim] (returned; q_out may be q) and k
     [tokens][kv_heads][head_dim] to the positions, and write k and v to the
     cache's slots (int32 [tokens]: page * page_size + place in the page,
     negative = not appended). table None: no rotation. q None: only the append.
+    q_norm, k_norm: norms of their heads before the rotation, as in rope.
     """
     dev, D, Hk = cache.device, cache.head_dim, cache.kv_heads
     if _current_gpu() != dev:
         with torch.cuda.device(dev):
-            return rope_append(cache, q, k, v, positions, slots, table, layout, q_out)
+            return rope_append(cache, q, k, v, positions, slots, table, layout, q_out, q_norm, k_norm, eps)
     kp, T, _, _, ks = _rows(k, "k", None, Hk, D, dev)
     vp, _, _, _, vs = _rows(v, "v", T, Hk, D, dev)
     sp = _operand(slots, "slots", _I32, (T,), dev)
@@ -264,10 +293,19 @@ def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torc
         op, _, _, _, ost = _rows(q_out, "q_out", T, heads, D, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    elif q_norm is not None:
+        raise ValueError("q_norm without q")
     if (T | heads | rows | rot) >> 31:
         T, heads, rows, rot = _int32(T, heads, rows, rot)
-    _check(lib().qlinear_rope_append(cache.ref, qp, qs, heads, kp, ks, vp, vs, op, ost, T, pos, sp, tab, rows, rot,
-                                     layout, _stream(dev)), "qlinear_rope_append")
+    if q_norm is None and k_norm is None:
+        _check(lib().qlinear_rope_append(cache.ref, qp, qs, heads, kp, ks, vp, vs, op, ost, T, pos, sp, tab, rows, rot,
+                                         layout, _stream(dev)), "qlinear_rope_append")
+        return q_out
+    qn, qn_heads = _norm_weight(q_norm, "q_norm", heads, D, dev)
+    kn, kn_heads = _norm_weight(k_norm, "k_norm", Hk, D, dev)
+    _check(lib().qlinear_norm_rope_append(cache.ref, qp, qs, heads, kp, ks, vp, vs, op, ost, T, qn, qn_heads, kn,
+                                          kn_heads, eps, pos, sp, tab, rows, rot, layout, _stream(dev)),
+           "qlinear_norm_rope_append")
     return q_out
 
 
@@ -391,4 +429,85 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual:
     if (M | K) >> 31:
         M, K = _int32(M, K)
     _check(lib().qlinear_rms_norm(xp, rp, wp, M, K, eps, op, hp, _stream(dev)), "qlinear_rms_norm")
+    return out
+
+
+# ---------------------------------------------------------------- log probabilities
+
+MAX_TOP = 64
+
+
+class TokenLogprobs(NamedTuple):
+    """Results of token_logprobs; None where one was not asked for."""
+    logprob: torch.Tensor | None          # float32 [rows]
+    entropy: torch.Tensor | None          # float32 [rows]
+    top_logprob: torch.Tensor | None      # float32 [rows][top]
+    top_id: torch.Tensor | None           # int32 [rows][top]
+
+
+def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int = 0, dtype: torch.dtype = torch.float16) -> int:
+    n = ctypes.c_size_t(0)
+    sizes = _int32(int(rows), int(vocab), 8 * dtype.itemsize, int(top))
+    _check(lib().qlinear_token_logprobs_workspace_bytes(*sizes, ctypes.byref(n)),
+           "qlinear_token_logprobs_workspace_bytes")
+    return int(n.value)
+
+
+def token_logprobs_workspace(rows: int, vocab: int, top: int = 0, dtype: torch.dtype = torch.float16,
+                             device="cuda") -> torch.Tensor:
+    """A token_logprobs workspace for calls of up to these sizes with logits of
+    this type (scratch: needs no initialization; calls that may overlap in time
+    must not share one)."""
+    n = token_logprobs_workspace_bytes(rows, vocab, top, dtype)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0, entropy: bool = True,
+                   out: TokenLogprobs | None = None, workspace: torch.Tensor | None = None) -> TokenLogprobs:
+    """What rows of logits say (natural logarithms): the log probabilities of
+    the given tokens (int32 [rows]), the entropies, and the `top` likeliest
+    tokens with their log probabilities, largest first, equal ones by index.
+
+    logits float16 or float32 [rows][vocab], row stride free. A row that holds
+    +infinity or NaN, or -infinity alone, has NaN for log probabilities and
+    entropy, and so has a token outside the vocabulary. out: a result of a call
+    with the same rows, top, tokens and entropy, written again.
+    """
+    dev = _gpu_of(logits, "logits")
+    if _current_gpu() != dev:
+        with torch.cuda.device(dev):
+            return token_logprobs(logits, tokens, top, entropy, out, workspace)
+    if logits.dim() != 2 or (logits.dtype is not _F16 and logits.dtype is not _F32):
+        raise ValueError(f"logits must be float16 or float32 [rows][vocab], got {logits.dtype} {tuple(logits.shape)}")
+    R, V = logits.shape
+    stride, along = logits.stride()
+    if V > 1 and along != 1:
+        raise ValueError("logits: the elements of a row must be contiguous")
+    if R < 2:
+        stride = V
+    bits = 16 if logits.dtype is _F16 else 32
+    tp = None if tokens is None else _operand(tokens, "tokens", _I32, (R,), dev)
+    if out is None:
+        f32 = dict(dtype=_F32, device=logits.device)
+        wide = (R, top) if 0 < top else None
+        out = TokenLogprobs(None if tp is None else torch.empty(R, **f32), torch.empty(R, **f32) if entropy else None,
+                            None if wide is None else torch.empty(wide, **f32),
+                            None if wide is None else torch.empty(wide, dtype=_I32, device=logits.device))
+    wanted = (tokens is not None, bool(entropy), top > 0, top > 0)
+    lp, ep, vp, ip = (_operand(t, name, dtype, shape, dev) if w and t is not None else None for t, name, dtype, shape, w in
+                      zip(out, TokenLogprobs._fields, (_F32, _F32, _F32, _I32), ((R,), (R,), (R, top), (R, top)), wanted))
+    if any(w != (t is not None) for w, t in zip(wanted, out)):
+        raise ValueError("out must hold what is asked for and None for the rest")
+    if (R | V | top) >> 31:
+        R, V, top = _int32(R, V, top)
+    n = ctypes.c_size_t(0)
+    if workspace is None:
+        _check(lib().qlinear_token_logprobs_workspace_bytes(R, V, bits, top, ctypes.byref(n)),
+               "qlinear_token_logprobs_workspace_bytes")
+        if n.value:
+            workspace = torch.empty(n.value, dtype=_U8, device=logits.device)
+    size = 0 if workspace is None else workspace.numel()
+    wp = None if workspace is None else _operand(workspace, "workspace", _U8, (size,), dev)
+    _check(lib().qlinear_token_logprobs(logits.data_ptr(), stride, R, V, bits, tp, top, lp, ep, vp, ip, wp, size,
+                                        _stream(dev)), "qlinear_token_logprobs")
     return out

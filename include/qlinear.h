@@ -453,6 +453,22 @@ int qlinear_rope(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t he
                  uint16_t* out, int64_t out_stride, void* stream);
 
 /*
+ * The same after a root-mean-square norm of every head's row:
+ *   x^[e] = x[e] / sqrt(mean_e x[e]^2 + eps) * weight[e]
+ * over the head_dim elements, then the rotation of x^. The norm and the
+ * rotation are float32 and the result is rounded once to float16.
+ *   weight : float16 [head_dim] (weight_heads == 1), or one for every head,
+ *            [heads][head_dim] (weight_heads == heads)
+ * rot_dim == 0 is the norm alone (positions and table may be NULL). Other
+ * errors: INVALID_ARGUMENT (weight NULL, another weight_heads, eps negative or
+ * not finite), MISALIGNED (weight 16 bytes).
+ */
+int qlinear_norm_rope(const uint16_t* x, int64_t x_stride, int32_t tokens, int32_t heads, int32_t head_dim,
+                      const uint16_t* weight, int32_t weight_heads, float eps, const int32_t* positions,
+                      const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout, uint16_t* out,
+                      int64_t out_stride, void* stream);
+
+/*
  * The rotary step of a layer and its append to the cache in one launch: q is
  * rotated into q_out, k is rotated and v taken as it is into the cache slots
  * slots[t], for a quantized cache through the codec (on the float16 rotated
@@ -472,6 +488,19 @@ int qlinear_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_
                         const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out,
                         int64_t q_out_stride, int32_t tokens, const int32_t* positions, const int32_t* slots,
                         const float* table, int32_t table_rows, int32_t rot_dim, int32_t layout, void* stream);
+
+/*
+ * qlinear_rope_append of models that norm each head of q and k before the
+ * rotation, in the same launch: q and k rows as in qlinear_norm_rope, v as it
+ * is. q_norm, k_norm: float16 [head_dim] (q_norm_heads, k_norm_heads == 1) or
+ * [q_heads][head_dim], [kv_heads][head_dim]; NULL: no norm of these rows.
+ */
+int qlinear_norm_rope_append(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t q_heads,
+                             const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* q_out,
+                             int64_t q_out_stride, int32_t tokens, const uint16_t* q_norm, int32_t q_norm_heads,
+                             const uint16_t* k_norm, int32_t k_norm_heads, float eps, const int32_t* positions,
+                             const int32_t* slots, const float* table, int32_t table_rows, int32_t rot_dim,
+                             int32_t layout, void* stream);
 
 /*
  * Attention of each sequence's new tokens over its cached ones, causal. A
@@ -555,6 +584,39 @@ int qlinear_copy_pages(const qlinear_kv_cache* caches_host, int32_t count, const
  */
 int qlinear_rms_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int32_t M, int32_t K,
                      float eps, uint16_t* y, uint16_t* residual_out, void* stream);
+
+/*
+ * What a row of logits x (the output head's, or a sampler's) says, natural
+ * logarithms, float32:
+ *   logprob[r]  = log p_r[tokens[r]],  p_r = softmax(x[r])
+ *   entropy[r]  = -sum_i p_r[i] log p_r[i]    (0 log 0 = 0)
+ *   top_id[r][j], top_logprob[r][j] : the j-th largest logit's index and its
+ *                 log probability, j < top; equal logits (both zeros among
+ *                 them) in the order of their indexes, NaN before all others
+ *   logits : float16 (logit_bits 16) or float32 (32) [rows][vocab], row r at
+ *            logits + r * stride elements; any stride >= vocab and any
+ *            alignment of the elements' own
+ *   tokens : int32 [rows]; outside 0 .. vocab - 1 gives NaN
+ * A logit of -infinity is a token that cannot come (log probability
+ * -infinity). A row of nothing else, and one that holds +infinity or NaN, has
+ * no distribution: its log probabilities and entropy are NaN, top_id is as
+ * above. Each output may be NULL if it is not wanted (tokens too without
+ * logprob; top_logprob and top_id with top == 0).
+ *   workspace : qlinear_token_logprobs_workspace_bytes of the same sizes or
+ *               larger ones with the same logit_bits. Scratch
+ * rows == 0 is a no-op. Errors: INVALID_ARGUMENT (rows < 0, vocab < 1, top < 0,
+ * top > vocab, stride < vocab, NULL), UNSUPPORTED (another logit_bits, top >
+ * QLINEAR_MAX_TOP, vocab > QLINEAR_MAX_VOCAB, rows >= 2^22, rows * vocab past
+ * 2^37), MISALIGNED (logits by their size, workspace 16 bytes, the others 4),
+ * WORKSPACE.
+ */
+#define QLINEAR_MAX_TOP 64
+#define QLINEAR_MAX_VOCAB (1 << 22)
+int qlinear_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t logit_bits, int32_t top,
+                                           size_t* bytes);
+int qlinear_token_logprobs(const void* logits, int64_t stride, int32_t rows, int32_t vocab, int32_t logit_bits,
+                           const int32_t* tokens, int32_t top, float* logprob, float* entropy, float* top_logprob,
+                           int32_t* top_id, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * On-the-fly LoRA update of a linear layer (ExLlamaV2 project page, LoRA
