@@ -51,6 +51,9 @@ from .decoder import (  # noqa: F401
     TokenLogprobs,
     copy_pages,
     paged_attention,
+    paged_attention_shared,
+    paged_attention_shared_workspace,
+    paged_attention_shared_workspace_bytes,
     paged_attention_workspace,
     paged_attention_workspace_bytes,
     rms_norm,

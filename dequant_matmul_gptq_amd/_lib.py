@@ -59,6 +59,10 @@ EXPORTS = (
     "qlinear_norm_rope_append",
     "qlinear_paged_attention_workspace_bytes",
     "qlinear_paged_attention",
+    "qlinear_paged_attention_sinks_workspace_bytes",
+    "qlinear_paged_attention_sinks",
+    "qlinear_paged_attention_shared_workspace_bytes",
+    "qlinear_paged_attention_shared",
     "qlinear_copy_pages",
     "qlinear_rms_norm",
     "qlinear_token_logprobs_workspace_bytes",
@@ -161,6 +165,14 @@ def lib() -> ctypes.CDLL:
         L.qlinear_paged_attention_workspace_bytes.argtypes = [cp, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
         L.qlinear_paged_attention.argtypes = [cp, vp, i64, i32, i32, i32, vp, vp, vp, i32, i32, i32, f32, i32, vp, vp,
                                               sz, vp]
+        L.qlinear_paged_attention_sinks_workspace_bytes.argtypes = [cp, i32, i32, i32, i32, i32, i32, i32,
+                                                                    ctypes.POINTER(sz)]
+        L.qlinear_paged_attention_sinks.argtypes = [cp, vp, i64, i32, i32, i32, vp, vp, vp, i32, i32, i32, f32, i32,
+                                                    i32, vp, vp, sz, vp]
+        L.qlinear_paged_attention_shared_workspace_bytes.argtypes = [cp, i32, i32, i32, i32, i32, i32, i32,
+                                                                     ctypes.POINTER(sz)]
+        L.qlinear_paged_attention_shared.argtypes = [cp, vp, i64, i32, i32, i32, vp, vp, vp, i32, i32, vp, vp, i32,
+                                                     i32, i32, f32, vp, vp, sz, vp]
         L.qlinear_copy_pages.argtypes = [cp, i32, vp, i32, vp]
         L.qlinear_rms_norm.argtypes = [vp, vp, vp, i32, i32, f32, vp, vp, vp]
         L.qlinear_norm_rope.argtypes = [vp, i64, i32, i32, i32, vp, i32, f32, vp, vp, i32, i32, i32, vp, i64, vp]

@@ -5,7 +5,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "qlinear_kernels.hpp"
+#include "attention.hpp"
 
 namespace {
 
@@ -21,6 +21,8 @@ constexpr int kMaxRows = (1 << 22) - 1;
 // Query rows of one attention call (a workgroup of 256 threads takes 128 rows
 // of a sequence and key/value head, or fewer where a sequence ends).
 constexpr int64_t kMaxQueryRows = (int64_t)1 << 29;
+// With shared prefixes a wave, or four below a million rows, joins each row.
+constexpr int64_t kMaxSharedRows = (int64_t)1 << 25;
 // Token slots that a call's block tables name: its steps (32 tokens, four row
 // tiles at most) are counted in 32 bits.
 constexpr int64_t kMaxTableSlots = (int64_t)1 << 33;
@@ -87,6 +89,44 @@ int check_logprob(int32_t rows, int32_t vocab, int32_t logit_bits, int32_t top, 
   a.f32 = logit_bits == 32;
   a.top = top;
   return QLINEAR_OK;
+}
+
+// The rest of what a call is checked for; `rows` of block tables.
+int check_attention_call(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t tokens,
+                         int32_t q_heads, int32_t batch, const int32_t* q_start, const int32_t* kv_len,
+                         const int32_t* block_table, int32_t table_width, float scale, const uint16_t* out,
+                         int64_t rows) {
+  if (table_width < 1 || !isfinite(scale)) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if (!q_start && tokens % batch != 0) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if (rows * table_width > kMaxTableSlots / cache->page_size) return QLINEAR_ERR_UNSUPPORTED;
+  const int st = check_rows(q, q_stride, q_heads, cache->head_dim);
+  if (st != QLINEAR_OK) return st;
+  if (!kv_len || !block_table || !out) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if (!aligned(out, 16) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4))
+    return QLINEAR_ERR_MISALIGNED;
+  return QLINEAR_OK;
+}
+
+// Sizes of a call with shared prefixes and of its workspace query.
+int check_shared(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads, int32_t batch, int32_t max_q_len,
+                 int32_t max_kv_len, int32_t groups, int32_t max_shared_len) {
+  const int st = check_attention(cache, tokens, q_heads, batch, max_q_len, max_kv_len, 0);
+  if (st != QLINEAR_OK) return st;
+  if (groups < 1 || max_shared_len < 0) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if ((int64_t)batch + groups > 65535 || ((int64_t)batch + groups) * cache->kv_heads > kMaxQueryRows / 128 ||
+      (int64_t)tokens * q_heads > kMaxSharedRows)
+    return QLINEAR_ERR_UNSUPPORTED;
+  return QLINEAR_OK;
+}
+
+ViewArgs view_sizes(const AttentionArgs& sizes, int32_t sinks, int32_t groups, int32_t max_shared_len) {
+  ViewArgs a = {};
+  static_cast<AttentionArgs&>(a) = sizes;
+  a.batch += groups;
+  a.sinks = sinks;
+  a.groups = groups;
+  a.max_shared_len = max_shared_len;
+  return a;
 }
 
 AttentionArgs attention_sizes(int32_t tokens, int32_t q_heads, int32_t batch, int32_t max_q_len, int32_t max_kv_len,
@@ -251,14 +291,9 @@ int qlinear_paged_attention(const qlinear_kv_cache* cache, const uint16_t* q, in
   int st = check_attention(cache, tokens, q_heads, batch, max_q_len, max_kv_len, window);
   if (st != QLINEAR_OK) return st;
   if (tokens == 0 || batch == 0) return QLINEAR_OK;
-  if (table_width < 1 || !isfinite(scale)) return QLINEAR_ERR_INVALID_ARGUMENT;
-  if (!q_start && tokens % batch != 0) return QLINEAR_ERR_INVALID_ARGUMENT;
-  if ((int64_t)batch * table_width > kMaxTableSlots / cache->page_size) return QLINEAR_ERR_UNSUPPORTED;
-  st = check_rows(q, q_stride, q_heads, cache->head_dim);
+  st = check_attention_call(cache, q, q_stride, tokens, q_heads, batch, q_start, kv_len, block_table, table_width, scale,
+                            out, batch);
   if (st != QLINEAR_OK) return st;
-  if (!kv_len || !block_table || !out) return QLINEAR_ERR_INVALID_ARGUMENT;
-  if (!aligned(out, 16) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4))
-    return QLINEAR_ERR_MISALIGNED;
   AttentionArgs a = attention_sizes(tokens, q_heads, batch, max_q_len, max_kv_len, window);
   a.q = q;
   a.q_stride = q_stride;
@@ -272,6 +307,93 @@ int qlinear_paged_attention(const qlinear_kv_cache* cache, const uint16_t* q, in
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLINEAR_ERR_WORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return QLINEAR_ERR_MISALIGNED;
   return hip_status(launch_paged_attention(*cache, a, workspace, (hipStream_t)stream));
+}
+
+int qlinear_paged_attention_sinks_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,
+                                                  int32_t batch, int32_t max_q_len, int32_t max_kv_len, int32_t window,
+                                                  int32_t sinks, size_t* bytes) {
+  if (!bytes) return QLINEAR_ERR_INVALID_ARGUMENT;
+  const int st = check_attention(cache, tokens, q_heads, batch, max_q_len, max_kv_len, window);
+  if (st != QLINEAR_OK) return st;
+  if (sinks < 0) return QLINEAR_ERR_INVALID_ARGUMENT;
+  *bytes = tokens == 0 || batch == 0
+               ? 0
+               : sinks_attention_workspace_bytes(
+                     *cache, view_sizes(attention_sizes(tokens, q_heads, batch, max_q_len, max_kv_len, window), sinks, 0, 0));
+  return QLINEAR_OK;
+}
+
+int qlinear_paged_attention_sinks(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t tokens,
+                                  int32_t q_heads, int32_t batch, const int32_t* q_start, const int32_t* kv_len,
+                                  const int32_t* block_table, int32_t table_width, int32_t max_q_len,
+                                  int32_t max_kv_len, float scale, int32_t window, int32_t sinks, uint16_t* out,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_attention(cache, tokens, q_heads, batch, max_q_len, max_kv_len, window);
+  if (st != QLINEAR_OK) return st;
+  if (sinks < 0) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if (tokens == 0 || batch == 0) return QLINEAR_OK;
+  st = check_attention_call(cache, q, q_stride, tokens, q_heads, batch, q_start, kv_len, block_table, table_width, scale,
+                            out, batch);
+  if (st != QLINEAR_OK) return st;
+  ViewArgs a = view_sizes(attention_sizes(tokens, q_heads, batch, max_q_len, max_kv_len, window), sinks, 0, 0);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.block_table = block_table;
+  a.table_width = table_width;
+  a.scale = scale;
+  a.out = out;
+  const size_t need = sinks_attention_workspace_need(*cache, a);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QLINEAR_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return QLINEAR_ERR_MISALIGNED;
+  return hip_status(launch_sinks_attention(*cache, a, workspace, (hipStream_t)stream));
+}
+
+int qlinear_paged_attention_shared_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,
+                                                   int32_t batch, int32_t max_q_len, int32_t max_kv_len,
+                                                   int32_t groups, int32_t max_shared_len, size_t* bytes) {
+  if (!bytes) return QLINEAR_ERR_INVALID_ARGUMENT;
+  const int st = check_shared(cache, tokens, q_heads, batch, max_q_len, max_kv_len, groups, max_shared_len);
+  if (st != QLINEAR_OK) return st;
+  *bytes = tokens == 0 || batch == 0
+               ? 0
+               : shared_attention_workspace_bytes(
+                     *cache, view_sizes(attention_sizes(tokens, q_heads, batch, max_q_len, max_kv_len, 0), 0, groups,
+                                        max_shared_len));
+  return QLINEAR_OK;
+}
+
+int qlinear_paged_attention_shared(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t tokens,
+                                   int32_t q_heads, int32_t batch, const int32_t* q_start, const int32_t* kv_len,
+                                   const int32_t* block_table, int32_t table_width, int32_t groups,
+                                   const int32_t* shared_start, const int32_t* shared_len, int32_t max_q_len,
+                                   int32_t max_kv_len, int32_t max_shared_len, float scale, uint16_t* out,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_shared(cache, tokens, q_heads, batch, max_q_len, max_kv_len, groups, max_shared_len);
+  if (st != QLINEAR_OK) return st;
+  if (tokens == 0 || batch == 0) return QLINEAR_OK;
+  st = check_attention_call(cache, q, q_stride, tokens, q_heads, batch, q_start, kv_len, block_table, table_width, scale,
+                            out, (int64_t)batch + groups);
+  if (st != QLINEAR_OK) return st;
+  if (!shared_len || (!shared_start && groups != 1)) return QLINEAR_ERR_INVALID_ARGUMENT;
+  if (!aligned(shared_start, 4) || !aligned(shared_len, 4)) return QLINEAR_ERR_MISALIGNED;
+  ViewArgs a =
+      view_sizes(attention_sizes(tokens, q_heads, batch, max_q_len, max_kv_len, 0), 0, groups, max_shared_len);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.block_table = block_table;
+  a.table_width = table_width;
+  a.scale = scale;
+  a.out = out;
+  a.shared_start = shared_start;
+  a.shared_len = shared_len;
+  const size_t need = shared_attention_workspace_need(*cache, a);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QLINEAR_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return QLINEAR_ERR_MISALIGNED;
+  return hip_status(launch_shared_attention(*cache, a, workspace, (hipStream_t)stream));
 }
 
 int qlinear_copy_pages(const qlinear_kv_cache* caches_host, int32_t count, const int32_t* pairs, int32_t moves,

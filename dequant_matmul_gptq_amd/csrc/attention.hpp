@@ -14,12 +14,45 @@
 // S^T, rounded to float16, are the B operand of the second product as they
 // stand, if its k index is counted in the order in which S^T's rows lie in
 // the lanes. No weight crosses a lane.
+//
+// Views (ViewArgs): calls whose rows see other tokens than the last ones, by the
+// same kernels in instances of their own.
+//   Sinks: with a window, a sequence's first tokens are seen too. The steps
+//   between them and the window are left out: a tile's steps are numbered
+//   without them (Item::gap).
+//   Shared prefixes: groups of sequences whose first tokens are the same cache
+//   slots. A group's rows over its shared tokens, all of which they all see,
+//   stand before the batch as a sequence of their own, and each sequence starts
+//   after them; what both leave, float32, is joined as parts of a row are.
 #pragma once
+
+#include <type_traits>
 
 #include "qlinear_kernels.hpp"
 
 namespace qlinear {
+
+// A call with sinks (groups == 0) or shared prefixes (groups > 0, no window, no
+// sinks): batch is then groups + sequences.
+struct ViewArgs : AttentionArgs {
+  int sinks, groups;
+  const int32_t *shared_start, *shared_len;      // shared_start NULL: one group of all
+  int max_shared_len;
+};
+
+// What a call takes of its workspace, and what is enough for it and for all
+// smaller ones (attention_views.hip).
+size_t sinks_attention_workspace_need(const qlinear_kv_cache& cache, const ViewArgs& a);
+size_t sinks_attention_workspace_bytes(const qlinear_kv_cache& cache, const ViewArgs& a);
+hipError_t launch_sinks_attention(const qlinear_kv_cache& cache, const ViewArgs& a, void* ws, hipStream_t stream);
+size_t shared_attention_workspace_need(const qlinear_kv_cache& cache, const ViewArgs& a);
+size_t shared_attention_workspace_bytes(const qlinear_kv_cache& cache, const ViewArgs& a);
+hipError_t launch_shared_attention(const qlinear_kv_cache& cache, const ViewArgs& a, void* ws, hipStream_t stream);
+
 namespace attn {
+
+template <class Args>
+constexpr bool kIsView = std::is_same_v<Args, ViewArgs>;
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
@@ -48,6 +81,10 @@ struct Plan {
   int chunk;
   int workers, slots, whole;
   int min_rows, max_rows;
+  // Views: tiles of a sequence (few-row kernel) or of all (chunk kernel) at most;
+  // whether each row of the cache is read by one workgroup.
+  int tiles;
+  bool once;
 };
 constexpr int kStep = 32;          // tokens of a step, few-row kernel
 constexpr int kChunkRows = 128;    // rows of a tile, chunk kernel
@@ -73,10 +110,19 @@ inline int64_t chunk_tiles(const AttentionArgs& a, int group) {
 // [splits][rows of the output]. Few-row kernel: a worker's span starts and
 // ends inside a tile, and what is between are whole tiles, so a worker has two
 // partial results at most: [workers][kv_heads][2][plan.rows].
+// Shared prefixes leave partial results where others write the output. All
+// rows of those stand in one array: whole tiles [2][rows of the output] (0: of a
+// prefix, 1: of a sequence's own tokens), the chunk kernel's ranges
+// [splits][chunk_kinds][rows] from row chunk0 on, the few-row kernel's from few0
+// on. rows: of the output.
 struct Partials {
   float* o;
   float2* ml;
   int64_t rows;
+};
+struct ViewPartials : Partials {
+  int64_t chunk0, few0;
+  int chunk_kinds;
 };
 
 // The kernels' loops come in kinds of step: whole ones that all rows see all
@@ -94,6 +140,10 @@ struct Work {
   int row0, rows;    // first row of the tile among n * group, rows in it
   int p_min, p_max;  // positions of the tile's first and last token
   int lo_min, lo_max;  // first tokens they see
+  // Views only:
+  int row;           // of the block table
+  int low;           // tokens below it are a shared prefix's
+  bool all;          // all rows see all tokens: a shared prefix
 };
 
 // A sequence's length as its table bounds it, and so far below 2^31 that the
@@ -114,9 +164,54 @@ __host__ __device__ __forceinline__ void bounded_rows(int q0, int q1, int tokens
   w.n = end > w.q0 ? end - w.q0 : 0;
 }
 
-// Sequence b's rows and length, bounded by what the buffers hold.
+// First row of sequence s of n (s == n: the row after the last).
+__host__ __device__ __forceinline__ int first_row(const ViewArgs& a, int n, int s) {
+  return a.q_start ? a.q_start[s] : s * (a.tokens / n);
+}
+
+// The group of sequence s, -1 if none.
+__host__ __device__ __forceinline__ int group_of(const ViewArgs& a, int s) {
+  if (!a.shared_start) return 0;
+  int lo = 0, hi = a.groups;       // the last one that starts at s or before
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.shared_start[mid] <= s)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo > 0 && s < a.shared_start[lo] ? lo - 1 : -1;
+}
+
+// Sequence b's rows and length, bounded by what the buffers hold. With shared
+// prefixes those come first (batch counts both).
+__host__ __device__ __forceinline__ void sequence(const ViewArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
+  const int sequences = a.batch - a.groups;
+  w.b = b;
+  w.all = b < a.groups;
+  w.low = 0;
+  if (w.all) {
+    const int s0 = a.shared_start ? min(max(a.shared_start[b], 0), sequences) : 0;
+    const int s1 = a.shared_start ? min(a.shared_start[b + 1], sequences) : sequences;
+    bounded_rows(first_row(a, sequences, s0), first_row(a, sequences, max(s0, s1)), a.tokens, w);
+    w.len = bounded_length(a.shared_len[b], a.table_width, c.page_size);
+    w.row = min(s0, sequences - 1);
+    if (w.len == 0) w.n = 0;
+    return;
+  }
+  w.row = b - a.groups;
+  bounded_rows(first_row(a, sequences, w.row), first_row(a, sequences, w.row + 1), a.tokens, w);
+  w.len = bounded_length(a.kv_len[w.row], a.table_width, c.page_size);
+  if (a.groups > 0) {
+    const int g = group_of(a, w.row);
+    if (g >= 0) w.low = bounded_length(a.shared_len[g], a.table_width, c.page_size);
+  }
+}
 __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
   w.b = b;
+  w.row = b;
+  w.low = 0;
+  w.all = false;
   if (a.q_start) {
     bounded_rows(a.q_start[b], a.q_start[b + 1], a.tokens, w);
   } else {
@@ -131,21 +226,54 @@ __host__ __device__ __forceinline__ int first_seen(int p, int window) {
   return window > 0 ? max(0, max(p, -1) - window + 1) : 0;
 }
 
+// The last token that new token `tok` of a sequence sees, and the first one
+// (but for sinks) that a row with this last one does.
+__host__ __device__ __forceinline__ int position(const AttentionArgs&, const Work& w, int tok) {
+  return w.len - w.n + tok;
+}
+__host__ __device__ __forceinline__ int position(const ViewArgs&, const Work& w, int tok) {
+  return w.all ? w.len - 1 : w.len - w.n + tok;
+}
+__host__ __device__ __forceinline__ int first_of(const AttentionArgs& a, const Work&, int p) {
+  return first_seen(p, a.window);
+}
+__host__ __device__ __forceinline__ int first_of(const ViewArgs& a, const Work& w, int p) {
+  return w.all ? 0 : max(w.low, first_seen(p, a.window));
+}
+// Whether a row that sees first .. p does not see token t.
+__host__ __device__ __forceinline__ bool hidden(const AttentionArgs&, int t, int first, int p) {
+  return t > p || t < first;
+}
+__host__ __device__ __forceinline__ bool hidden(const ViewArgs& a, int t, int first, int p) {
+  return t > p || (t < first && t >= a.sinks);
+}
+
 // The tile of `tile_rows` rows from row0 on (group rows per token).
-__host__ __device__ __forceinline__ void row_tile(const AttentionArgs& a, int group, int row0, int tile_rows, Work& w) {
+template <class Args>
+__host__ __device__ __forceinline__ void row_tile(const Args& a, int group, int row0, int tile_rows, Work& w) {
   w.row0 = row0;
   w.rows = min(tile_rows, w.n * group - row0);
-  w.p_min = w.len - w.n + row0 / group;
-  w.p_max = w.len - w.n + (row0 + w.rows - 1) / group;
-  w.lo_min = first_seen(w.p_min, a.window);
-  w.lo_max = first_seen(w.p_max, a.window);
+  w.p_min = position(a, w, row0 / group);
+  w.p_max = position(a, w, (row0 + w.rows - 1) / group);
+  w.lo_min = first_of(a, w, w.p_min);
+  w.lo_max = first_of(a, w, w.p_max);
+}
+
+// Steps before a tile's window that hold sinks, if its window starts in step
+// `first`, in steps of 2^shift tokens.
+__host__ __device__ __forceinline__ int sink_steps(const AttentionArgs&, int, int) { return 0; }
+__host__ __device__ __forceinline__ int sink_steps(const ViewArgs& a, int first, int shift) {
+  return min((a.sinks >> shift) + ((a.sinks & ((1 << shift) - 1)) != 0), first);
 }
 
 // A sequence's page numbers, through the scalar cache where the place is
 // uniform (the table is not written during a launch).
 typedef const __attribute__((address_space(4))) int32_t* PageTable;
-__device__ __forceinline__ PageTable page_table(const AttentionArgs& a, int b) {
-  return (PageTable)(uintptr_t)(a.block_table + (int64_t)b * a.table_width);
+__device__ __forceinline__ PageTable page_table(const AttentionArgs& a, const Work& w) {
+  return (PageTable)(uintptr_t)(a.block_table + (int64_t)w.b * a.table_width);
+}
+__device__ __forceinline__ PageTable page_table(const ViewArgs& a, const Work& w) {
+  return (PageTable)(uintptr_t)(a.block_table + (int64_t)w.row * a.table_width);
 }
 
 // The page of token t: numbers are taken into the pool, table places to the
@@ -162,9 +290,10 @@ __device__ __forceinline__ int64_t pool_row(const qlinear_kv_cache& c, int page,
 // The sequence and row tile of tile number y, counting the tiles of the
 // sequences of at least min_rows rows, found by all lanes together. False if
 // there are fewer.
-__device__ __forceinline__ bool find_tile(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
-                                          int group, int y, Work& w, int& tile) {
-  if (!a.q_start || a.batch == 1) {
+template <class Args>
+__device__ __forceinline__ bool find_tile(const Args& a, const qlinear_kv_cache& c, const Plan& plan, int group, int y,
+                                          Work& w, int& tile) {
+  if (!kIsView<Args> && (!a.q_start || a.batch == 1)) {
     sequence(a, c, 0, w);
     const int per = (int)(((int64_t)w.n * group + kChunkRows - 1) / kChunkRows);
     if (per == 0 || (int64_t)w.n * group < plan.min_rows) return false;
@@ -204,39 +333,55 @@ __device__ __forceinline__ bool find_tile(const AttentionArgs& a, const qlinear_
 // ---- the few-row kernel's spans
 // A sequence's row tiles, and the steps counted for each (from the first token
 // that its first new token sees; 1 where none sees any, for the zeros).
+// Views number the steps that their rows may see from 0 on: `sinks` steps of
+// sinks, then from first_step on, which is `gap` further than its number.
 struct Item {
   int tiles, steps, first_step;
+  int sinks, gap;
+  __host__ __device__ __forceinline__ int real(int step) const { return step < sinks ? step : step + gap; }
 };
-__host__ __device__ __forceinline__ Item few_item(const AttentionArgs& a, const Plan& plan, int group, const Work& w) {
+template <class Args>
+__host__ __device__ __forceinline__ Item few_item(const Args& a, const Plan& plan, int group, const Work& w) {
   const int rows = w.n * group;
   Item it;
   it.tiles = rows > plan.max_rows ? 0 : (rows + plan.rows - 1) >> __builtin_ctz(plan.rows);
-  it.first_step = first_seen(w.len - w.n, a.window) / kStep;
-  it.steps = max((w.len - 1) / kStep - it.first_step, 0) + 1;
+  it.first_step = first_of(a, w, position(a, w, 0)) / kStep;
+  it.sinks = sink_steps(a, it.first_step, 5);
+  it.gap = it.first_step - it.sinks;
+  it.steps = it.sinks + max((w.len - 1) / kStep - it.first_step, 0) + 1;
   return it;
 }
+static_assert(kStep == 1 << 5);
 // Steps of the 64 sequences from b0 on, one per lane, with their running sum.
 // (The entry point bounds the slots of all tables, so that the sums fit.)
 struct Costs {
   int own, upto;
   int q0, n, len, tiles, steps;     // the lane's sequence, each of its tiles' steps
+  int row, low, all;
   // Sequence b, from the lane that holds it.
   __device__ __forceinline__ void get(int b, Work& w) const {
     w.b = b;
     w.q0 = __builtin_amdgcn_readlane(q0, b & 63);
     w.n = __builtin_amdgcn_readlane(n, b & 63);
     w.len = __builtin_amdgcn_readlane(len, b & 63);
+    w.row = __builtin_amdgcn_readlane(row, b & 63);
+    w.low = __builtin_amdgcn_readlane(low, b & 63);
+    w.all = __builtin_amdgcn_readlane(all, b & 63);
   }
   __device__ __forceinline__ void set(const Work& w, const Item& it) {
     q0 = w.q0;
     n = w.n;
     len = w.len;
+    row = w.row;
+    low = w.low;
+    all = w.all;
     tiles = it.tiles;
     steps = it.tiles > 0 ? it.steps : 0;
     own = upto = it.tiles * it.steps;
   }
 };
-__device__ __forceinline__ Costs few_costs(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+template <class Args>
+__device__ __forceinline__ Costs few_costs(const Args& a, const qlinear_kv_cache& c, const Plan& plan,
                                            int group, int b0) {
   const int lane = threadIdx.x & 63;
   Costs k = {};
@@ -284,7 +429,8 @@ __device__ __forceinline__ int few_tiles(const Costs& k) {
   for (int n = 0; n < 4; ++n) tiles += __builtin_popcountll(__ballot(k.tiles > n));
   return tiles;
 }
-__device__ __forceinline__ Spans few_spans(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+template <class Args>
+__device__ __forceinline__ Spans few_spans(const Args& a, const qlinear_kv_cache& c, const Plan& plan,
                                            int group) {
   Spans s;
   if (a.batch == 1) {      // no lane work on the way to the first load
@@ -317,7 +463,8 @@ __device__ __forceinline__ Spans few_spans(const AttentionArgs& a, const qlinear
   return s;
 }
 // The sequence w that holds step `at` (below the total), and the steps before it.
-__device__ __forceinline__ void few_find(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan, int group,
+template <class Args>
+__device__ __forceinline__ void few_find(const Args& a, const qlinear_kv_cache& c, const Plan& plan, int group,
                                         const Spans& s, int at, int& before, Work& w) {
   Costs k = s.costs;
   before = 0;
@@ -333,7 +480,8 @@ __device__ __forceinline__ void few_find(const AttentionArgs& a, const qlinear_k
   }
 }
 // The steps before sequence b.
-__device__ __forceinline__ int few_before(const AttentionArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+template <class Args>
+__device__ __forceinline__ int few_before(const Args& a, const qlinear_kv_cache& c, const Plan& plan,
                                           int group, const Spans& s, int b) {
   Costs k = s.costs;
   int before = 0;
@@ -409,6 +557,17 @@ __device__ __forceinline__ half2v code_pair(uint32_t codes, half2v scale) {
 }
 
 }  // namespace attn
+
+// Launchers of the views' kernels, one file per head width (see attention_views.hip).
+#define QLINEAR_VIEW_LAUNCHER(name)                                                                               \
+  hipError_t name(const qlinear_kv_cache& c, const ViewArgs& a, const attn::Plan& p, const attn::ViewPartials& part, \
+                  hipStream_t stream)
+QLINEAR_VIEW_LAUNCHER(launch_view_few_64);
+QLINEAR_VIEW_LAUNCHER(launch_view_few_128);
+QLINEAR_VIEW_LAUNCHER(launch_view_few_256);
+QLINEAR_VIEW_LAUNCHER(launch_view_chunk_64);
+QLINEAR_VIEW_LAUNCHER(launch_view_chunk_128);
+QLINEAR_VIEW_LAUNCHER(launch_view_chunk_256);
 
 // Launchers, one file per head width (see paged_attention.hip).
 hipError_t launch_attention_few_64(const qlinear_kv_cache& c, const AttentionArgs& a, const attn::Plan& p,

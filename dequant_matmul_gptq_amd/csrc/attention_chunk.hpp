@@ -111,11 +111,11 @@ struct ChunkShape {
   static constexpr int kRunWords = B == 16 ? 1 : kRun * B / 32;
 };
 
-template <int D, int B>
-__global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chunk_kernel(AttentionArgs a,
-                                                                                          qlinear_kv_cache c,
-                                                                                          Plan plan, Partials part) {
+template <int D, int B, class Args, class Parts>
+__global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chunk_kernel(Args a, qlinear_kv_cache c,
+                                                                                          Plan plan, Parts part) {
   typedef ChunkShape<D, B> Sh;
+  constexpr bool kView = kIsView<Args>;
   constexpr int T = Sh::T, kKeyTiles = T / 32, kFrags = D / 16, kOutTiles = D / 32;
   __shared__ __attribute__((aligned(16))) uint16_t ks[2][T * D];
   __shared__ __attribute__((aligned(16))) uint16_t vs[2][T * D];
@@ -127,19 +127,32 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const int page_shift = __builtin_ctz(c.page_size);
   const int group_shift = B == 16 ? 0 : __builtin_ctz(c.group);
 
-  // Later rows see more tokens: they start first.
+  // Later rows see more tokens: they start first (shared prefixes, which do, come first).
   Work w;
   int tile = 0;
-  if (!find_tile(a, c, plan, group, (gridDim.x - 1 - blockIdx.x) / c.kv_heads, w, tile)) return;
+  bool forward = false;
+  if constexpr (kView) forward = a.groups > 0;
+  if (!find_tile(a, c, plan, group, (forward ? blockIdx.x : gridDim.x - 1 - blockIdx.x) / c.kv_heads, w, tile)) return;
   row_tile(a, group, tile * kChunkRows, kChunkRows, w);
   const int step_lo = w.lo_min / T;
   const int step_end = w.p_max < 0 ? 0 : w.p_max / T + 1;
-  const int begin = step_lo + split * plan.chunk;
-  const int end = split == plan.splits - 1 ? step_end : min(begin + plan.chunk, step_end);
+  // Views number the steps that the tile sees from 0 on, those of sinks first.
+  const int sinks = sink_steps(a, step_lo, T == 64 ? 6 : 5), gap = kView ? step_lo - sinks : 0;
+  const int begin = (kView ? 0 : step_lo) + split * plan.chunk;
+  const int end = split == plan.splits - 1 ? step_end - gap : min(begin + plan.chunk, step_end - gap);
+  auto token = [&](int step) { return (kView && step >= sinks ? step + gap : step) * T; };     // a step's first
+  // Where partial results go, if the launch leaves any; whether this one does.
+  bool partial = plan.splits > 1;
+  int64_t part_row0 = split * part.rows;
+  if constexpr (kView) {
+    part_row0 = plan.splits > 1 ? part.chunk0 + ((int64_t)split * part.chunk_kinds + !w.all * (part.chunk_kinds - 1)) * part.rows
+                                : (w.all ? 0 : part.rows);
+    partial = partial || a.groups > 0;
+  }
   if (begin >= end && plan.splits > 1) {   // nothing in this range
     for (int r = threadIdx.x; r < w.rows; r += kChunkThreads) {
       const int rr = w.row0 + r;
-      part.ml[split * part.rows + (int64_t)(w.q0 + rr / group) * a.q_heads + head * group + rr % group] =
+      part.ml[part_row0 + (int64_t)(w.q0 + rr / group) * a.q_heads + head * group + rr % group] =
           make_float2(-INFINITY, 0.0f);
     }
     return;
@@ -150,10 +163,10 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const bool live = row < w.rows;
   const int rr = w.row0 + (live ? row : 0);
   const int tok = rr / group, qh = head * group + rr - tok * group;
-  const int pos = w.len - w.n + tok, first = first_seen(pos, a.window);
+  const int pos = position(a, w, tok), first = first_of(a, w, pos);
   const int64_t out_row = (int64_t)(w.q0 + tok) * a.q_heads + qh;
   const int wr0 = w.row0 + 32 * wave, wr1 = w.row0 + min(32 * wave + 31, w.rows - 1);
-  const int wp_max = w.len - w.n + wr1 / group, wlo_min = first_seen(w.len - w.n + wr0 / group, a.window);
+  const int wp_max = position(a, w, wr1 / group), wlo_min = first_of(a, w, position(a, w, wr0 / group));
 
   half8 q[kFrags];
   {
@@ -174,7 +187,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const float slack = 8.0f / (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e);
   const float sc = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
 
-  const PageTable table = page_table(a, w.b);
+  const PageTable table = page_table(a, w);
   const int last_page = max(w.len - 1, 0) >> page_shift;
 
   // ---- staging
@@ -189,13 +202,13 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
     if constexpr (B == 16)
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
-        pages[i] = page_of(c, table, page_shift, last_page, step * T + (4 * i + wave) * kGroupRows);
+        pages[i] = page_of(c, table, page_shift, last_page, token(step) + (4 * i + wave) * kGroupRows);
   };
   auto stage_direct = [&](int step, Lds kn, Lds vn) {
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       const int r0 = (4 * i + wave) * kGroupRows;
-      const int64_t pool = pool_row(c, pages[i], page_shift, head, step * T + r0) * D;
+      const int64_t pool = pool_row(c, pages[i], page_shift, head, token(step) + r0) * D;
       // lane's row and piece in LDS order
       const int r = r0 + lane / Sh::kPieces, x = lane % Sh::kPieces;
       typedef const __attribute__((address_space(1))) void* gptr;
@@ -214,7 +227,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const int my_row = threadIdx.x / kPerRow, my_run = threadIdx.x % kPerRow;
   auto fetch = [&](int step) {
     if constexpr (B != 16) {
-      const int t = step * T + my_row;
+      const int t = token(step) + my_row;
       const int64_t pool = pool_row(c, page_of(c, table, page_shift, last_page, t), page_shift, head, t);
       const uint32_t* kp = (const uint32_t*)c.k + pool * (D * B / 32) + my_run * Sh::kRunWords;
       const uint32_t* vp = (const uint32_t*)c.v + pool * (D * B / 32) + my_run * Sh::kRunWords;
@@ -285,7 +298,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   auto one_step = [&](auto kind, int step, Lds __restrict__ kc, Lds __restrict__ vc, Lds __restrict__ kn,
                       Lds __restrict__ vn) __attribute__((always_inline)) -> bool {
     constexpr bool kSplit = decltype(kind)::value == kCareful;
-    const int t0 = step * T;
+    const int t0 = token(step);
     constexpr bool kEdge = decltype(kind)::value == kEdgeStep || kSplit;
     if (decltype(kind)::value != kGrow && step + 1 < end) {
       if constexpr (B == 16) {
@@ -304,7 +317,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       for (int i = threadIdx.x; i < T * D / 8; i += kChunkThreads) {
         const int t = t0 + i / Sh::kPieces;
         const Lds4 at = (Lds4)(vc + i * 8);
-        if (t > w.p_max || t < w.lo_min) {
+        if (hidden(a, t, w.lo_min, w.p_max)) {
           *at = u32x4{0, 0, 0, 0};
         } else {
           const u32x4 v = *at;
@@ -316,7 +329,8 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       if (!kSplit && nonfinite) return false;
     }
 
-    const bool active = !kEdge || (t0 <= wp_max && t0 + T - 1 >= wlo_min);
+    bool active = !kEdge || (t0 <= wp_max && t0 + T - 1 >= wlo_min);
+    if constexpr (kView) active = active || (t0 <= wp_max && t0 < a.sinks);
     half8 p[T / 16];
     if (active) {
       float16v s[kKeyTiles];
@@ -341,7 +355,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int t = t0 + 32 * k + 8 * (r / 4) + 4 * h + r % 4;
-            if (t > pos || t < first) s[k][r] = -INFINITY;
+            if (hidden(a, t, first, pos)) s[k][r] = -INFINITY;
           }
       }
       float mx = s[0][0];
@@ -386,7 +400,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = t0 + 16 * cc + 8 * (i / 2) + 4 * h + 2 * (i % 2);
-            sees[i] = kOnes & both(t <= pos && t >= first, t < pos && t + 1 >= first);
+            sees[i] = kOnes & both(!hidden(a, t, first, pos), !hidden(a, t + 1, first, pos));
           }
 #pragma unroll
           for (int d = 0; d < kOutTiles; ++d) {
@@ -494,9 +508,12 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   bool done = true;
   // Steps at the window's start, whole steps, steps at the diagonal: two rounds
   // of whole and then edge steps, so that each kind's code is there once.
-  const int whole_lo = (w.lo_max + T - 1) / T, whole_hi = max((w.p_min + 1) / T, whole_lo);
+  // (Views have whole steps of sinks before the window's start.)
+  const int whole_lo = (w.lo_max + T - 1) / T - gap, whole_hi = max((w.p_min + 1) / T - gap, whole_lo);
+  int whole_first = begin;
+  if constexpr (kView) whole_first = min(a.sinks / T, (w.p_min + 1) / T);
   for (int round = 0; round < 2 && done; ++round) {
-    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end));
+    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : whole_first, end));
     done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
   }
   if (!done) {
@@ -511,7 +528,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   l = sum32(l);
   if (!live) return;
   const bool none = pos < first;     // sees no token
-  if (plan.splits == 1) {
+  if (!partial) {
     const float inv = 1.0f / l;
     uint16_t* out = a.out + out_row * D;
 #pragma unroll
@@ -532,7 +549,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
         }
       }
   } else {
-    float* out = part.o + (split * part.rows + out_row) * D;
+    float* out = part.o + (part_row0 + out_row) * D;
 #pragma unroll
     for (int d = 0; d < kOutTiles; ++d)
 #pragma unroll
@@ -547,25 +564,29 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       }
     if (h == 0) {
       // A range that the row sees part of, all of it at -infinity, is not an empty one.
-      const bool sees = max(first, begin * T) <= min(pos, end * T - 1);
-      part.ml[split * part.rows + out_row] = make_float2(m == -INFINITY ? (sees ? kLowest : m) : m * sc, l);
+      bool sees = max(first, begin * T) <= min(pos, end * T - 1);
+      if constexpr (kView)
+        sees = begin < end &&
+               (max(first, token(begin)) <= min(pos, token(end - 1) + T - 1) || token(begin) < min(a.sinks, pos + 1));
+      part.ml[part_row0 + out_row] = make_float2(m == -INFINITY ? (sees ? kLowest : m) : m * sc, l);
     }
   }
 }
 
-template <int D, int B>
-hipError_t launch_chunk(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
+template <int D, int B, class Args, class Parts>
+hipError_t launch_chunk(const qlinear_kv_cache& c, const Args& a, const Plan& p, const Parts& part,
                         hipStream_t stream) {
   const int group = a.q_heads / c.kv_heads;
   // Key/value heads are neighbours in the grid: with 8 of them (or a multiple)
   // one XCD's L2 sees the keys and values of its own heads only.
-  const dim3 grid((unsigned)(chunk_tiles(a, group) * c.kv_heads), (unsigned)p.splits);
-  hipLaunchKernelGGL((attention_chunk_kernel<D, B>), grid, dim3(kChunkThreads), 0, stream, a, c, p, part);
+  const int64_t tiles = kIsView<Args> ? p.tiles : chunk_tiles(a, group);
+  const dim3 grid((unsigned)(tiles * c.kv_heads), (unsigned)p.splits);
+  hipLaunchKernelGGL((attention_chunk_kernel<D, B, Args, Parts>), grid, dim3(kChunkThreads), 0, stream, a, c, p, part);
   return hipGetLastError();
 }
 
-template <int D>
-hipError_t launch_chunk_width(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
+template <int D, class Args, class Parts>
+hipError_t launch_chunk_width(const qlinear_kv_cache& c, const Args& a, const Plan& p, const Parts& part,
                               hipStream_t stream) {
   if (c.bits == 16) return launch_chunk<D, 16>(c, a, p, part, stream);
   if (c.bits == 8) return launch_chunk<D, 8>(c, a, p, part, stream);

@@ -284,9 +284,10 @@ __device__ __forceinline__ void add_nonfinite(const u32x4& v, const u32x4& sees,
     sum[r * stride] += (nu[r] > 0.0f ? INFINITY : 0.0f) - (nd[r] > 0.0f ? INFINITY : 0.0f);
 }
 
-template <int D, int B, int NT, bool ONCE>
+template <int D, int B, int NT, bool ONCE, class Args, class Parts>
 __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void attention_few_kernel(
-    AttentionArgs a, qlinear_kv_cache c, Plan plan, Partials part) {
+    Args a, qlinear_kv_cache c, Plan plan, Parts part) {
+  constexpr bool kView = kIsView<Args>;
   typedef ValueRaw<D, B> VR;
   constexpr int W = VR::W, U = VR::U, kTiles = D / 16, kFrags = D / 32;
   constexpr int kRow = D + 4;     // LDS row of the join, in floats
@@ -342,9 +343,16 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
   const int taken = min(it.steps - i0, stop - at);
   const bool alone = taken == it.steps;
   row_tile(a, group, tile * 16 * NT, 16 * NT, w);
-  const int begin = max(it.first_step + i0, w.lo_min / kStep);
-  const int end = min(it.first_step + i0 + taken, w.p_max < 0 ? 0 : w.p_max / kStep + 1);
+  int begin, end;
+  if constexpr (kView) {     // numbers as in Item
+    begin = i0 < it.sinks ? i0 : max(i0, w.lo_min / kStep - it.gap);
+    end = min(i0 + taken, (w.p_max < 0 ? 0 : w.p_max / kStep + 1) - it.gap);
+  } else {
+    begin = max(it.first_step + i0, w.lo_min / kStep);
+    end = min(it.first_step + i0 + taken, w.p_max < 0 ? 0 : w.p_max / kStep + 1);
+  }
   const int64_t part_row0 = (((int64_t)worker * c.kv_heads + head) * 2 + slot) * (16 * NT);
+  auto token = [&](int step) { return (kView ? it.real(step) : step) * kStep; };     // a step's first
 
   // Rows: column col of tile nt is row row0 + 16 nt + col of the sequence.
   int pos[NT], first[NT];
@@ -355,17 +363,20 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
     const bool live = r < w.rows;
     const int rr = w.row0 + (live ? r : 0);
     const int tok = rr / group, h = head * group + rr % group;
-    pos[nt] = w.len - w.n + tok;
-    first[nt] = first_seen(pos[nt], a.window);
+    pos[nt] = position(a, w, tok);
+    first[nt] = first_of(a, w, pos[nt]);
     const uint16_t* p = a.q + (w.q0 + tok) * a.q_stride + (int64_t)h * D;
     uint32_t run[D / 8];
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
       u32x4 v = {0, 0, 0, 0};
-      if (live)
+      // In views all lanes load (the tile's first row where there is none): around
+      // a branch here, hipcc 7.2 spilled a register while some lanes were off,
+      // which the others then lacked (tests/test_attention_listing_views.py).
+      if (kView || live)
         v = *reinterpret_cast<const u32x4*>(p + (B == 16 ? 32 * f + 8 * g : g * (D / 4) + 8 * f));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) run[4 * f + e] = v[e];
+      for (int e = 0; e < 4; ++e) run[4 * f + e] = kView && !live ? 0 : v[e];
     }
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
@@ -377,7 +388,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
     }
   }
 
-  const PageTable table = page_table(a, w.b);
+  const PageTable table = page_table(a, w);
   const int last_page = max(w.len - 1, 0) >> page_shift;
   float4v o[NT][kTiles];
   float m[NT], l[NT];
@@ -391,12 +402,12 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
   int64_t rows[2];
   auto look_up = [&](int step) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) pages[i] = page_of(c, table, page_shift, last_page, step * kStep + 16 * i);
+    for (int i = 0; i < 2; ++i) pages[i] = page_of(c, table, page_shift, last_page, token(step) + 16 * i);
   };
   auto keys = [&](int step) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      rows[i] = pool_row(c, pages[i], page_shift, head, step * kStep + 16 * i);
+      rows[i] = pool_row(c, pages[i], page_shift, head, token(step) + 16 * i);
       load_keys<D, B, ONCE>(kr, i, c, group_shift, rows[i], col, g);
     }
   };
@@ -410,7 +421,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
   // that only some rows see.
   auto one_step = [&](auto kind, int step) __attribute__((always_inline)) -> bool {
     constexpr bool kEdge = decltype(kind)::value != kWhole, kSplit = decltype(kind)::value == kCareful;
-    const int t0 = step * kStep;
+    const int t0 = token(step);
     // Whole steps are never the wave's last (see below): their loads stand
     // in no branch, which would make the waits for them whole.
     const bool more = !kEdge || step + kFewWaves < end;
@@ -442,7 +453,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int t = t0 + 16 * (i / 4) + 4 * g + i % 4;
-          if (t > pos[nt] || t < first[nt]) x[i] = -INFINITY;
+          if (hidden(a, t, first[nt], pos[nt])) x[i] = -INFINITY;
         }
       }
       float mx = x[0];
@@ -477,7 +488,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int ta = t0 + 16 * (t / 2) + 4 * g + 2 * (t % 2);
-          const uint32_t keep = both(ta <= w.p_max && ta >= w.lo_min, ta < w.p_max && ta + 1 >= w.lo_min);
+          const uint32_t keep = both(!hidden(a, ta, w.lo_min, w.p_max), !hidden(a, ta + 1, w.lo_min, w.p_max));
 #pragma unroll
           for (int j = 0; j < W; ++j) {
             vf[j][t] &= keep;
@@ -498,7 +509,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const int ta = t0 + 16 * (t / 2) + 4 * g + 2 * (t % 2);
-              sees[t] = kOnes & both(ta <= pos[nt] && ta >= first[nt], ta < pos[nt] && ta + 1 >= first[nt]);
+              sees[t] = kOnes & both(!hidden(a, ta, first[nt], pos[nt]), !hidden(a, ta + 1, first[nt], pos[nt]));
             }
 #pragma unroll
             for (int j = 0; j < W; ++j) {
@@ -552,10 +563,14 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
   start();
   // Steps at the window's start, whole steps, steps at the diagonal: two rounds
   // of whole and then edge steps, so that each kind's code is there once.
-  const int whole_lo = (w.lo_max + kStep - 1) / kStep, whole_hi = max((w.p_min + 1) / kStep, whole_lo);
+  // (Views have whole steps of sinks before the window's start.)
+  const int gap = kView ? it.gap : 0;
+  const int whole_lo = (w.lo_max + kStep - 1) / kStep - gap, whole_hi = max((w.p_min + 1) / kStep - gap, whole_lo);
+  int whole_first = begin;
+  if constexpr (kView) whole_first = min(a.sinks / kStep, (w.p_min + 1) / kStep);
   bool done = true;
   for (int round = 0; round < 2 && done; ++round) {
-    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : begin, end - kFewWaves));
+    steps_to(std::integral_constant<int, kWhole>{}, min(round ? whole_hi : whole_first, end - kFewWaves));
     done = steps_to(std::integral_constant<int, kEdgeStep>{}, round ? end : min(whole_lo, end));
   }
   if (!done) {
@@ -599,9 +614,15 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
         total += f[i] * join_ml[nt][i][row].y;
       }
       const int tok = (w.row0 + rr) / group, h = head * group + (w.row0 + rr) % group;
-      const int pr = w.len - w.n + tok, fr = first_seen(pr, a.window);
+      const int pr = position(a, w, tok), fr = first_of(a, w, pr);
       const int64_t out_row = (int64_t)(w.q0 + tok) * a.q_heads + h;
       const float inv = pr < fr ? 0.0f : 1.0f / total;
+      bool final = alone;      // else a partial result, in row part_row
+      int64_t part_row = part_row0 + rr;
+      if constexpr (kView) {
+        final = alone && a.groups == 0;
+        part_row = alone ? (w.all ? 0 : part.rows) + out_row : part.few0 + part_row;
+      }
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
         float4v v = {0, 0, 0, 0};
@@ -611,19 +632,22 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += f[i] * x[e];
         }
-        if (alone) {
+        if (final) {
           half4 y;
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = (_Float16)(pr < fr ? 0.0f : v[e] * inv);
           *reinterpret_cast<half4*>(a.out + out_row * D + d * 64 + d0) = y;
         } else {
-          *reinterpret_cast<float4v*>(part.o + (part_row0 + rr) * D + d * 64 + d0) = v;
+          *reinterpret_cast<float4v*>(part.o + part_row * D + d * 64 + d0) = v;
         }
       }
-      if (!alone && d0 == 0) {
+      if (!final && d0 == 0) {
         // A range that the row sees part of, all of it at -infinity, is not an empty one.
-        const bool sees = max(fr, begin * kStep) <= min(pr, end * kStep - 1);
-        part.ml[part_row0 + rr] = make_float2(top == -INFINITY && sees ? kLowest : top, total);
+        bool sees = max(fr, begin * kStep) <= min(pr, end * kStep - 1);
+        if constexpr (kView)
+          sees = begin < end && (max(fr, token(begin)) <= min(pr, token(end - 1) + kStep - 1) ||
+                                 token(begin) < min(a.sinks, pr + 1));
+        part.ml[part_row] = make_float2(top == -INFINITY && sees ? kLowest : top, total);
       }
     }
   }
@@ -643,12 +667,12 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
   }
 }
 
-template <int D, int B>
-hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
-                      hipStream_t stream) {
+template <int D, int B, class Args, class Parts>
+hipError_t launch_few(const qlinear_kv_cache& c, const Args& a, const Plan& p, const Parts& part, hipStream_t stream) {
   const int group = a.q_heads / c.kv_heads;
   const int64_t most = (int64_t)a.max_q_len * group;
-  const int tiles = (int)(((most < p.max_rows ? most : p.max_rows) + p.rows - 1) / p.rows);
+  const int tiles =
+      kIsView<Args> ? p.tiles : (int)(((most < p.max_rows ? most : p.max_rows) + p.rows - 1) / p.rows);
   const int workgroups = p.whole * a.batch > p.workers ? p.whole * a.batch : p.workers;
   const dim3 grid = p.workers ? dim3((unsigned)(c.kv_heads * workgroups))
                               : dim3((unsigned)(c.kv_heads * tiles), (unsigned)a.batch);
@@ -656,19 +680,22 @@ hipError_t launch_few(const qlinear_kv_cache& c, const AttentionArgs& a, const P
   // them share it through L2 (both sides measured, cold: 64 sequences of 2048
   // tokens, 64/8 heads, one tile 98.2 us with plain loads, 87.4 us past the
   // caches; 8 of 8192 with 7 new tokens each, two tiles, 69.3 and 76.7 us).
+  const bool once = kIsView<Args> ? p.once : tiles == 1;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kFewWaves), 0, stream, a, c, p, part);
     return hipGetLastError();
   };
   if (p.rows == 16)
-    return tiles == 1 ? go(attention_few_kernel<D, B, 1, true>) : go(attention_few_kernel<D, B, 1, false>);
+    return once ? go(attention_few_kernel<D, B, 1, true, Args, Parts>)
+                : go(attention_few_kernel<D, B, 1, false, Args, Parts>);
   if constexpr (D < 256)
-    return tiles == 1 ? go(attention_few_kernel<D, B, 2, true>) : go(attention_few_kernel<D, B, 2, false>);
+    return once ? go(attention_few_kernel<D, B, 2, true, Args, Parts>)
+                : go(attention_few_kernel<D, B, 2, false, Args, Parts>);
   return hipErrorInvalidValue;      // no plan has more rows for 256 wide heads
 }
 
-template <int D>
-hipError_t launch_few_width(const qlinear_kv_cache& c, const AttentionArgs& a, const Plan& p, const Partials& part,
+template <int D, class Args, class Parts>
+hipError_t launch_few_width(const qlinear_kv_cache& c, const Args& a, const Plan& p, const Parts& part,
                             hipStream_t stream) {
   if (c.bits == 16) return launch_few<D, 16>(c, a, p, part, stream);
   if (c.bits == 8) return launch_few<D, 8>(c, a, p, part, stream);

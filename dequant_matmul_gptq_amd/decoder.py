@@ -312,27 +312,33 @@ def rope_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torc
 # ---------------------------------------------------------------- attention
 
 def paged_attention_workspace_bytes(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int,
-                                    max_kv_len: int, window: int = 0) -> int:
+                                    max_kv_len: int, window: int = 0, sinks: int = 0) -> int:
     n = ctypes.c_size_t(0)
     sizes = _int32(int(tokens), int(q_heads), int(batch), int(max_q_len), int(max_kv_len), int(window))
-    _check(lib().qlinear_paged_attention_workspace_bytes(cache.ref, *sizes, ctypes.byref(n)),
-           "qlinear_paged_attention_workspace_bytes")
+    if sinks:
+        _check(lib().qlinear_paged_attention_sinks_workspace_bytes(cache.ref, *sizes, *_int32(int(sinks)),
+                                                                   ctypes.byref(n)),
+               "qlinear_paged_attention_sinks_workspace_bytes")
+    else:
+        _check(lib().qlinear_paged_attention_workspace_bytes(cache.ref, *sizes, ctypes.byref(n)),
+               "qlinear_paged_attention_workspace_bytes")
     return int(n.value)
 
 
 def paged_attention_workspace(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int, max_kv_len: int,
-                              device, window: int = 0) -> torch.Tensor:
+                              device, window: int = 0, sinks: int = 0) -> torch.Tensor:
     """A paged_attention workspace for calls of up to these sizes with the same
-    q_heads and window (scratch: needs no initialization; calls that may overlap
-    in time must not share one)."""
-    n = paged_attention_workspace_bytes(cache, tokens, q_heads, batch, max_q_len, max_kv_len, window)
+    q_heads, window and sinks (scratch: needs no initialization; calls that may
+    overlap in time must not share one)."""
+    n = paged_attention_workspace_bytes(cache, tokens, q_heads, batch, max_q_len, max_kv_len, window, sinks)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
 def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
                     q_start: torch.Tensor | None = None, max_q_len: int | None = None,
                     max_kv_len: int | None = None, scale: float | None = None, window: int = 0,
-                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    sinks: int = 0) -> torch.Tensor:
     """Causal attention of each sequence's new tokens over its cached ones (the
     new ones among them, appended before the call).
 
@@ -340,17 +346,17 @@ def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, 
     int32 [batch][width], a sequence's pages in order; kv_len int32 [batch],
     tokens in the cache; q_start int32 [batch + 1], sequence b's rows of q are
     q_start[b] .. q_start[b + 1] - 1 (None: tokens / batch rows each). window
-    w > 0: a token sees the w last positions up to its own. scale: None =
-    head_dim^-0.5. max_q_len and max_kv_len bound the lengths for the launch
-    plan (None: tokens, width * page_size); lengths stay on the device. Returns
-    out float16 [tokens][q_heads][head_dim]; a token that sees nothing gets
-    zeros.
+    w > 0: a token sees the w last positions up to its own, and with sinks the
+    sequence's first `sinks` tokens too. scale: None = head_dim^-0.5. max_q_len
+    and max_kv_len bound the lengths for the launch plan (None: tokens, width *
+    page_size); lengths stay on the device. Returns out float16
+    [tokens][q_heads][head_dim]; a token that sees nothing gets zeros.
     """
     dev, D = cache.device, cache.head_dim
     if _current_gpu() != dev:
         with torch.cuda.device(dev):
             return paged_attention(cache, q, block_table, kv_len, q_start, max_q_len, max_kv_len, scale, window, out,
-                                   workspace)
+                                   workspace, sinks)
     qp, T, H, _, qs = _rows(q, "q", None, None, D, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch][width]")
@@ -368,13 +374,95 @@ def paged_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, 
         out = torch.empty((T, H, D), dtype=_F16, device=q.device)
     op = _operand(out, "out", _F16, (T, H, D), dev)
     if workspace is None:
-        workspace = paged_attention_workspace(cache, T, H, B, max_q_len, max_kv_len, q.device, window)
+        workspace = paged_attention_workspace(cache, T, H, B, max_q_len, max_kv_len, q.device, window, sinks)
     n = workspace.numel()
     wp = _operand(workspace, "workspace", _U8, (n,), dev)
-    if (T | H | B | W | max_q_len | max_kv_len | window) >> 31:
-        T, H, B, W, max_q_len, max_kv_len, window = _int32(T, H, B, W, max_q_len, max_kv_len, window)
-    _check(lib().qlinear_paged_attention(cache.ref, qp, qs, T, H, B, sp, lp, tp, W, max_q_len, max_kv_len, scale,
-                                         window, op, wp, n, _stream(dev)), "qlinear_paged_attention")
+    if (T | H | B | W | max_q_len | max_kv_len | window | sinks) >> 31:
+        T, H, B, W, max_q_len, max_kv_len, window, sinks = _int32(T, H, B, W, max_q_len, max_kv_len, window, sinks)
+    if sinks:
+        _check(lib().qlinear_paged_attention_sinks(cache.ref, qp, qs, T, H, B, sp, lp, tp, W, max_q_len, max_kv_len,
+                                                   scale, window, sinks, op, wp, n, _stream(dev)),
+               "qlinear_paged_attention_sinks")
+    else:
+        _check(lib().qlinear_paged_attention(cache.ref, qp, qs, T, H, B, sp, lp, tp, W, max_q_len, max_kv_len, scale,
+                                             window, op, wp, n, _stream(dev)), "qlinear_paged_attention")
+    return out
+
+
+def paged_attention_shared_workspace_bytes(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int,
+                                           max_kv_len: int, groups: int, max_shared_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    sizes = _int32(int(tokens), int(q_heads), int(batch), int(max_q_len), int(max_kv_len), int(groups),
+                   int(max_shared_len))
+    _check(lib().qlinear_paged_attention_shared_workspace_bytes(cache.ref, *sizes, ctypes.byref(n)),
+           "qlinear_paged_attention_shared_workspace_bytes")
+    return int(n.value)
+
+
+def paged_attention_shared_workspace(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int,
+                                     max_kv_len: int, groups: int, max_shared_len: int, device) -> torch.Tensor:
+    """A paged_attention_shared workspace for calls of up to these sizes with
+    the same q_heads (scratch: needs no initialization; calls that may overlap in
+    time must not share one)."""
+    n = paged_attention_shared_workspace_bytes(cache, tokens, q_heads, batch, max_q_len, max_kv_len, groups,
+                                               max_shared_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def paged_attention_shared(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                           shared_len: torch.Tensor, shared_start: torch.Tensor | None = None,
+                           q_start: torch.Tensor | None = None, max_q_len: int | None = None,
+                           max_kv_len: int | None = None, max_shared_len: int | None = None,
+                           scale: float | None = None, out: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """paged_attention for sequences that share their first tokens, as forks of
+    one sequence do: those are read once for all of a group's rows.
+
+    Group g is the sequences shared_start[g] .. shared_start[g + 1] - 1 (int32
+    [groups + 1]; None: one group of all), whose first shared_len[g] tokens
+    (int32 [groups]; PagePool.shared_tokens counts them) are the same slots of
+    the cache: at most each one's tokens before its new ones. Sequences of no
+    group share nothing. max_shared_len bounds shared_len for the launch plan
+    (None: width * page_size). The rest is as for paged_attention.
+    """
+    dev, D = cache.device, cache.head_dim
+    if _current_gpu() != dev:
+        with torch.cuda.device(dev):
+            return paged_attention_shared(cache, q, block_table, kv_len, shared_len, shared_start, q_start, max_q_len,
+                                          max_kv_len, max_shared_len, scale, out, workspace)
+    qp, T, H, _, qs = _rows(q, "q", None, None, D, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][width]")
+    B, W = block_table.shape
+    tp = _operand(block_table, "block_table", _I32, (B, W), dev)
+    lp = _operand(kv_len, "kv_len", _I32, (B,), dev)
+    G = shared_len.numel()
+    if shared_start is None and G != 1:
+        raise ValueError("without shared_start all sequences are one group")
+    gl = _operand(shared_len, "shared_len", _I32, (G,), dev)
+    gs = None if shared_start is None else _operand(shared_start, "shared_start", _I32, (G + 1,), dev)
+    sp = None if q_start is None else _operand(q_start, "q_start", _I32, (B + 1,), dev)
+    if max_q_len is None:
+        max_q_len = T if q_start is not None or B == 0 else T // B
+    if max_kv_len is None:
+        max_kv_len = W * cache.page_size
+    if max_shared_len is None:
+        max_shared_len = W * cache.page_size
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty((T, H, D), dtype=_F16, device=q.device)
+    op = _operand(out, "out", _F16, (T, H, D), dev)
+    if workspace is None:
+        workspace = paged_attention_shared_workspace(cache, T, H, B, max_q_len, max_kv_len, G, max_shared_len, q.device)
+    n = workspace.numel()
+    wp = _operand(workspace, "workspace", _U8, (n,), dev)
+    if (T | H | B | W | G | max_q_len | max_kv_len | max_shared_len) >> 31:
+        T, H, B, W, G, max_q_len, max_kv_len, max_shared_len = _int32(T, H, B, W, G, max_q_len, max_kv_len,
+                                                                      max_shared_len)
+    _check(lib().qlinear_paged_attention_shared(cache.ref, qp, qs, T, H, B, sp, lp, tp, W, G, gs, gl, max_q_len,
+                                                max_kv_len, max_shared_len, scale, op, wp, n, _stream(dev)),
+           "qlinear_paged_attention_shared")
     return out
 
 

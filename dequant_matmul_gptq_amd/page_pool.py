@@ -39,6 +39,20 @@ class PagePool:
     def length(self, seq) -> int:
         return self._length[seq]
 
+    def shared_tokens(self, seqs) -> int:
+        """Tokens in the leading pages that all of `seqs` hold (no more than the
+        shortest has): what they may share in paged_attention_shared, if asked
+        before they are extended by the new tokens."""
+        seqs = list(seqs)
+        if not seqs:
+            return 0
+        n = 0
+        for same in zip(*(self._pages[s] for s in seqs)):
+            if len(set(same)) > 1:
+                break
+            n += self.page_size
+        return min([n] + [self._length[s] for s in seqs])
+
     def _take(self) -> int:
         p = self._free.pop()
         self._refs[p] = 1

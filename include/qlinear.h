@@ -554,6 +554,62 @@ int qlinear_paged_attention(const qlinear_kv_cache* cache, const uint16_t* q, in
                             void* stream);
 
 /*
+ * qlinear_paged_attention with a window whose sequences' first `sinks` tokens
+ * stay visible: the new token at position p sees the tokens t <= p with
+ * t > p - window or t < sinks. Without a window (0), and with sinks == 0, this
+ * is qlinear_paged_attention. Arguments and errors are the same ones
+ * (INVALID_ARGUMENT for sinks < 0); the workspace is that of
+ * qlinear_paged_attention_sinks_workspace_bytes, enough for all calls up to its
+ * tokens, batch, max_q_len and max_kv_len with the same window and sinks.
+ */
+int qlinear_paged_attention_sinks_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,
+                                                  int32_t batch, int32_t max_q_len, int32_t max_kv_len, int32_t window,
+                                                  int32_t sinks, size_t* bytes);
+int qlinear_paged_attention_sinks(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t tokens,
+                                  int32_t q_heads, int32_t batch, const int32_t* q_start, const int32_t* kv_len,
+                                  const int32_t* block_table, int32_t table_width, int32_t max_q_len,
+                                  int32_t max_kv_len, float scale, int32_t window, int32_t sinks, uint16_t* out,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * qlinear_paged_attention (without a window) for batches in which sequences
+ * share their first tokens, as forks of one sequence do: what they share is
+ * read and multiplied once for all of a group's rows.
+ *   groups, shared_start : group g is the sequences shared_start[g] ..
+ *               shared_start[g + 1] - 1, int32 [groups + 1], non-decreasing.
+ *               NULL: one group of all (groups == 1). Sequences of no group
+ *               share nothing
+ *   shared_len : int32 [groups]; the first shared_len[g] tokens of each
+ *               sequence of group g are those of its first sequence: they are
+ *               read from that one's row of the block table. At most the
+ *               sequences' cached tokens before their new ones (kv_len - n),
+ *               which the call does not check: a larger one shows them tokens
+ *               that they should not see. Any length, also inside a page; 0
+ *               or less: nothing
+ *   max_shared_len : upper bound of shared_len, for the launch plan only
+ *   workspace : qlinear_paged_attention_shared_workspace_bytes of the same
+ *               sizes, or of larger tokens, batch, max_q_len, max_kv_len, groups
+ *               and max_shared_len with the same cache shape and q_heads
+ * The other arguments are those of qlinear_paged_attention; kv_len counts all
+ * of a sequence's tokens and its row of the block table has all its pages (those
+ * below shared_len are read of a group's first sequence only). Errors: those of
+ * qlinear_paged_attention, and INVALID_ARGUMENT (groups < 1, max_shared_len < 0,
+ * shared_len NULL, shared_start NULL with groups != 1), UNSUPPORTED (batch +
+ * groups > 65535, (batch + groups) * kv_heads > 2^22, (batch + groups) *
+ * table_width * page_size > 2^33, tokens * q_heads > 2^25), MISALIGNED
+ * (shared_start, shared_len 4 bytes).
+ */
+int qlinear_paged_attention_shared_workspace_bytes(const qlinear_kv_cache* cache, int32_t tokens, int32_t q_heads,
+                                                   int32_t batch, int32_t max_q_len, int32_t max_kv_len,
+                                                   int32_t groups, int32_t max_shared_len, size_t* bytes);
+int qlinear_paged_attention_shared(const qlinear_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t tokens,
+                                   int32_t q_heads, int32_t batch, const int32_t* q_start, const int32_t* kv_len,
+                                   const int32_t* block_table, int32_t table_width, int32_t groups,
+                                   const int32_t* shared_start, const int32_t* shared_len, int32_t max_q_len,
+                                   int32_t max_kv_len, int32_t max_shared_len, float scale, uint16_t* out,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Copy pages inside each of `count` caches (a model's layers, which share one
  * page numbering): for every i < moves, page pairs[i][1] becomes a copy of
  * page pairs[i][0], in k, v and the scales. All copies happen as if at once
