@@ -159,6 +159,7 @@ int set_norms(const Norms& n, int32_t q_heads, int32_t kv_heads, int32_t head_di
   a.q_norm_stride = n.q_heads == 1 ? 0 : head_dim;
   a.k_norm_stride = n.k_heads == 1 ? 0 : head_dim;
   a.eps = n.eps;
+  a.per_element = 1.0f / (float)head_dim;
   return QLINEAR_OK;
 }
 

@@ -118,7 +118,7 @@ struct RopeArgs {
   // Norm weights of q and k heads, one for all (stride 0) or one a head; NULL: no norm.
   const uint16_t *q_norm, *k_norm;
   int64_t q_norm_stride, k_norm_stride;
-  float eps;
+  float eps, per_element;         // per_element: 1 / head_dim
 };
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_rope_append(const RopeArgs& a, const qlinear_kv_cache& cache, hipStream_t stream);
