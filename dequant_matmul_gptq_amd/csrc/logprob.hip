@@ -12,9 +12,16 @@
 // parts where there are few of them, or where a row is longer than the
 // registers; a second launch joins the parts. The search: the k-th largest of
 // 64 maxima, over a 64th of the part each, is below the k-th largest element or
-// equal to it. What is not below it (k to 5 k elements of rows without order)
-// goes to LDS and is ranked there by counting larger keys. Rows with very many
-// equal elements, which do not fit there, give up one maximum after another.
+// equal to it. What is not below it (about k to 2 k elements of rows without
+// order) goes to LDS and is ranked there by counting larger keys. Where too many
+// are equal to it (rows with masks), the first ones by index are taken in order.
+//
+// Measured: 2047 rows of 32000 float16 logits 27.5 us without alternatives (4.8
+// TB/s, what a large copy reaches), 33.6 with 5, 36 with 20, 46 with 64; float32
+// with 5 56.7; 1000 of 65536 with 20 39.8; one row of 131072 float32 with 20, in
+// 64 parts, 13 with the host's call. With all elements converted once and kept
+// (256 registers) the first took 65 with 5; with the largest of 64 columns for 64
+// alternatives, which leaves too many above it now and then, 711 with 64.
 #include <type_traits>
 
 #include "qlinear_kernels.hpp"
@@ -77,46 +84,107 @@ __device__ __forceinline__ float wave_sum(float v) {
 struct Shared {
   float lane_max[kWaves][64];
   float l[kWaves], s[kWaves];
+  float least[kWaves];
+  int ties[kWaves];
   uint64_t best[kWaves];
   uint64_t candidates[kCandidates];
   int count;
 };
 
-// The k-th largest of the 64 columns' maxima (column: a lane of all waves).
-__device__ __forceinline__ float threshold(float column, float top, int k) {
+// A value that the k-th largest element is not below: the k-th largest of 64
+// maxima (column: that of a lane of all waves) or, for more than 32, where those
+// would leave too many above it, of 256 (sh.lane_max). top: the largest.
+__device__ __forceinline__ float threshold(Shared& sh, float column, float top, int k) {
   if (k == 1) return top;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int larger = 0;
-  for (int j = 0; j < 64; ++j) larger += __shfl(column, j) > column ? 1 : 0;
-  float v = larger < k ? column : INFINITY;
+  float mine = column;
+  if (k <= 32) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      larger += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, column), j)) > mine ? 1 : 0;
+  } else {
+    mine = sh.lane_max[wave][lane];
+    for (int j = 0; j < kThreads; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(&sh.lane_max[0][0] + j);
+      larger += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+    }
+  }
+  float v = larger < k ? mine : INFINITY;
 #pragma unroll
   for (int j = 1; j < 64; j <<= 1) v = fminf(v, __shfl_xor(v, j));
-  return v;
+  if (k <= 32) return v;
+  if (lane == 0) sh.least[wave] = v;
+  __syncthreads();
+  return fminf(fminf(sh.least[0], sh.least[1]), fminf(sh.least[2], sh.least[3]));
 }
 
-// Calls put(rank, key) for the k largest keys of all threads. each(f) calls
-// f(key) for the thread's own keys that can be among them, all(f) for all of
-// its keys. Fewer than k: the others are not put.
-template <typename Each, typename All, typename Put>
-__device__ __forceinline__ void top_keys(int k, Shared& sh, Each each, All all, Put put) {
-  each([&](uint64_t key) {
+// Which of its keys a thread passes on, by their values.
+enum Pass { kNotBelow, kAbove, kAll };
+
+// Calls put(rank, key) for the k largest keys of all threads, of which one is
+// `least` or larger. each(pass, f) calls f(key) for the thread's own keys that are
+// to be passed on, and tied(turn, f) for those of turn 0 .. turns - 1 that have the
+// value `least`; turns are in the order of indexes, and in a turn threads are.
+// Fewer than k: the others are not put. Returns how many there were to choose from.
+template <typename Each, typename Tied, typename Put>
+__device__ __forceinline__ int top_keys(int k, Shared& sh, Each each, int turns, Tied tied, Put put) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto push = [&](uint64_t key) {
     const int at = atomicAdd(&sh.count, 1);
     if (at < kCandidates) sh.candidates[at] = key;
-  });
+  };
+  each(std::integral_constant<int, kNotBelow>{}, push);
   __syncthreads();
-  const int n = sh.count;
+  int n = sh.count;
+  if (n > kCandidates) {
+    // Many of one value: those above it, and of it the first ones by index.
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    each(std::integral_constant<int, kAbove>{}, push);
+    __syncthreads();
+    n = sh.count;
+    for (int turn = 0; turn < turns && n < k; ++turn) {
+      int own = 0;
+      tied(turn, [&](uint64_t) { ++own; });
+      int upto = own;
+#pragma unroll
+      for (int j = 1; j < 64; j <<= 1) {
+        const int o = __shfl_up(upto, j);
+        if (lane >= j) upto += o;
+      }
+      if (lane == 63) sh.ties[wave] = upto;
+      __syncthreads();
+      int at = n + upto - own, all = 0;
+#pragma unroll
+      for (int j = 0; j < kWaves; ++j) {
+        if (j < wave) at += sh.ties[j];
+        all += sh.ties[j];
+      }
+      tied(turn, [&](uint64_t key) {
+        if (at < k) sh.candidates[at] = key;
+        ++at;
+      });
+      n = min(n + all, k);
+      __syncthreads();
+    }
+  }
   if (n <= kCandidates) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint64_t key = sh.candidates[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) rank += sh.candidates[j] > key ? 1 : 0;
       if (rank < k) put(rank, key);
     }
-    return;
+    return n;
   }
+  // More different values than that are above it: one maximum after another.
   uint64_t last = ~0ull;
   for (int r = 0; r < k; ++r) {
     uint64_t best = 0;
-    all([&](uint64_t key) {
+    each(std::integral_constant<int, kAll>{}, [&](uint64_t key) {
       if (key < last && key > best) best = key;
     });
 #pragma unroll
@@ -125,12 +193,13 @@ __device__ __forceinline__ void top_keys(int k, Shared& sh, Each each, All all, 
       best = o > best ? o : best;
     }
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh.best[threadIdx.x >> 6] = best;
+    if (lane == 0) sh.best[wave] = best;
     __syncthreads();
     for (int j = 0; j < kWaves; ++j) best = sh.best[j] > best ? sh.best[j] : best;
     if (threadIdx.x == 0) put(r, best);
     last = best;
   }
+  return n;
 }
 
 // A part's results (m the maximum, l and s as above), or a row's.
@@ -190,12 +259,24 @@ struct Group {
     const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFC00FC00u;
     v = make_uint4(w, w, w, w);
   }
-  __device__ __forceinline__ void set(int e, const T* p) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (sizeof(T) == 4)
-      w[e] = __builtin_bit_cast(uint32_t, *p);
-    else
-      w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | ((uint32_t)*p << 16) : (w[e / 2] & 0xFFFF0000u) | *p;
+  // Elements at .. of a row of n; what is outside it is -infinity.
+  __device__ __forceinline__ void load(const T* row, int at, int n) {
+    if (at >= 0 && at <= n - kSize) {
+      v = *reinterpret_cast<const uint4*>(row + at);
+      return;
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < kSize; ++e) {
+      uint32_t x = sizeof(T) == 4 ? 0xFF800000u : 0xFC00u;
+      if (at + e >= 0 && at + e < n) {
+        if constexpr (sizeof(T) == 4)
+          x = __builtin_bit_cast(uint32_t, row[at + e]);
+        else
+          x = row[at + e];
+      }
+      w[e * sizeof(T) / 4] |= sizeof(T) == 4 ? x : x << 16 * (e % 2);
+    }
     v = make_uint4(w[0], w[1], w[2], w[3]);
   }
   // NaN is left out.
@@ -224,34 +305,38 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a, Parts 
   const int first = (part * NG * kThreads + t) * G - shift;     // the thread's groups start kThreads * G elements apart
   if (t == 0) sh.count = 0;
 
+  auto place = [&](int i) { return first + i * kThreads * G; };
   Group<T> x[NG];
-  const bool few = a.vocab < 2 * G;
-  if (!few) {
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
     // Groups that are not whole read the row's second, which is, instead of branching.
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int at = first + i * kThreads * G;
-      const bool whole = at >= 0 && at <= a.vocab - G;
-      x[i].v = *reinterpret_cast<const uint4*>(p + (whole ? at : G - shift));
-      if (!whole) x[i].none();
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NG; ++i) x[i].none();
+    const bool whole = place(i) >= 0 && place(i) <= a.vocab - G;
+    if (a.vocab >= 2 * G) x[i].v = *reinterpret_cast<const uint4*>(p + (whole ? place(i) : G - shift));
+    if (!whole) x[i].none();
   }
-  if (few || shift != 0 || a.vocab % G != 0) {
+  if (a.vocab < 2 * G || shift != 0 || a.vocab % G != 0) {
+    // A row's first group is a thread's first, its last one any.
+    const int last = (a.vocab - 1 + shift) / G * G - shift, i_last = (last - first) / (kThreads * G);
+    const bool has_last = last >= first && last == place(i_last) && i_last < NG;
+    if (place(0) > -G && place(0) < a.vocab) x[0].load(p, place(0), a.vocab);
+    Group<T> end;
+    end.none();
+    if (has_last) end.load(p, last, a.vocab);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int at = first + i * kThreads * G;
-      if ((few || at < 0 || at > a.vocab - G) && at > -G && at < a.vocab)
-        for (int e = 0; e < G; ++e)
-          if (at + e >= 0 && at + e < a.vocab) x[i].set(e, p + at + e);
-    }
+    for (int i = 0; i < NG; ++i)
+      if (has_last && i == i_last) x[i] = end;
   }
 
+  // The elements stay as loaded: converted ones are not kept from one use to the next.
+  auto keep = [&]() {
+#pragma unroll
+    for (int i = 0; i < NG; ++i) asm("" : "+v"(x[i].v.x), "+v"(x[i].v.y), "+v"(x[i].v.z), "+v"(x[i].v.w));
+  };
+  keep();
   float mine = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NG; ++i) mine = fmaxf(mine, x[i].max());
+  keep();
   sh.lane_max[wave][lane] = mine;
   __syncthreads();
   float column = sh.lane_max[0][lane];
@@ -290,39 +375,40 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a, Parts 
   }
   if (a.top == 0) return;
 
-  const float least = threshold(column, r.m, a.top);
+  keep();
+  const float least = threshold(sh, column, r.m, a.top);
   const bool nan = r.l != r.l;        // there may be NaN, which no maximum shows
-  auto put = [&](int rank, uint64_t key) {
-    if (direct)
-      write_top<T>(a, row, r, rank, key);
-    else
-      parts.keys[(int64_t)blockIdx.x * a.top + rank] = key;
+  // The thread's groups that hold one of the largest: few, so they are loaded again.
+  unsigned groups = 0;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) groups |= x[i].max() >= least || nan ? 1u << i : 0u;
+  auto keys_of = [&](int i, auto wanted, auto f) {
+    Group<T> y;
+    y.load(p, place(i), a.vocab);
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+      const int at = place(i) + e;
+      if (wanted(y.get(e)) && at >= 0 && at < a.vocab) f(make_key(y.get(e), at));
+    }
   };
-  auto key_of = [&](int i, int e, auto f) {
-    const int at = first + i * kThreads * G + e;
-    if (at >= 0 && at < a.vocab) f(make_key(x[i].get(e), at));
-  };
-  top_keys(
+  const int found = top_keys(
       a.top, sh,
-      [&](auto f) {
-        if (mine < least && !nan) return;
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          if (x[i].max() < least && !nan) continue;
-#pragma unroll
-          for (int e = 0; e < G; ++e)
-            if (!(x[i].get(e) < least)) key_of(i, e, f);
-        }
+      [&](auto pass, auto f) {
+        constexpr int kPass = decltype(pass)::value;
+#pragma unroll 1
+        for (unsigned m = kPass == kAll ? (1u << NG) - 1 : groups; m != 0; m &= m - 1)
+          keys_of(__builtin_ctz(m),
+                  [&](float y) { return kPass == kAll || !(kPass == kAbove ? y <= least : y < least); }, f);
       },
-      [&](auto f) {
-#pragma unroll
-        for (int i = 0; i < NG; ++i)
-#pragma unroll
-          for (int e = 0; e < G; ++e) key_of(i, e, f);
-      },
-      put);
+      NG, [&](int i, auto f) { keys_of(i, [&](float y) { return y == least; }, f); },
+      [&](int rank, uint64_t key) {
+        if (direct)
+          write_top<T>(a, row, r, rank, key);
+        else
+          parts.keys[(int64_t)blockIdx.x * a.top + rank] = key;
+      });
   // A part of fewer elements than that (never a whole row).
-  if (!direct && t < a.top && t >= sh.count) parts.keys[(int64_t)blockIdx.x * a.top + t] = 0;
+  if (!direct && t < a.top && t >= found) parts.keys[(int64_t)blockIdx.x * a.top + t] = 0;
 }
 
 // A workgroup joins a row's parts.
@@ -373,21 +459,26 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, P
   }
   if (t == 0) write_row<T>(a, row, r);
   if (a.top == 0) return;
-  const float least = threshold(column, wave_max(column), a.top);
-  const uint64_t least_key = (uint64_t)ordered(least) << 32;
-  auto all = [&](auto f) {
-    for (int i = t; i < n; i += kThreads)
-      if (keys[i] != 0) f(keys[i]);
-  };
+  const float least = threshold(sh, column, wave_max(column), a.top);
+  const uint32_t from = ordered(least);
+  // Keys stand in the order of indexes where their values are the same.
   top_keys(
       a.top, sh,
-      [&](auto f) {
-        if (most < least_key || none) return;
-        all([&](uint64_t key) {
-          if (key >= least_key) f(key);
-        });
+      [&](auto pass, auto f) {
+        constexpr int kPass = decltype(pass)::value;
+        if (none || (kPass != kAll && (uint32_t)(most >> 32) < from)) return;
+        for (int i = t; i < n; i += kThreads) {
+          const uint64_t key = keys[i];
+          const uint32_t v = (uint32_t)(key >> 32);
+          if (key != 0 && (kPass == kAll || (kPass == kAbove ? v > from : v >= from))) f(key);
+        }
       },
-      all, [&](int rank, uint64_t key) { write_top<T>(a, row, r, rank, key); });
+      (n + kThreads - 1) / kThreads,
+      [&](int turn, auto f) {
+        const int i = turn * kThreads + t;
+        if (i < n && (uint32_t)(keys[i] >> 32) == from) f(keys[i]);
+      },
+      [&](int rank, uint64_t key) { write_top<T>(a, row, r, rank, key); });
 }
 
 struct Plan {
@@ -397,10 +488,13 @@ struct Plan {
 
 // As few parts as give every CU two workgroups.
 constexpr int kMaxGroups = 16, kWanted = 512;
-Plan make_plan(int rows, int vocab, bool f32) {
+Plan make_plan(int rows, int vocab, bool f32, bool whole) {
   const int size = f32 ? 4 : 8;
-  // A row that starts inside a group has one more.
-  auto parts = [&](int groups) { return (int)(((int64_t)vocab + size - 1 + kThreads * groups * size - 1) / (kThreads * groups * size)); };
+  // Rows that start inside a group (not `whole`) may have one more.
+  auto parts = [&](int groups) {
+    const int64_t all = (int64_t)vocab + (whole ? 0 : size - 1), part = kThreads * groups * size;
+    return (int)((all + part - 1) / part);
+  };
   int g = kMaxGroups;
   while (g > 1 && (int64_t)rows * parts(g) < kWanted && parts(g / 2) <= kMaxParts) g /= 2;
   const int n = parts(g);
@@ -410,21 +504,26 @@ Plan make_plan(int rows, int vocab, bool f32) {
 
 }  // namespace
 
+// Whether all rows start at whole groups.
+static bool whole_rows(const LogprobArgs& a) {
+  return ((uintptr_t)a.logits & 15) == 0 && (a.rows == 1 || a.stride * (a.f32 ? 4 : 2) % 16 == 0);
+}
+
 size_t logprob_workspace_need(const LogprobArgs& a) {
-  const Plan p = make_plan(a.rows, a.vocab, a.f32);
+  const Plan p = make_plan(a.rows, a.vocab, a.f32, whole_rows(a));
   return p.parts == 1 ? 0 : (size_t)a.rows * p.parts * (sizeof(float4) + sizeof(uint64_t) * a.top);
 }
 
 size_t logprob_workspace_bytes(const LogprobArgs& a) {
   // Fewer rows are cut into more parts, but only while they are below kWanted in all
-  // (halving a part less than doubles their number); shorter rows have fewer.
-  const int64_t most = (int64_t)a.rows * make_plan(1 << 22, a.vocab, a.f32).parts;
-  const size_t parts = make_plan(1, a.vocab, a.f32).parts == 1 ? 0 : most > 2 * kWanted ? most : 2 * kWanted;
+  // (halving a part doubles their number at most); shorter rows have fewer.
+  const int64_t most = (int64_t)a.rows * make_plan(1 << 22, a.vocab, a.f32, false).parts;
+  const size_t parts = make_plan(1, a.vocab, a.f32, false).parts == 1 ? 0 : most > 2 * kWanted ? most : 2 * kWanted;
   return parts * (sizeof(float4) + sizeof(uint64_t) * a.top);
 }
 
 hipError_t launch_logprob(const LogprobArgs& a, void* ws, hipStream_t stream) {
-  const Plan p = make_plan(a.rows, a.vocab, a.f32);
+  const Plan p = make_plan(a.rows, a.vocab, a.f32, whole_rows(a));
   Parts parts = {(float4*)ws, nullptr, p.parts};
   if (p.parts > 1) parts.keys = (uint64_t*)(parts.sums + (int64_t)a.rows * p.parts);
   auto go = [&](auto type) {

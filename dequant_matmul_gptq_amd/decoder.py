@@ -575,17 +575,31 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top
         stride = V
     bits = 16 if logits.dtype is _F16 else 32
     tp = None if tokens is None else _operand(tokens, "tokens", _I32, (R,), dev)
+    lp = ep = vp = ip = None
     if out is None:
-        f32 = dict(dtype=_F32, device=logits.device)
-        wide = (R, top) if 0 < top else None
-        out = TokenLogprobs(None if tp is None else torch.empty(R, **f32), torch.empty(R, **f32) if entropy else None,
-                            None if wide is None else torch.empty(wide, **f32),
-                            None if wide is None else torch.empty(wide, dtype=_I32, device=logits.device))
-    wanted = (tokens is not None, bool(entropy), top > 0, top > 0)
-    lp, ep, vp, ip = (_operand(t, name, dtype, shape, dev) if w and t is not None else None for t, name, dtype, shape, w in
-                      zip(out, TokenLogprobs._fields, (_F32, _F32, _F32, _I32), ((R,), (R,), (R, top), (R, top)), wanted))
-    if any(w != (t is not None) for w, t in zip(wanted, out)):
-        raise ValueError("out must hold what is asked for and None for the rest")
+        on = logits.device
+        logprob = h = values = ids = None
+        if tp is not None:
+            logprob = torch.empty(R, dtype=_F32, device=on)
+            lp = logprob.data_ptr()
+        if entropy:
+            h = torch.empty(R, dtype=_F32, device=on)
+            ep = h.data_ptr()
+        if top > 0:
+            values, ids = torch.empty((R, top), dtype=_F32, device=on), torch.empty((R, top), dtype=_I32, device=on)
+            vp, ip = values.data_ptr(), ids.data_ptr()
+        out = TokenLogprobs(logprob, h, values, ids)
+    else:
+        wanted = (tokens is not None, bool(entropy), top > 0, top > 0)
+        if any(w != (t is not None) for w, t in zip(wanted, out)):
+            raise ValueError("out must hold what is asked for and None for the rest")
+        if tokens is not None:
+            lp = _operand(out.logprob, "logprob", _F32, (R,), dev)
+        if entropy:
+            ep = _operand(out.entropy, "entropy", _F32, (R,), dev)
+        if top > 0:
+            vp = _operand(out.top_logprob, "top_logprob", _F32, (R, top), dev)
+            ip = _operand(out.top_id, "top_id", _I32, (R, top), dev)
     if (R | V | top) >> 31:
         R, V, top = _int32(R, V, top)
     n = ctypes.c_size_t(0)
