@@ -113,8 +113,11 @@ inline int64_t chunk_tiles(const AttentionArgs& a, int group) {
 // Shared prefixes leave partial results where others write the output. All
 // rows of those stand in one array: whole tiles [2][rows of the output] (0: of a
 // prefix, 1: of a sequence's own tokens), the chunk kernel's ranges
-// [splits][chunk_kinds][rows] from row chunk0 on, the few-row kernel's from few0
-// on. rows: of the output.
+// [items][kv_heads][kChunkRows] from row chunk0 on, the few-row kernel's from few0
+// on. rows: of the output. found [2][rows] says where each row has its results of
+// either kind: x of them, the first in row y, result i > 0 in row z + i w. The
+// workgroup that has the first one writes it, so that the join need not look
+// through the lengths again.
 struct Partials {
   float* o;
   float2* ml;
@@ -122,7 +125,7 @@ struct Partials {
 };
 struct ViewPartials : Partials {
   int64_t chunk0, few0;
-  int chunk_kinds;
+  int4* found;
 };
 
 // The kernels' loops come in kinds of step: whole ones that all rows see all
@@ -164,9 +167,19 @@ __host__ __device__ __forceinline__ void bounded_rows(int q0, int q1, int tokens
   w.n = end > w.q0 ? end - w.q0 : 0;
 }
 
+// Number i of an array that no launch writes: through the scalar cache where i
+// is uniform.
+__host__ __device__ __forceinline__ int number(const int32_t* p, int i) {
+#ifdef __HIP_DEVICE_COMPILE__
+  return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[i];
+#else
+  return p[i];
+#endif
+}
+
 // First row of sequence s of n (s == n: the row after the last).
 __host__ __device__ __forceinline__ int first_row(const ViewArgs& a, int n, int s) {
-  return a.q_start ? a.q_start[s] : s * (a.tokens / n);
+  return a.q_start ? number(a.q_start, s) : s * (a.tokens / n);
 }
 
 // The group of sequence s, -1 if none.
@@ -175,12 +188,12 @@ __host__ __device__ __forceinline__ int group_of(const ViewArgs& a, int s) {
   int lo = 0, hi = a.groups;       // the last one that starts at s or before
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (a.shared_start[mid] <= s)
+    if (number(a.shared_start, mid) <= s)
       lo = mid + 1;
     else
       hi = mid;
   }
-  return lo > 0 && s < a.shared_start[lo] ? lo - 1 : -1;
+  return lo > 0 && s < number(a.shared_start, lo) ? lo - 1 : -1;
 }
 
 // Sequence b's rows and length, bounded by what the buffers hold. With shared
@@ -191,20 +204,20 @@ __host__ __device__ __forceinline__ void sequence(const ViewArgs& a, const qline
   w.all = b < a.groups;
   w.low = 0;
   if (w.all) {
-    const int s0 = a.shared_start ? min(max(a.shared_start[b], 0), sequences) : 0;
-    const int s1 = a.shared_start ? min(a.shared_start[b + 1], sequences) : sequences;
+    const int s0 = a.shared_start ? min(max(number(a.shared_start, b), 0), sequences) : 0;
+    const int s1 = a.shared_start ? min(number(a.shared_start, b + 1), sequences) : sequences;
     bounded_rows(first_row(a, sequences, s0), first_row(a, sequences, max(s0, s1)), a.tokens, w);
-    w.len = bounded_length(a.shared_len[b], a.table_width, c.page_size);
+    w.len = bounded_length(number(a.shared_len, b), a.table_width, c.page_size);
     w.row = min(s0, sequences - 1);
     if (w.len == 0) w.n = 0;
     return;
   }
   w.row = b - a.groups;
   bounded_rows(first_row(a, sequences, w.row), first_row(a, sequences, w.row + 1), a.tokens, w);
-  w.len = bounded_length(a.kv_len[w.row], a.table_width, c.page_size);
+  w.len = bounded_length(number(a.kv_len, w.row), a.table_width, c.page_size);
   if (a.groups > 0) {
     const int g = group_of(a, w.row);
-    if (g >= 0) w.low = bounded_length(a.shared_len[g], a.table_width, c.page_size);
+    if (g >= 0) w.low = bounded_length(number(a.shared_len, g), a.table_width, c.page_size);
   }
 }
 __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
@@ -330,11 +343,105 @@ __device__ __forceinline__ bool find_tile(const Args& a, const qlinear_kv_cache&
   return false;
 }
 
+// ---- the chunk kernel's items with shared prefixes: a tile's steps in ranges of
+// `chunk`, such that the chip is filled by what the lengths on the device are,
+// and one round of workgroups takes them all (three groups of 8192, 4096 and 640
+// tokens over Q8, 640, 288 and 32 rows a key/value head: 95 us with as many
+// ranges for all tiles as the longest may have, 116 us with 66 items of 13 steps
+// for 64 places, 81 us so).
+struct Ranges {
+  int chunk;
+  __device__ __forceinline__ int of(int steps) const { return steps <= chunk ? 1 : (steps + chunk - 1) / chunk; }
+};
+// Tiles of sequence w, 0 if it is not the chunk kernel's, and each one's steps at most.
+__device__ __forceinline__ int chunk_item(const ViewArgs& a, const Plan& plan, int group, int shift, const Work& w,
+                                          int& steps) {
+  const int64_t rows = (int64_t)w.n * group;
+  steps = max(((w.len - 1) >> shift) - (first_of(a, w, position(a, w, 0)) >> shift), 0) + 1;
+  steps = min(steps, 1 << 22);     // 512 tiles' sum fits; a last range has the rest
+  return rows < plan.min_rows ? 0 : (int)((rows + kChunkRows - 1) / kChunkRows);
+}
+__device__ __forceinline__ int wave_total(int x) {
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) x += __shfl_xor(x, k);
+  return __builtin_amdgcn_readfirstlane(x);
+}
+__device__ __forceinline__ Ranges chunk_ranges(const ViewArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                               int group, int shift) {
+  if (plan.slots == 0) return {INT32_MAX};      // more tiles than the chip holds, as it is
+  int tiles, items;
+  unsigned total;
+  auto sum = [&](const Ranges& ranges) {
+    int n_all = 0, items_all = 0;
+    total = 0;
+    for (int b = threadIdx.x & 63; b < a.batch; b += 64) {
+      Work w;
+      int steps;
+      sequence(a, c, b, w);
+      const int n = chunk_item(a, plan, group, shift, w, steps);
+      n_all += n;
+      items_all += n * ranges.of(steps);
+      total += n * steps;
+    }
+    tiles = wave_total(n_all);
+    items = wave_total(items_all);
+    total = wave_total(total);
+  };
+  sum({INT32_MAX});
+  if (tiles >= plan.slots) return {INT32_MAX};
+  Ranges ranges = {max(8, (int)((total + plan.slots - 1) / plan.slots))};
+  sum(ranges);
+  // Every tile's last range may be a short one.
+  const int free = plan.slots - tiles;
+  if (items > plan.slots) ranges.chunk = (int)((total + free - 1) / free);
+  return ranges;
+}
+// Item y's sequence, tile, range and number of ranges, found by all lanes
+// together. False if there are fewer.
+__device__ __forceinline__ bool find_item(const ViewArgs& a, const qlinear_kv_cache& c, const Plan& plan, int group,
+                                          int shift, const Ranges& ranges, int y, Work& w, int& tile, int& split,
+                                          int& splits) {
+  const int lane = threadIdx.x & 63;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    int n = 0, each = 1;
+    if (b0 + lane < a.batch) {
+      Work t;
+      int steps;
+      sequence(a, c, b0 + lane, t);
+      n = chunk_item(a, plan, group, shift, t, steps);
+      each = ranges.of(steps);
+      n *= each;
+    }
+    int upto = n;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+      const int o = __shfl_up(upto, k);
+      if (lane >= k) upto += o;
+    }
+    const uint64_t past = __ballot(upto > y);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      y -= __builtin_amdgcn_readlane(upto - n, at);
+      splits = __builtin_amdgcn_readlane(each, at);
+      tile = __builtin_amdgcn_readfirstlane(y / splits);
+      split = y - tile * splits;
+      sequence(a, c, b0 + at, w);
+      return true;
+    }
+    y -= __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
 // ---- the few-row kernel's spans
 // A sequence's row tiles, and the steps counted for each (from the first token
 // that its first new token sees; 1 where none sees any, for the zeros).
 // Views number the steps that their rows may see from 0 on: `sinks` steps of
-// sinks, then from first_step on, which is `gap` further than its number.
+// sinks, then from first_step on, which is `gap` further than its number. They
+// count whole turns of a workgroup's waves, which cost what they cost however
+// many of the waves have a step: else a span takes many short sequences, one
+// after another (30 of 4 to 900 tokens behind three prefixes, 4 new ones each,
+// 64/8 heads, Q8: 39 us with single steps, 18.5 us so).
 struct Item {
   int tiles, steps, first_step;
   int sinks, gap;
@@ -349,6 +456,7 @@ __host__ __device__ __forceinline__ Item few_item(const Args& a, const Plan& pla
   it.sinks = sink_steps(a, it.first_step, 5);
   it.gap = it.first_step - it.sinks;
   it.steps = it.sinks + max((w.len - 1) / kStep - it.first_step, 0) + 1;
+  if constexpr (kIsView<Args>) it.steps = (it.steps + 3) & ~3;      // whole turns, see Item
   return it;
 }
 static_assert(kStep == 1 << 5);

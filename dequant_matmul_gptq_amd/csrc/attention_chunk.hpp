@@ -123,36 +123,53 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n32 = lane & 31, h = lane >> 5;
   const int group = a.q_heads / c.kv_heads;
-  const int head = blockIdx.x % c.kv_heads, split = blockIdx.y;
+  const int head = blockIdx.x % c.kv_heads;
+  int split = blockIdx.y, splits = plan.splits, chunk = plan.chunk;
   const int page_shift = __builtin_ctz(c.page_size);
   const int group_shift = B == 16 ? 0 : __builtin_ctz(c.group);
 
   // Later rows see more tokens: they start first (shared prefixes, which do, come first).
   Work w;
   int tile = 0;
-  bool forward = false;
-  if constexpr (kView) forward = a.groups > 0;
-  if (!find_tile(a, c, plan, group, (forward ? blockIdx.x : gridDim.x - 1 - blockIdx.x) / c.kv_heads, w, tile)) return;
+  bool shared = false;
+  if constexpr (kView) shared = a.groups > 0;
+  if (shared) {
+    if constexpr (kView) {
+      constexpr int kShift = T == 64 ? 6 : 5;
+      const Ranges ranges = chunk_ranges(a, c, plan, group, kShift);
+      chunk = ranges.chunk;
+      if (!find_item(a, c, plan, group, kShift, ranges, blockIdx.x / c.kv_heads, w, tile, split, splits)) return;
+    }
+  } else {
+    if (!find_tile(a, c, plan, group, (gridDim.x - 1 - blockIdx.x) / c.kv_heads, w, tile)) return;
+  }
   row_tile(a, group, tile * kChunkRows, kChunkRows, w);
   const int step_lo = w.lo_min / T;
   const int step_end = w.p_max < 0 ? 0 : w.p_max / T + 1;
   // Views number the steps that the tile sees from 0 on, those of sinks first.
   const int sinks = sink_steps(a, step_lo, T == 64 ? 6 : 5), gap = kView ? step_lo - sinks : 0;
-  const int begin = (kView ? 0 : step_lo) + split * plan.chunk;
-  const int end = split == plan.splits - 1 ? step_end - gap : min(begin + plan.chunk, step_end - gap);
+  const int begin = (kView ? 0 : step_lo) + split * chunk;
+  const int end = split == splits - 1 ? step_end - gap : min(begin + chunk, step_end - gap);
   auto token = [&](int step) { return (kView && step >= sinks ? step + gap : step) * T; };     // a step's first
-  // Where partial results go, if the launch leaves any; whether this one does.
-  bool partial = plan.splits > 1;
+  // Where partial results go, if the launch leaves any: by row of the output, or of
+  // the tile.
+  const bool partial = splits > 1 || shared, by_tile = shared && splits > 1;
   int64_t part_row0 = split * part.rows;
-  if constexpr (kView) {
-    part_row0 = plan.splits > 1 ? part.chunk0 + ((int64_t)split * part.chunk_kinds + !w.all * (part.chunk_kinds - 1)) * part.rows
-                                : (w.all ? 0 : part.rows);
-    partial = partial || a.groups > 0;
-  }
-  if (begin >= end && plan.splits > 1) {   // nothing in this range
+  if constexpr (kView)
+    if (shared) {
+      const int64_t whole = w.all ? 0 : part.rows;
+      part_row0 = by_tile ? part.chunk0 + (int64_t)blockIdx.x * kChunkRows : whole;
+      if (split == 0 && (int)threadIdx.x < w.rows) {
+        const int rr = w.row0 + threadIdx.x;
+        const int64_t out = (int64_t)(w.q0 + rr / group) * a.q_heads + head * group + rr % group;
+        const int row = (int)(part_row0 + (by_tile ? threadIdx.x : out));
+        part.found[whole + out] = make_int4(splits, row, row, c.kv_heads * kChunkRows);
+      }
+    }
+  if (begin >= end && splits > 1) {   // nothing in this range
     for (int r = threadIdx.x; r < w.rows; r += kChunkThreads) {
       const int rr = w.row0 + r;
-      part.ml[part_row0 + (int64_t)(w.q0 + rr / group) * a.q_heads + head * group + rr % group] =
+      part.ml[part_row0 + (by_tile ? r : (int64_t)(w.q0 + rr / group) * a.q_heads + head * group + rr % group)] =
           make_float2(-INFINITY, 0.0f);
     }
     return;
@@ -549,7 +566,8 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
         }
       }
   } else {
-    float* out = part.o + (part_row0 + out_row) * D;
+    const int64_t part_row = part_row0 + (by_tile ? row : out_row);
+    float* out = part.o + part_row * D;
 #pragma unroll
     for (int d = 0; d < kOutTiles; ++d)
 #pragma unroll
@@ -568,7 +586,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
       if constexpr (kView)
         sees = begin < end &&
                (max(first, token(begin)) <= min(pos, token(end - 1) + T - 1) || token(begin) < min(a.sinks, pos + 1));
-      part.ml[part_row0 + out_row] = make_float2(m == -INFINITY ? (sees ? kLowest : m) : m * sc, l);
+      part.ml[part_row] = make_float2(m == -INFINITY ? (sees ? kLowest : m) : m * sc, l);
     }
   }
 }

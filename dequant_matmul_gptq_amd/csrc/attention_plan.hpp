@@ -315,8 +315,7 @@ hipError_t launch_attention(const qlinear_kv_cache& cache, const Args& a, void* 
   const int D = cache.head_dim, group = a.q_heads / cache.kv_heads;
   if (r.chunk) {
     const Plan& p = r.chunk_plan;
-    Parts part = partials<Parts>(ws, p.splits, r.chunk_rows, D);
-    if constexpr (kIsView<Args>) part.chunk_kinds = 1;
+    const Parts part = partials<Parts>(ws, p.splits, r.chunk_rows, D);
     const hipError_t e = chunk(D)(cache, a, p, part, stream);
     if (e != hipSuccess) return e;
     if (r.chunk_rows > 0) {
