@@ -117,14 +117,15 @@ inline int64_t chunk_tiles(const AttentionArgs& a, int group) {
 // on. rows: of the output. found [2][rows] says where each row has its results of
 // either kind: x of them, the first in row y, result i > 0 in row z + i w. The
 // workgroup that has the first one writes it, so that the join need not look
-// through the lengths again.
+// through the lengths again. Kind 1 starts at row own0; with sinks there is no
+// other, and what is whole stands in the output.
 struct Partials {
   float* o;
   float2* ml;
   int64_t rows;
 };
 struct ViewPartials : Partials {
-  int64_t chunk0, few0;
+  int64_t own0, chunk0, few0;
   int4* found;
 };
 
@@ -197,8 +198,9 @@ __host__ __device__ __forceinline__ int group_of(const ViewArgs& a, int s) {
 }
 
 // Sequence b's rows and length, bounded by what the buffers hold. With shared
-// prefixes those come first (batch counts both).
-__host__ __device__ __forceinline__ void sequence(const ViewArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
+// prefixes those come first (batch counts both), and the last step of it finds
+// where own tokens start.
+__host__ __device__ __forceinline__ void sequence_rows(const ViewArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
   const int sequences = a.batch - a.groups;
   w.b = b;
   w.all = b < a.groups;
@@ -215,10 +217,15 @@ __host__ __device__ __forceinline__ void sequence(const ViewArgs& a, const qline
   w.row = b - a.groups;
   bounded_rows(first_row(a, sequences, w.row), first_row(a, sequences, w.row + 1), a.tokens, w);
   w.len = bounded_length(number(a.kv_len, w.row), a.table_width, c.page_size);
-  if (a.groups > 0) {
-    const int g = group_of(a, w.row);
-    if (g >= 0) w.low = bounded_length(number(a.shared_len, g), a.table_width, c.page_size);
-  }
+}
+__host__ __device__ __forceinline__ void sequence_low(const ViewArgs& a, const qlinear_kv_cache& c, Work& w) {
+  if (a.groups == 0 || w.all) return;
+  const int g = group_of(a, w.row);
+  if (g >= 0) w.low = bounded_length(number(a.shared_len, g), a.table_width, c.page_size);
+}
+__host__ __device__ __forceinline__ void sequence(const ViewArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
+  sequence_rows(a, c, b, w);
+  sequence_low(a, c, w);
 }
 __device__ __forceinline__ void sequence(const AttentionArgs& a, const qlinear_kv_cache& c, int b, Work& w) {
   w.b = b;
@@ -353,70 +360,71 @@ struct Ranges {
   int chunk;
   __device__ __forceinline__ int of(int steps) const { return steps <= chunk ? 1 : (steps + chunk - 1) / chunk; }
 };
-// Tiles of sequence w, 0 if it is not the chunk kernel's, and each one's steps at most.
-__device__ __forceinline__ int chunk_item(const ViewArgs& a, const Plan& plan, int group, int shift, const Work& w,
-                                          int& steps) {
-  const int64_t rows = (int64_t)w.n * group;
-  steps = max(((w.len - 1) >> shift) - (first_of(a, w, position(a, w, 0)) >> shift), 0) + 1;
-  steps = min(steps, 1 << 22);     // 512 tiles' sum fits; a last range has the rest
-  return rows < plan.min_rows ? 0 : (int)((rows + kChunkRows - 1) / kChunkRows);
-}
 __device__ __forceinline__ int wave_total(int x) {
 #pragma unroll
   for (int k = 1; k < 64; k <<= 1) x += __shfl_xor(x, k);
   return __builtin_amdgcn_readfirstlane(x);
 }
-__device__ __forceinline__ Ranges chunk_ranges(const ViewArgs& a, const qlinear_kv_cache& c, const Plan& plan,
-                                               int group, int shift) {
-  if (plan.slots == 0) return {INT32_MAX};      // more tiles than the chip holds, as it is
-  int tiles, items;
-  unsigned total;
-  auto sum = [&](const Ranges& ranges) {
-    int n_all = 0, items_all = 0;
-    total = 0;
-    for (int b = threadIdx.x & 63; b < a.batch; b += 64) {
-      Work w;
-      int steps;
-      sequence(a, c, b, w);
-      const int n = chunk_item(a, plan, group, shift, w, steps);
-      n_all += n;
-      items_all += n * ranges.of(steps);
-      total += n * steps;
+// Tiles, and each one's steps at most, of the lane's sequence of the 64 from b0
+// on; none if it is not the chunk kernel's.
+struct Tiles {
+  int n, steps;
+};
+__device__ __forceinline__ Tiles chunk_tiles_of(const ViewArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                                int group, int shift, int b0) {
+  const int b = b0 + (threadIdx.x & 63);
+  Tiles t = {0, 1};
+  if (b < a.batch) {
+    Work w;
+    sequence_rows(a, c, b, w);
+    const int64_t rows = (int64_t)w.n * group;
+    if (rows >= plan.min_rows) {
+      sequence_low(a, c, w);
+      t.n = (int)((rows + kChunkRows - 1) / kChunkRows);
+      t.steps = max(((w.len - 1) >> shift) - (first_of(a, w, position(a, w, 0)) >> shift), 0) + 1;
+      t.steps = min(t.steps, 1 << 22);     // 512 tiles' sum fits; a last range has the rest
     }
-    tiles = wave_total(n_all);
-    items = wave_total(items_all);
-    total = wave_total(total);
-  };
-  sum({INT32_MAX});
+  }
+  return t;
+}
+// t0: of the first 64 sequences, here and below.
+__device__ __forceinline__ Ranges chunk_ranges(const ViewArgs& a, const qlinear_kv_cache& c, const Plan& plan,
+                                               int group, int shift, const Tiles& t0) {
+  if (plan.slots == 0) return {INT32_MAX};      // more tiles than the chip holds, as it is
+  int tiles = t0.n;
+  unsigned total = t0.n * t0.steps;
+  for (int b0 = 64; b0 < a.batch; b0 += 64) {
+    const Tiles t = chunk_tiles_of(a, c, plan, group, shift, b0);
+    tiles += t.n;
+    total += t.n * t.steps;
+  }
+  tiles = wave_total(tiles);
   if (tiles >= plan.slots) return {INT32_MAX};
+  total = wave_total(total);
   Ranges ranges = {max(8, (int)((total + plan.slots - 1) / plan.slots))};
-  sum(ranges);
+  int items = t0.n * ranges.of(t0.steps);
+  for (int b0 = 64; b0 < a.batch; b0 += 64) {
+    const Tiles t = chunk_tiles_of(a, c, plan, group, shift, b0);
+    items += t.n * ranges.of(t.steps);
+  }
   // Every tile's last range may be a short one.
   const int free = plan.slots - tiles;
-  if (items > plan.slots) ranges.chunk = (int)((total + free - 1) / free);
+  if (wave_total(items) > plan.slots) ranges.chunk = (int)((total + free - 1) / free);
   return ranges;
 }
 // Item y's sequence, tile, range and number of ranges, found by all lanes
 // together. False if there are fewer.
 __device__ __forceinline__ bool find_item(const ViewArgs& a, const qlinear_kv_cache& c, const Plan& plan, int group,
-                                          int shift, const Ranges& ranges, int y, Work& w, int& tile, int& split,
-                                          int& splits) {
-  const int lane = threadIdx.x & 63;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    int n = 0, each = 1;
-    if (b0 + lane < a.batch) {
-      Work t;
-      int steps;
-      sequence(a, c, b0 + lane, t);
-      n = chunk_item(a, plan, group, shift, t, steps);
-      each = ranges.of(steps);
-      n *= each;
-    }
+                                          int shift, const Tiles& t0, const Ranges& ranges, int y, Work& w, int& tile,
+                                          int& split, int& splits) {
+  Tiles t = t0;
+  for (int b0 = 0;;) {
+    const int each = ranges.of(t.steps), n = t.n * each;
     int upto = n;
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) {
       const int o = __shfl_up(upto, k);
-      if (lane >= k) upto += o;
+      if ((int)(threadIdx.x & 63) >= k) upto += o;
     }
     const uint64_t past = __ballot(upto > y);
     if (past) {
@@ -429,8 +437,10 @@ __device__ __forceinline__ bool find_item(const ViewArgs& a, const qlinear_kv_ca
       return true;
     }
     y -= __builtin_amdgcn_readlane(upto, 63);
+    b0 += 64;
+    if (b0 >= a.batch) return false;
+    t = chunk_tiles_of(a, c, plan, group, shift, b0);
   }
-  return false;
 }
 
 // ---- the few-row kernel's spans

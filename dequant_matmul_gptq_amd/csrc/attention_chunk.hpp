@@ -136,9 +136,10 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   if (shared) {
     if constexpr (kView) {
       constexpr int kShift = T == 64 ? 6 : 5;
-      const Ranges ranges = chunk_ranges(a, c, plan, group, kShift);
+      const Tiles t0 = chunk_tiles_of(a, c, plan, group, kShift, 0);
+      const Ranges ranges = chunk_ranges(a, c, plan, group, kShift, t0);
       chunk = ranges.chunk;
-      if (!find_item(a, c, plan, group, kShift, ranges, blockIdx.x / c.kv_heads, w, tile, split, splits)) return;
+      if (!find_item(a, c, plan, group, kShift, t0, ranges, blockIdx.x / c.kv_heads, w, tile, split, splits)) return;
     }
   } else {
     if (!find_tile(a, c, plan, group, (gridDim.x - 1 - blockIdx.x) / c.kv_heads, w, tile)) return;
@@ -157,7 +158,7 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   int64_t part_row0 = split * part.rows;
   if constexpr (kView)
     if (shared) {
-      const int64_t whole = w.all ? 0 : part.rows;
+      const int64_t whole = w.all ? 0 : part.own0;
       part_row0 = by_tile ? part.chunk0 + (int64_t)blockIdx.x * kChunkRows : whole;
       if (split == 0 && (int)threadIdx.x < w.rows) {
         const int rr = w.row0 + threadIdx.x;

@@ -621,7 +621,18 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
       int64_t part_row = part_row0 + rr;
       if constexpr (kView) {
         final = alone && a.groups == 0;
-        part_row = alone ? (w.all ? 0 : part.rows) + out_row : part.few0 + part_row;
+        const int64_t whole = (w.all ? 0 : part.own0) + out_row;
+        part_row = alone ? whole : part.few0 + part_row;
+        if (d0 == 0 && i0 == 0 && (plan.workers > 0 || a.groups > 0)) {
+          // A tile that goes on behind this span: others have spans of stop / (worker + 1) steps each.
+          int4 f = make_int4(1, (int)part_row, 0, 0);
+          if (!alone) {
+            f.x = (int)((unsigned)(at + it.steps - 1) / ((unsigned)stop / (worker + 1u))) - worker + 1;
+            f.z = (int)part_row - slot * (16 * NT);
+            f.w = c.kv_heads * 2 * (16 * NT);
+          }
+          part.found[whole] = f;
+        }
       }
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
@@ -648,17 +659,6 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
           sees = begin < end && (max(fr, token(begin)) <= min(pr, token(end - 1) + kStep - 1) ||
                                  token(begin) < min(a.sinks, pr + 1));
         part.ml[part_row] = make_float2(top == -INFINITY && sees ? kLowest : top, total);
-        if constexpr (kView)
-          if (a.groups > 0 && i0 == 0) {
-            // A tile that goes on behind this span: others have spans of stop / (worker + 1) steps each.
-            int4 f = make_int4(1, (int)part_row, 0, 0);
-            if (!alone) {
-              f.x = (int)((unsigned)(at + it.steps - 1) / ((unsigned)stop / (worker + 1u))) - worker + 1;
-              f.z = (int)part_row - slot * (16 * NT);
-              f.w = c.kv_heads * 2 * (16 * NT);
-            }
-            part.found[(w.all ? 0 : part.rows) + out_row] = f;
-          }
       }
     }
   }

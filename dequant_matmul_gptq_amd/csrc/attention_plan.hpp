@@ -201,6 +201,17 @@ struct Route {
   int64_t few_rows, chunk_rows;     // rows of the partial results, 0 if not split
 };
 
+// Rows that a view's sequences likely have in the few-row kernel, where at most
+// cap: their mean. One of more has several tiles, which share what they read
+// through L2 (36 single tokens and 4 drafts of 4 over up to 65000 tokens in a
+// window of 4096, 64/8 heads, Q8: tiles of 32 rows 75.6 us, of 16 64.3 us).
+inline int64_t likely_rows(int64_t cap, int64_t mean) { return cap < mean ? cap : mean; }
+
+// The join of views (attention_views.hip): of the results in `total` rows, `most`
+// of a row of the output at most.
+hipError_t launch_view_join(const qlinear_kv_cache& c, const ViewArgs& a, const ViewPartials& part, int64_t total,
+                            int most, hipStream_t stream);
+
 template <class Args>
 Route make_route(const qlinear_kv_cache& c, const Args& a) {
   const int64_t group = a.q_heads / c.kv_heads, most = a.max_q_len * group;
@@ -211,11 +222,13 @@ Route make_route(const qlinear_kv_cache& c, const Args& a) {
     Plan& p = r.few_plan;
     r.few_cap = (int)(most < kFewRows ? most : kFewRows);
     // Two tiles of 256 wide heads do not fit the registers.
-    p.rows = r.few_cap <= 16 || c.head_dim == 256 ? 16 : 32;
+    int64_t likely = r.few_cap;
+    if constexpr (kIsView<Args>) likely = likely_rows(r.few_cap, a.tokens * group / a.batch);
+    p.rows = likely <= 16 || c.head_dim == 256 ? 16 : 32;
     p.min_rows = 1;
     p.max_rows = kFewRows;
     p.tiles = (r.few_cap + p.rows - 1) / p.rows;
-    p.once = p.tiles == 1;
+    p.once = likely <= p.rows;
     const int64_t tiles = (int64_t)(r.few_cap + p.rows - 1) / p.rows * a.batch;
     const int64_t steps = plan_steps(a, kStep);
     if (steps > kWholeSteps) {
@@ -263,12 +276,18 @@ Parts partials(void* ws, int64_t ranges, int64_t rows, int D) {
 }
 
 // The two kernels' launches follow one another on the stream and share the workspace.
+// Views' calls find their rows' results by what the few-row kernel says of them.
+inline size_t found_bytes(const AttentionArgs&) { return 0; }
+inline size_t found_bytes(const ViewArgs& a) {
+  return (size_t)a.tokens * a.q_heads * (a.groups > 0 ? 2 : 1) * sizeof(int4);
+}
+
 template <class Args>
 size_t workspace_need(const qlinear_kv_cache& cache, const Args& a) {
   const Route r = make_route(cache, a);
   const size_t few = partial_bytes(1, r.few_rows, cache.head_dim);
   const size_t chunk = partial_bytes(r.chunk_plan.splits, r.chunk_rows, cache.head_dim);
-  return few > chunk ? few : chunk;
+  return (few > chunk ? few : chunk) + (r.few_rows > 0 ? found_bytes(a) : 0);
 }
 
 // Smaller calls may need more (fewer rows are split further), so this goes over
@@ -293,6 +312,8 @@ size_t workspace_bytes(const qlinear_kv_cache& c, const Args& a) {
   if ((group <= kFewRows || a.batch > 1) && steps_of(kStep) > kWholeSteps) {
     if (c.head_dim == 256)
       few(16, cap);
+    else if (kIsView<Args>)
+      few(16, cap);
     else if (group <= 16)
       few(16, cap < 16 ? cap : 16);
     if (c.head_dim != 256 && cap > 16) few(32, cap);
@@ -304,7 +325,7 @@ size_t workspace_bytes(const qlinear_kv_cache& c, const Args& a) {
     const int64_t r = all < 512 * kChunkRows ? all : 512 * kChunkRows;
     if (r > rows) rows = r;
   }
-  return partial_bytes(1, rows, c.head_dim);
+  return partial_bytes(1, rows, c.head_dim) + (rows > 0 ? found_bytes(a) : 0);
 }
 
 // few(D), chunk(D): the launchers for heads of D.
@@ -328,12 +349,20 @@ hipError_t launch_attention(const qlinear_kv_cache& cache, const Args& a, void* 
   // Without q_start all sequences have the same length.
   if (r.few && (!r.chunk || a.q_start || (int64_t)(a.tokens / a.batch) * group <= kFewRows)) {
     const Plan& p = r.few_plan;
-    const Parts part = partials<Parts>(ws, 1, r.few_rows, D);
+    Parts part = partials<Parts>(ws, 1, r.few_rows, D);
+    if constexpr (kIsView<Args>) {
+      part.rows = (int64_t)a.tokens * a.q_heads;
+      part.found = (int4*)(part.ml + r.few_rows);
+    }
     const hipError_t e = few(D)(cache, a, p, part, stream);
     if (e != hipSuccess) return e;
-    if (r.few_rows > 0)
-      return launch_join<true>(cache, a, p, part, r.few_cap,
-                               dim3(1, (unsigned)cache.kv_heads, (unsigned)a.batch), p.workers / a.batch, stream);
+    if (r.few_rows > 0) {
+      if constexpr (kIsView<Args>)
+        return launch_view_join(cache, a, part, r.few_rows, p.workers, stream);
+      else
+        return launch_join<true>(cache, a, p, part, r.few_cap,
+                                 dim3(1, (unsigned)cache.kv_heads, (unsigned)a.batch), p.workers / a.batch, stream);
+    }
   }
   return hipSuccess;
 }

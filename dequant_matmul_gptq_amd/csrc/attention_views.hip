@@ -18,10 +18,6 @@ auto chunk_launcher(int D) {
   return D == 64 ? launch_view_chunk_64 : D == 128 ? launch_view_chunk_128 : launch_view_chunk_256;
 }
 
-struct SharedPlan {
-  Plan few, chunk;
-};
-
 // Sequence of row `token` of q, 0 .. n - 1; all lanes together.
 __device__ __forceinline__ int sequence_of(const ViewArgs& a, int n, int token) {
   if (!a.q_start) return min(token / (a.tokens / n), n - 1);
@@ -34,35 +30,36 @@ __device__ __forceinline__ int sequence_of(const ViewArgs& a, int n, int token) 
 }
 
 // Whether row `token` has results of (virtual) sequence b: not one of no
-// sequence, of one that is longer than the call said, of no shared prefix.
+// sequence, of one that is longer than the call said, of no shared prefix; with
+// sinks, of the few-row kernel's.
 __device__ __forceinline__ bool has_results(const ViewArgs& a, const qlinear_kv_cache& c, int b, int token) {
   Work w;
   sequence(a, c, b, w);
-  return token >= w.q0 && token < w.q0 + w.n && (w.all || w.n <= a.max_q_len);
+  return token >= w.q0 && token < w.q0 + w.n && (w.all || w.n <= a.max_q_len) &&
+         (a.groups > 0 || (int64_t)w.n * (a.q_heads / c.kv_heads) <= kFewRows);
 }
 
 constexpr int kJoinRows = 16;      // of a wave, at most
-// Joins the results of the rows of the output. WAVES == 1: a wave takes `rows`
-// rows, and finds where their results are once for the heads of a token; most
-// have two, which take no more than their loads. WAVES == 4: four waves to a row
-// share its many results out.
-template <int D, int WAVES>
-__global__ __launch_bounds__(256) void shared_join_kernel(ViewArgs a, qlinear_kv_cache c, ViewPartials part, int rows,
-                                                          int most, unsigned last) {
+// Joins the results of the rows of the output: a wave takes `rows` rows, and finds
+// which sequence they are of once for the heads of a token. Most rows have two
+// results, which take no more than their loads. (Four waves to a row lost: 2048
+// rows of 33 results 12.9 us and 9.7 so, 7680 of 10 28 and 12.5; 128 rows of 64
+// take 7.6.)
+template <int D>
+__global__ __launch_bounds__(256) void view_join_kernel(ViewArgs a, qlinear_kv_cache c, ViewPartials part, int rows,
+                                                        int most, unsigned last) {
   constexpr int kOwn = D / 64;      // elements of a lane
   typedef float own_t __attribute__((ext_vector_type(kOwn)));
   typedef _Float16 half_t __attribute__((ext_vector_type(kOwn)));
-  __shared__ own_t o_all[4][64];
-  __shared__ float2 ml_all[4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int64_t first = ((int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES) * rows;
+  const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * rows;
   const own_t* os = reinterpret_cast<const own_t*>(part.o) + lane;
   int token = -1;
   bool own = false, shared = false;
   // Where the results are: row first + i's in lane i.
   int4 found[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) found[k] = part.found[k * part.rows + min(first + lane % kJoinRows, part.rows - 1)];
+  for (int k = 0; k < 2; ++k) found[k] = part.found[k * part.own0 + min(first + lane % kJoinRows, part.rows - 1)];
   auto of_row = [&](int4 x, int i) {
     return make_int4(__builtin_amdgcn_readlane(x.x, i), __builtin_amdgcn_readlane(x.y, i),
                      __builtin_amdgcn_readlane(x.z, i), __builtin_amdgcn_readlane(x.w, i));
@@ -71,7 +68,7 @@ __global__ __launch_bounds__(256) void shared_join_kernel(ViewArgs a, qlinear_kv
     const int t = (int)(out / a.q_heads);
     if (t != token) {
       token = t;
-      const int s = sequence_of(a, a.batch - a.groups, t), g = group_of(a, s);
+      const int s = sequence_of(a, a.batch - a.groups, t), g = a.groups > 0 ? group_of(a, s) : -1;
       own = has_results(a, c, a.groups + s, t);
       shared = g >= 0 && has_results(a, c, g, t);
     }
@@ -81,6 +78,7 @@ __global__ __launch_bounds__(256) void shared_join_kernel(ViewArgs a, qlinear_kv
     int4 y = of_row(found[0], (int)(out - first)), x = of_row(found[1], (int)(out - first));
     y.x = shared ? min(max(y.x, 0), most) : 0;
     x.x = min(max(x.x, 1), most);
+    if (a.groups == 0 && x.x == 1) continue;      // it stands in the output
     const int n = x.x + y.x;
     auto at = [&](int i) -> int64_t {
       const int j = i < y.x ? i : i - y.x;
@@ -91,55 +89,35 @@ __global__ __launch_bounds__(256) void shared_join_kernel(ViewArgs a, qlinear_kv
     constexpr int kTurn = 8;
     float top = -INFINITY, total = 0.0f;
     own_t o = 0.0f;
-    const int each = (n + WAVES - 1) / WAVES, stop = min(n, (wave % WAVES + 1) * each);
     auto turn = [&](auto count, int i0) {
       constexpr int N = decltype(count)::value;
       float2 ml[N];
       own_t v[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int64_t r = at(min(i0 + i, stop - 1));
+        const int64_t r = at(min(i0 + i, n - 1));
         ml[i] = part.ml[r];
         v[i] = os[r * 64];
       }
       float most = top;
 #pragma unroll
-      for (int i = 0; i < N; ++i) most = fmaxf(most, i0 + i < stop ? ml[i].x : -INFINITY);
+      for (int i = 0; i < N; ++i) most = fmaxf(most, i0 + i < n ? ml[i].x : -INFINITY);
       const float keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - most);
       total *= keep;
       o *= keep;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (i0 + i >= stop || ml[i].x == -INFINITY) continue;
+        if (i0 + i >= n || ml[i].x == -INFINITY) continue;
         const float f = __builtin_amdgcn_exp2f(ml[i].x - most);
         total += f * ml[i].y;
         o += f * v[i];
       }
       top = most;
     };
-    if (WAVES == 1 && n <= 2) {
+    if (n <= 2) {
       turn(std::integral_constant<int, 2>{}, 0);
     } else {
-      for (int i0 = wave % WAVES * each; i0 < stop; i0 += kTurn) turn(std::integral_constant<int, kTurn>{}, i0);
-    }
-    if constexpr (WAVES > 1) {     // the whole workgroup is on one row
-      o_all[wave][lane] = o;
-      if (lane == 0) ml_all[wave] = make_float2(top, total);
-      __syncthreads();
-      if (wave == 0) {
-        top = fmaxf(fmaxf(ml_all[0].x, ml_all[1].x), fmaxf(ml_all[2].x, ml_all[3].x));
-        total = 0.0f;
-        o = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (ml_all[i].x == -INFINITY) continue;
-          const float f = __builtin_amdgcn_exp2f(ml_all[i].x - top);
-          total += f * ml_all[i].y;
-          o += f * o_all[i][lane];
-        }
-      }
-      if (rows > 1) __syncthreads();
-      if (wave != 0) continue;
+      for (int i0 = 0; i0 < n; i0 += kTurn) turn(std::integral_constant<int, kTurn>{}, i0);
     }
     half_t z;
 #pragma unroll
@@ -151,8 +129,8 @@ __global__ __launch_bounds__(256) void shared_join_kernel(ViewArgs a, qlinear_kv
 // The plan of a call with shared prefixes: one for the prefixes and the
 // sequences together. `rows`: partial results in all.
 struct SharedRoute {
-  bool chunk;
-  SharedPlan plan;
+  bool long_rows;
+  Plan few, chunk;
   ViewPartials part;
   int64_t rows;
 };
@@ -170,14 +148,15 @@ SharedRoute make_shared_route(const qlinear_kv_cache& c, const ViewArgs& a) {
   const int64_t group = a.q_heads / c.kv_heads, prefix = a.tokens * group, own = a.max_q_len * group;
   const int64_t most = prefix > own ? prefix : own;
   SharedRoute r = {};
-  r.part.rows = (int64_t)a.tokens * a.q_heads;
+  r.part.rows = r.part.own0 = (int64_t)a.tokens * a.q_heads;
   r.rows = 2 * r.part.rows;
-  r.chunk = most > kFewRows;
+  r.long_rows = most > kFewRows;
   const int64_t cap = most < kFewRows ? most : kFewRows;
-  Plan& f = r.plan.few;
-  // Tiles for the sequences that the few-row kernel is known to serve; one group
-  // of more rows than that leaves the others.
-  const int64_t likely = a.groups == 1 && prefix > kFewRows && own <= kFewRows ? own : cap;
+  Plan& f = r.few;
+  // Tiles for the prefixes, which are the longer ones, if the few-row kernel
+  // likely has them.
+  const int64_t group_rows = prefix / a.groups, own_rows = prefix / (a.batch - a.groups);
+  const int64_t likely = likely_rows(cap, group_rows > kFewRows ? own_rows : group_rows);
   f.rows = likely <= 16 || c.head_dim == 256 ? 16 : 32;
   f.once = likely <= f.rows;
   f.min_rows = 1;
@@ -190,14 +169,14 @@ SharedRoute make_shared_route(const qlinear_kv_cache& c, const ViewArgs& a) {
     f.workers = few_workers(c, f.rows, tiles, steps);
     if (tiles <= 2 * f.slots) f.whole = f.tiles;
   }
-  Plan& p = r.plan.chunk;
+  Plan& p = r.chunk;
   p.rows = kChunkRows;
   p.min_rows = kFewRows + 1;
   p.max_rows = INT32_MAX;
   p.splits = 1;
   p.chunk = INT32_MAX;
   r.part.chunk0 = r.rows;
-  if (r.chunk) {
+  if (r.long_rows) {
     // Tiles are cut, on the device, where there are fewer than the chip holds.
     p.tiles = (int)shared_tiles(a, group, own > kFewRows);
     const int slots = chunk_slots(c);
@@ -213,6 +192,22 @@ SharedRoute make_shared_route(const qlinear_kv_cache& c, const ViewArgs& a) {
 
 }  // namespace
 
+// As many rows to a wave as leave the chip eight waves a CU and more.
+hipError_t attn::launch_view_join(const qlinear_kv_cache& c, const ViewArgs& a, const ViewPartials& part, int64_t total,
+                                  int most, hipStream_t stream) {
+  int rows = 1;
+  static_assert(kJoinRows <= 64, "a lane for each");
+  while (rows < kJoinRows && part.rows / (2 * rows) >= 4096) rows *= 2;
+  const int64_t waves = (part.rows + rows - 1) / rows;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a, c, part, rows,
+                       most > 1 ? most : 1, (unsigned)(total - 1));
+    return hipGetLastError();
+  };
+  return c.head_dim == 64 ? go(view_join_kernel<64>) : c.head_dim == 128 ? go(view_join_kernel<128>)
+                                                                         : go(view_join_kernel<256>);
+}
+
 size_t sinks_attention_workspace_need(const qlinear_kv_cache& cache, const ViewArgs& a) {
   return workspace_need(cache, a);
 }
@@ -225,7 +220,7 @@ hipError_t launch_sinks_attention(const qlinear_kv_cache& cache, const ViewArgs&
 
 size_t shared_attention_workspace_need(const qlinear_kv_cache& cache, const ViewArgs& a) {
   const SharedRoute r = make_shared_route(cache, a);
-  return partial_bytes(1, r.rows, cache.head_dim) + 2 * r.part.rows * sizeof(int4);
+  return partial_bytes(1, r.rows, cache.head_dim) + found_bytes(a);
 }
 
 // Enough for all smaller calls too: each part of the workspace at its most.
@@ -244,7 +239,7 @@ size_t shared_attention_workspace_bytes(const qlinear_kv_cache& c, const ViewArg
     }
   // (Fewer tiles may be cut where these are not.)
   if (most > kFewRows) chunk = (int64_t)chunk_slots(c) * c.kv_heads * kChunkRows;
-  return partial_bytes(1, 2 * rows + chunk + few, c.head_dim) + 2 * rows * sizeof(int4);
+  return partial_bytes(1, 2 * rows + chunk + few, c.head_dim) + found_bytes(a);
 }
 
 hipError_t launch_shared_attention(const qlinear_kv_cache& cache, const ViewArgs& a, void* ws, hipStream_t stream) {
@@ -253,29 +248,14 @@ hipError_t launch_shared_attention(const qlinear_kv_cache& cache, const ViewArgs
   r.part.o = (float*)ws;
   r.part.found = (int4*)(r.part.o + r.rows * D);
   r.part.ml = (float2*)(r.part.found + 2 * r.part.rows);
-  if (r.chunk) {
-    const hipError_t e = chunk_launcher(D)(cache, a, r.plan.chunk, r.part, stream);
+  if (r.long_rows) {
+    const hipError_t e = chunk_launcher(D)(cache, a, r.chunk, r.part, stream);
     if (e != hipSuccess) return e;
   }
-  const hipError_t e = few_launcher(D)(cache, a, r.plan.few, r.part, stream);
+  const hipError_t e = few_launcher(D)(cache, a, r.few, r.part, stream);
   if (e != hipSuccess) return e;
-  // Four waves to a row if there may be many results; else as many rows to a wave
-  // as leave the chip eight waves a CU and more.
-  const int64_t parts = r.plan.chunk.slots + r.plan.few.workers / a.batch;
-  const bool many = parts > 16 && r.part.rows <= 1 << 11;
-  int rows = 1;
-  static_assert(kJoinRows <= 64, "a lane for each");
-  while (!many && rows < kJoinRows && r.part.rows / (2 * rows) >= 4096) rows *= 2;
-  const int most = r.plan.chunk.slots > r.plan.few.workers ? r.plan.chunk.slots : r.plan.few.workers;
-  const int64_t waves = (r.part.rows + rows - 1) / rows * (many ? 4 : 1);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a, cache, r.part, rows,
-                       most > 1 ? most : 1, (unsigned)(r.rows - 1));
-    return hipGetLastError();
-  };
-  if (D == 64) return many ? go(shared_join_kernel<64, 4>) : go(shared_join_kernel<64, 1>);
-  if (D == 128) return many ? go(shared_join_kernel<128, 4>) : go(shared_join_kernel<128, 1>);
-  return many ? go(shared_join_kernel<256, 4>) : go(shared_join_kernel<256, 1>);
+  const int most = r.chunk.slots > r.few.workers ? r.chunk.slots : r.few.workers;
+  return launch_view_join(cache, a, r.part, r.rows, most, stream);
 }
 
 }  // namespace qlinear
