@@ -3,9 +3,10 @@ sequences that come, share a prompt, branch and go: the library's calls in the
 order in which a server makes them. Weights are random.
 
     python examples/decoder.py [--layers 4] [--hidden 4096] [--heads 32] [--kv-heads 8] [--bits 16]
+                               [--window 0] [--sinks 0] [--head-norms 0] [--share 1]
 
 prints the times of a prompt, of single-token steps over four branches of it,
-and the pages that the branches share.
+the pages that the branches share, and how likely the prompt and the branches are.
 """
 
 from __future__ import annotations
@@ -47,14 +48,22 @@ class Linear:
 class Decoder:
     """layers of: norm, q/k/v, rotary step into the cache, attention, output
     projection, norm, gated MLP. A step takes any mix of sequences, each with
-    its new tokens: whole prompts, parts of them, drafts, single tokens."""
+    its new tokens: whole prompts, parts of them, drafts, single tokens.
+
+    sinks: first tokens that a window leaves in sight; head_norms: the heads of q
+    and k are normed before the rotation; share: neighbours in a batch that are
+    branches of one sequence read the pages they share once for all of them."""
+
+    sinks, share = 0, False
 
     def __init__(self, layers: int = 4, hidden: int = 4096, heads: int = 32, kv_heads: int = 8, mlp: int = 11008,
                  vocab: int = 32000, pages: int = 256, page_size: int = 64, max_pos: int = 8192, bits: int = 16,
-                 window: int = 0, seed: int = 0, device="cuda"):
+                 window: int = 0, seed: int = 0, device="cuda", sinks: int = 0, head_norms: bool = False,
+                 share: bool = False):
         gen = torch.Generator(device=device).manual_seed(seed)
         D = hidden // heads
         self.heads, self.kv_heads, self.dim, self.window, self.device = heads, kv_heads, D, window, torch.device(device)
+        self.sinks, self.share = sinks, share
         self.embedding = torch.randn((vocab, hidden), generator=gen, device=device).half()
         self.table = dq.rope_table(max_pos, D, device=device)
         self.layers = []
@@ -64,6 +73,9 @@ class Decoder:
                 norms=norms, qkv=Linear(hidden, (heads + 2 * kv_heads) * D, gen), out=Linear(hidden, hidden, gen),
                 gate=Linear(hidden, mlp, gen), up=Linear(hidden, mlp, gen), down=Linear(mlp, hidden, gen),
                 cache=dq.KVCache.empty(pages, kv_heads, D, page_size, bits, device=device)))
+        for layer in self.layers:
+            layer["head_norms"] = [(1 + 0.1 * torch.randn(D, generator=gen, device=device)).half() if head_norms else None
+                                   for _ in range(2)]
         self.norm = torch.ones(hidden, dtype=torch.float16, device=device)
         self.head = Linear(hidden, vocab, gen)
         self.pool = dq.PagePool(pages, page_size)
@@ -93,6 +105,7 @@ class Decoder:
         Raises MemoryError, changing nothing, if the pool has too few free pages."""
         ints = lambda x: torch.tensor(x, dtype=torch.int32, device=self.device)    # noqa: E731
         tokens, positions, slots, starts, lens = [], [], [], [0], []
+        groups, shared = self._branches([seq for seq, _ in batch])
         for seq, new in batch:
             at = self.pool.length(seq)
             try:
@@ -110,20 +123,48 @@ class Decoder:
         where = dict(block_table=ints([p + [0] * (width - len(p)) for p in pages]), kv_len=ints(lens),
                      q_start=ints(starts), max_q_len=max(len(new) for _, new in batch), max_kv_len=max(lens),
                      window=self.window)
+        if self.sinks:
+            where["sinks"] = self.sinks
+        if any(shared):
+            del where["window"]                   # there is none
+            where.update(shared_start=ints(groups), shared_len=ints(shared), max_shared_len=max(shared))
         return self.forward(ints(tokens), ints(positions), ints(slots), where)
+
+    def _branches(self, seqs) -> tuple[list[int], list[int]]:
+        """Neighbours that share pages: where each group starts, and what it shares (a window sees too
+        little of it)."""
+        groups, shared = [0], []
+        while self.share and self.window == 0 and groups[-1] < len(seqs):
+            at, n, tokens = groups[-1], 1, 0
+            while at + n < len(seqs):
+                more = self.pool.shared_tokens(seqs[at:at + n + 1])
+                if more < max(self.pool.page_size, tokens // 2):
+                    break
+                n, tokens = n + 1, more
+            groups.append(at + n)
+            shared.append(tokens)
+        return groups, shared
 
     def forward(self, tokens, positions, slots, where) -> torch.Tensor:
         T, H, Hk, D = tokens.shape[0], self.heads, self.kv_heads, self.dim
-        workspace = dq.paged_attention_workspace(self.layers[0]["cache"], T, H, where["kv_len"].shape[0],
-                                                 where["max_q_len"], where["max_kv_len"], self.device, self.window)
+        sizes = self.layers[0]["cache"], T, H, where["kv_len"].shape[0], where["max_q_len"], where["max_kv_len"]
+        if "shared_len" in where:
+            attention = dq.paged_attention_shared
+            workspace = dq.paged_attention_shared_workspace(*sizes, where["shared_len"].shape[0],
+                                                            where["max_shared_len"], self.device)
+        else:
+            attention = dq.paged_attention
+            workspace = dq.paged_attention_workspace(*sizes, self.device, self.window, where.get("sinks", 0))
         x = self.embedding[tokens]
         delta = None                              # the previous block's output, added by the next norm
         for layer in self.layers:
             y = dq.rms_norm(x, layer["norms"][0], residual=delta, residual_out=None if delta is None else x)
             qkv = layer["qkv"](y).view(T, H + 2 * Hk, D)
             q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
-            dq.rope_append(layer["cache"], q, k, v, positions, slots, self.table, q_out=q)
-            y = dq.paged_attention(layer["cache"], q, workspace=workspace, **where)
+            q_norm, k_norm = layer["head_norms"]
+            dq.rope_append(layer["cache"], q, k, v, positions, slots, self.table, q_out=q, q_norm=q_norm,
+                           k_norm=k_norm)
+            y = attention(layer["cache"], q, workspace=workspace, **where)
             y = dq.rms_norm(layer["out"](y.view(T, H * D)), layer["norms"][1], residual=x, residual_out=x)
             delta = layer["down"](layer["gate"](y, activation=dq.ACT_SILU).mul_(layer["up"](y)))
         return self.head(dq.rms_norm(x, self.norm, residual=delta))
@@ -132,10 +173,12 @@ class Decoder:
 def main() -> None:
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     for name, value in (("layers", 4), ("hidden", 4096), ("heads", 32), ("kv-heads", 8), ("mlp", 11008),
-                        ("bits", 16), ("prompt", 1000), ("steps", 32), ("window", 0)):
+                        ("bits", 16), ("prompt", 1000), ("steps", 32), ("window", 0), ("sinks", 0), ("head-norms", 0),
+                        ("share", 1)):
         p.add_argument("--" + name, type=int, default=value)
     a = p.parse_args()
     d = Decoder(a.layers, a.hidden, a.heads, a.kv_heads, a.mlp, bits=a.bits, window=a.window,
+                sinks=a.sinks, head_norms=bool(a.head_norms), share=bool(a.share),
                 max_pos=a.prompt + a.steps + 1, pages=5 + 5 * (a.prompt + a.steps) // 64)
     prompt = torch.randint(0, 32000, (a.prompt,), generator=torch.Generator().manual_seed(1)).tolist()
 
@@ -152,8 +195,11 @@ def main() -> None:
     d.add("a")
     logits, ms = timed(lambda: d.step([("a", prompt)]))
     print(f"prompt of {a.prompt} tokens, {a.layers} layers: {ms:.2f} ms")
+    said = dq.token_logprobs(logits[:-1], torch.tensor(prompt[1:], dtype=torch.int32, device=d.device))
+    print(f"its tokens' mean log probability: {said.logprob.mean().item():.3f}, entropy {said.entropy.mean().item():.3f}")
     names = ["a", "b", "c", "d"]
-    nxt = logits[-1].topk(4).indices.tolist()     # four branches, each with its own next token
+    first = dq.token_logprobs(logits[-1:], top=4, entropy=False)     # four branches, each with its own next token
+    nxt, likely = first.top_id[0].tolist(), first.top_logprob[0].clone()
     for name in names[1:]:
         d.fork("a", name)
     held = d.pool.num_pages - d.pool.free_pages
@@ -162,11 +208,14 @@ def main() -> None:
     def decode():
         tokens = nxt
         for _ in range(a.steps):
-            tokens = d.step([(n, [t]) for n, t in zip(names, tokens)]).argmax(-1).tolist()
+            best = dq.token_logprobs(d.step([(n, [t]) for n, t in zip(names, tokens)]), top=1, entropy=False)
+            likely.add_(best.top_logprob[:, 0])
+            tokens = best.top_id[:, 0].tolist()
         return tokens
 
     _, ms = timed(decode)
     print(f"{a.steps} steps of four branches: {ms / a.steps:.3f} ms each")
+    print("the branches' log probabilities: " + ", ".join(f"{x:.2f}" for x in likely.tolist()))
     for name in names[:3]:
         d.free(name)
     d.compact()
