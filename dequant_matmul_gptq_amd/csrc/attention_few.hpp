@@ -315,14 +315,15 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
   } else {
     const Spans sp = few_spans(a, c, plan, group);
     if (sp.whole) {
-      const int b = worker / plan.whole;
-      if (b >= a.batch) return;
+      // Views: first tiles of all sequences first, for many have no more.
+      const int b = kView ? worker % a.batch : worker / plan.whole;
+      if (kView ? worker >= plan.whole * a.batch : b >= a.batch) return;
       if (b < 64)
         sp.costs.get(b, w);
       else
         sequence(a, c, b, w);
       it = few_item(a, plan, group, w);
-      tile = worker - b * plan.whole;
+      tile = kView ? worker / a.batch : worker - b * plan.whole;
       if (tile >= it.tiles) return;
       at = 0;
       stop = it.steps;

@@ -153,11 +153,14 @@ SharedRoute make_shared_route(const qlinear_kv_cache& c, const ViewArgs& a) {
   r.long_rows = most > kFewRows;
   const int64_t cap = most < kFewRows ? most : kFewRows;
   Plan& f = r.few;
-  // Tiles for the prefixes, which are the longer ones, if the few-row kernel
-  // likely has them.
+  // Tiles for the prefixes, which are the longer ones, if the few-row kernel likely
+  // has them. Else two of 16 rows do better than one of 32 on own tokens, of which
+  // there are few (20 sequences of 77 own tokens, 4 of them new, 64/8 heads, us:
+  // float16 10 and 11.4, Q8 10.4 and 14.9; 30 of 4 to 900, Q8: 17.0 and 19.4).
   const int64_t group_rows = prefix / a.groups, own_rows = prefix / (a.batch - a.groups);
-  const int64_t likely = likely_rows(cap, group_rows > kFewRows ? own_rows : group_rows);
-  f.rows = likely <= 16 || c.head_dim == 256 ? 16 : 32;
+  const bool prefixes = group_rows <= kFewRows;
+  const int64_t likely = likely_rows(cap, prefixes ? group_rows : own_rows);
+  f.rows = !prefixes || likely <= 16 || c.head_dim == 256 ? 16 : 32;
   f.once = likely <= f.rows;
   f.min_rows = 1;
   f.max_rows = kFewRows;
