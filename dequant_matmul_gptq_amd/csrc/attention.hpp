@@ -401,7 +401,9 @@ __device__ __forceinline__ Ranges chunk_ranges(const ViewArgs& a, const qlinear_
   tiles = wave_total(tiles);
   if (tiles >= plan.slots) return {INT32_MAX};
   total = wave_total(total);
-  Ranges ranges = {max(8, (int)((total + plan.slots - 1) / plan.slots))};
+  // Four steps at least (32 sequences behind 512 and 4096 tokens, 64/8 heads, us:
+  // two 25.2 and 37.4, four 28.2 and 33.0, eight 33.0 and 37.0).
+  Ranges ranges = {max(4, (int)((total + plan.slots - 1) / plan.slots))};
   int items = t0.n * ranges.of(t0.steps);
   for (int b0 = 64; b0 < a.batch; b0 += 64) {
     const Tiles t = chunk_tiles_of(a, c, plan, group, shift, b0);

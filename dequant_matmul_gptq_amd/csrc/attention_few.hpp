@@ -345,15 +345,15 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
   const bool alone = taken == it.steps;
   row_tile(a, group, tile * 16 * NT, 16 * NT, w);
   int begin, end;
-  if constexpr (kView) {     // numbers as in Item
-    begin = i0 < it.sinks ? i0 : max(i0, w.lo_min / kStep - it.gap);
+  auto token = [&](int step) { return (kView ? it.real(step) : step) * kStep; };     // a step's first
+  if constexpr (kView) {     // numbers as in Item; sinks may go on behind the first step
+    begin = token(i0) < a.sinks ? i0 : max(i0, w.lo_min / kStep - it.gap);
     end = min(i0 + taken, (w.p_max < 0 ? 0 : w.p_max / kStep + 1) - it.gap);
   } else {
     begin = max(it.first_step + i0, w.lo_min / kStep);
     end = min(it.first_step + i0 + taken, w.p_max < 0 ? 0 : w.p_max / kStep + 1);
   }
   const int64_t part_row0 = (((int64_t)worker * c.kv_heads + head) * 2 + slot) * (16 * NT);
-  auto token = [&](int step) { return (kView ? it.real(step) : step) * kStep; };     // a step's first
 
   // Rows: column col of tile nt is row row0 + 16 nt + col of the sequence.
   int pos[NT], first[NT];

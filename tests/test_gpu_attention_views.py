@@ -86,6 +86,19 @@ def test_sinks_long_and_mixed(bits):
     _check_sinks(b, 900, 5)
 
 
+@pytest.mark.parametrize("bits,group", [(16, 128), (8, 64), (6, 32), (4, 128)])
+@pytest.mark.parametrize("D", (64, 128, 256))
+@pytest.mark.parametrize("n,window,sinks", [(7, 23, 1), (8, 5, 33), (6, 40, 100), (2, 1, 2)])
+def test_sinks_of_tiles_that_start_behind_them(D, bits, group, n, window, sinks):
+    """Rows of a sequence in several tiles, whose windows start in other steps than its first row's, with sinks
+    before, in and behind that step."""
+    say(f"sinks tiles D={D} bits={bits} n={n} window={window} sinks={sinks}")
+    lens = [n, 33, 35, 60, 64, 66, 79, 91, 97, 130, 342]
+    for Hq, Hk in ((16, 2), (8, 4)):
+        b = Batch(Hq, Hk, D, 128, bits, min(group, D), [n] * len(lens), lens, seed=D + bits + n)
+        _check_sinks(b, window, sinks)
+
+
 def test_sinks_without_a_window_and_bounds():
     say("sinks bounds")
     b = Batch(8, 2, 64, 16, 16, 64, [1, 30], [700, 90], seed=5)
