@@ -390,7 +390,6 @@ __device__ __forceinline__ Tiles chunk_tiles_of(const ViewArgs& a, const qlinear
 // t0: of the first 64 sequences, here and below.
 __device__ __forceinline__ Ranges chunk_ranges(const ViewArgs& a, const qlinear_kv_cache& c, const Plan& plan,
                                                int group, int shift, const Tiles& t0) {
-  if (plan.slots == 0) return {INT32_MAX};      // more tiles than the chip holds, as it is
   int tiles = t0.n;
   unsigned total = t0.n * t0.steps;
   for (int b0 = 64; b0 < a.batch; b0 += 64) {

@@ -180,13 +180,12 @@ SharedRoute make_shared_route(const qlinear_kv_cache& c, const ViewArgs& a) {
   p.chunk = INT32_MAX;
   r.part.chunk0 = r.rows;
   if (r.long_rows) {
-    // Tiles are cut, on the device, where there are fewer than the chip holds.
-    p.tiles = (int)shared_tiles(a, group, own > kFewRows);
-    const int slots = chunk_slots(c);
-    if (p.tiles < slots) {
-      p.slots = p.tiles = slots;
-      r.rows += (int64_t)p.tiles * c.kv_heads * kChunkRows;
-    }
+    // Tiles are cut, on the device, where there are fewer than the chip holds: the
+    // parts are no more than that.
+    const int tiles = (int)shared_tiles(a, group, own > kFewRows);
+    p.slots = chunk_slots(c);
+    p.tiles = tiles > p.slots ? tiles : p.slots;
+    r.rows += (int64_t)p.slots * c.kv_heads * kChunkRows;
   }
   r.part.few0 = r.rows;
   if (f.workers > 0) r.rows += few_partial_rows(c, f.rows, f.workers);
@@ -240,7 +239,6 @@ size_t shared_attention_workspace_bytes(const qlinear_kv_cache& c, const ViewArg
       const int64_t n = few_partial_rows(c, tile, few_workers(c, tile, (cap + tile - 1) / tile * a.batch, steps));
       if (n > few) few = n;
     }
-  // (Fewer tiles may be cut where these are not.)
   if (most > kFewRows) chunk = (int64_t)chunk_slots(c) * c.kv_heads * kChunkRows;
   return partial_bytes(1, 2 * rows + chunk + few, c.head_dim) + found_bytes(a);
 }

@@ -293,6 +293,16 @@ def test_shared_many_sequences():
     b.compare(b.call())
 
 
+@pytest.mark.parametrize("bits", (16, 6))
+def test_shared_prompt_among_many(bits):
+    """A prompt among so many single tokens that the bound on row tiles is past what the chip holds, and the tiles
+    themselves are not."""
+    say(f"shared prompt among many bits={bits}")
+    n = [1] * 30 + [40] + [1] * 59
+    b = Shared(32, 8, 64, 64, bits, 32, [70, 20], [900, 400], n, [x + 9 * i % 80 for i, x in enumerate(n)], seed=bits)
+    b.compare(b.call())
+
+
 def test_shared_rows_that_see_nothing_of_their_own():
     """More new tokens than own ones: nothing is shared there, and the first rows have no position."""
     say("shared empty")
