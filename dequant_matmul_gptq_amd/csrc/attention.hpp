@@ -355,7 +355,7 @@ __device__ __forceinline__ bool find_tile(const Args& a, const qlinear_kv_cache&
 // and one round of workgroups takes them all (three groups of 8192, 4096 and 640
 // tokens over Q8, 640, 288 and 32 rows a key/value head: 95 us with as many
 // ranges for all tiles as the longest may have, 116 us with 66 items of 13 steps
-// for 64 places, 81 us so).
+// for 64 places, 81 us so; 50 us since that kernel spills nothing).
 struct Ranges {
   int chunk;
   __device__ __forceinline__ int of(int steps) const { return steps <= chunk ? 1 : (steps + chunk - 1) / chunk; }

@@ -151,7 +151,16 @@ __global__ __launch_bounds__(kChunkThreads, D == 256 ? 1 : 2) void attention_chu
   const int sinks = sink_steps(a, step_lo, T == 64 ? 6 : 5), gap = kView ? step_lo - sinks : 0;
   const int begin = (kView ? 0 : step_lo) + split * chunk;
   const int end = split == splits - 1 ? step_end - gap : min(begin + chunk, step_end - gap);
-  auto token = [&](int step) { return (kView && step >= sinks ? step + gap : step) * T; };     // a step's first
+  // A step's first token. (The statement without instructions keeps the compiler from
+  // making loops of their own for the steps on either side of the gap, whose
+  // addresses it then spills: 43 to 55 registers of 128 wide heads with codes, loaded
+  // in every step. 32 rows of 8 heads over 65536 shared tokens: Q8 161 us with them,
+  // 97 so, float16, which had 39 registers more but none spilled, 97 and 91.5.)
+  auto token = [&](int step) {
+    int real = kView && step >= sinks ? step + gap : step;
+    if constexpr (kView) asm("" : "+s"(real));
+    return real * T;
+  };
   // Where partial results go, if the launch leaves any: by row of the output, or of
   // the tile.
   const bool partial = splits > 1 || shared, by_tile = shared && splits > 1;
