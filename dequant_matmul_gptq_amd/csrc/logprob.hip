@@ -422,8 +422,22 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, P
   if (t == 0) sh.count = 0;
   float4 v = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
   if (t < parts.per_row) v = parts.sums[p0 + t];
+  // The thread's keys, in the order of their places: loads of a turn do not wait for
+  // one another (one row of 131072 with 20 alternatives: 7.7 us with one after another, 6.4 so).
+  constexpr int kTurn = 8;
+  auto own = [&](auto f) {
+#pragma unroll 1
+    for (int i0 = t; i0 < n; i0 += kTurn * kThreads) {
+      uint64_t key[kTurn];
+#pragma unroll
+      for (int j = 0; j < kTurn; ++j) key[j] = keys[min(i0 + j * kThreads, n - 1)];
+#pragma unroll
+      for (int j = 0; j < kTurn; ++j)
+        if (i0 + j * kThreads < n) f(key[j]);
+    }
+  };
   uint64_t most = 0;
-  for (int i = t; i < n; i += kThreads) most = keys[i] > most ? keys[i] : most;
+  own([&](uint64_t key) { most = key > most ? key : most; });
   // NaN, which is no column's maximum here either, is looked for where there is one.
   const bool none = most == 0, odd = (uint32_t)(most >> 32) == ~0u;
   const float mine = none || odd ? -INFINITY : unordered((uint32_t)(most >> 32));
@@ -467,11 +481,10 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, P
       [&](auto pass, auto f) {
         constexpr int kPass = decltype(pass)::value;
         if (none || (kPass != kAll && (uint32_t)(most >> 32) < from)) return;
-        for (int i = t; i < n; i += kThreads) {
-          const uint64_t key = keys[i];
+        own([&](uint64_t key) {
           const uint32_t v = (uint32_t)(key >> 32);
           if (key != 0 && (kPass == kAll || (kPass == kAbove ? v > from : v >= from))) f(key);
-        }
+        });
       },
       (n + kThreads - 1) / kThreads,
       [&](int turn, auto f) {

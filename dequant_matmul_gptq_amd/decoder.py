@@ -423,7 +423,8 @@ def paged_attention_shared(cache: KVCache, q: torch.Tensor, block_table: torch.T
     (int32 [groups]; PagePool.shared_tokens counts them) are the same slots of
     the cache: at most each one's tokens before its new ones. Sequences of no
     group share nothing. max_shared_len bounds shared_len for the launch plan
-    (None: width * page_size). The rest is as for paged_attention.
+    (None: width * page_size). The rest is as for paged_attention, which does as
+    well for two branches, short prefixes, and prompts of many new tokens.
     """
     dev, D = cache.device, cache.head_dim
     if _current_gpu() != dev:
