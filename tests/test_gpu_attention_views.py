@@ -375,6 +375,65 @@ def test_shared_rows_of_no_sequence_strides_and_guards():
         b.compare(o[2:T - 3])
 
 
+def test_sinks_rows_of_no_sequence_strides_and_guards():
+    """Spans that are joined, prompts beside them, rows before the first sequence and behind the last."""
+    say("sinks guards")
+    for bits, lens, n in ((16, [3000, 700, 2000], [1, 4, 1]), (8, [5000, 300, 90], [2, 1, 40])):
+        b = Batch(8, 2, 128, 64, bits, 128, n, lens, seed=bits)
+        dev = device()
+        T = sum(n) + 5
+        fused = torch.full((T, 8 + 4, 128), float("nan"), dtype=torch.float16, device=dev)
+        fused[2:T - 3, :8] = torch.from_numpy(np.concatenate(b.q)).to(dev)
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)      # noqa: E731
+        need = dq.paged_attention_workspace_bytes(b.cache, T, 8, 3, max(n), max(lens), 1500, 40)
+        assert need > 0
+        ws, og = Guarded(need, dev), Guarded(T * 8 * 128 * 2, dev)
+        out = og.view(torch.float16, (T, 8, 128))
+        out.fill_(7)
+        dq.paged_attention(b.cache, fused[:, :8], ints(b.table), ints(lens), ints(np.cumsum([2] + n)), max(n), max(lens),
+                           window=1500, out=out, workspace=ws.bytes(), sinks=40)
+        assert ws.intact() and og.intact()
+        o = out.float().cpu().numpy().astype(np.float64)
+        assert (o[:2] == 7).all() and (o[T - 3:] == 7).all()
+        at = 2
+        for i, m in enumerate(n):
+            ref, w, total = oracle.decoder.attention(b.q[i], b.kv[0][i], b.kv[1][i], 128 ** -0.5, 1500, 40)
+            _close(b, i, o[at:at + m], ref, w, total, f"bits={bits}")
+            at += m
+
+
+def test_shared_one_workspace_for_two_graphs():
+    """Calls of two sizes, captured with one workspace, replayed in turn."""
+    say("shared two graphs")
+    dev = device()
+    one = Shared(8, 2, 128, 32, 16, 64, [5, 2], [900, 64], [1] * 7, [1 + 50 * i for i in range(7)], seed=13)
+    two = Shared(8, 2, 128, 32, 16, 64, [30], [1500], [2] * 30, [2 + 9 * i for i in range(30)], seed=14)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)      # noqa: E731
+    ws = dq.paged_attention_shared_workspace(two.cache, 60, 8, 30, 2, 2000, 2, 1500, dev)
+    calls = []
+    for b, n in ((one, 1), (two, 2)):
+        q = torch.from_numpy(np.concatenate(b.q)).to(dev)
+        where = [ints(b.table), ints(b.kv_lens), ints(b.shared), ints(b.starts),
+                 ints(np.concatenate([[0], np.cumsum(b.q_lens)]))]
+        out = torch.zeros(q.shape, dtype=torch.float16, device=dev)
+
+        def call(b=b, q=q, where=where, out=out, n=n):
+            dq.paged_attention_shared(b.cache, q, *where, max_q_len=n, max_kv_len=2000, max_shared_len=max(b.shared),
+                                      out=out, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        calls.append((g, b, out))
+    for _ in range(3):
+        for g, b, out in calls:
+            out.fill_(9.0)
+            g.replay()
+            torch.cuda.synchronize()
+            b.compare(out.float().cpu().numpy().astype(np.float64))
+
+
 def test_shared_graph_streams_and_repeats():
     say("shared graph")
     b = Shared(8, 2, 128, 32, 16, 64, [5, 2], [900, 64], [1] * 7, [1 + 50 * i for i in range(7)], seed=12)
