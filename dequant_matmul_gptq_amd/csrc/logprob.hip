@@ -32,7 +32,12 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kCandidates = 512;
-constexpr int kMaxParts = kThreads;
+constexpr int kMaxParts = kThreads;      // of a row that is cut for the sake of more workgroups
+constexpr int kMaxGroups = 16;           // of elements that a thread holds: 1, 2, 4, 8 or 16
+// Turns of the join's threads over a row's parts. A float32 row of the longest that
+// starts inside a group has one part more than there are threads.
+constexpr int kJoinTurns = 2;
+static_assert((QLINEAR_MAX_VOCAB + 3 - 1) / (kThreads * kMaxGroups * 4) + 1 <= kJoinTurns * kThreads);
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
@@ -420,8 +425,15 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, P
   const uint64_t* keys = parts.keys + p0 * a.top;
   const int n = parts.per_row * a.top;
   if (t == 0) sh.count = 0;
-  float4 v = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-  if (t < parts.per_row) v = parts.sums[p0 + t];
+  float4 v[kJoinTurns];
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kJoinTurns; ++j) {
+    const int i = t + j * kThreads;
+    v[j] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    if (i < parts.per_row) v[j] = parts.sums[p0 + i];
+    m = fmaxf(m, v[j].x);
+  }
   // The thread's keys, in the order of their places: loads of a turn do not wait for
   // one another (one row of 131072 with 20 alternatives: 7.7 us with one after another, 6.4 so).
   constexpr int kTurn = 8;
@@ -442,7 +454,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, P
   const bool none = most == 0, odd = (uint32_t)(most >> 32) == ~0u;
   const float mine = none || odd ? -INFINITY : unordered((uint32_t)(most >> 32));
 
-  float m = wave_max(v.x);
+  m = wave_max(m);
   if (lane == 0) sh.s[wave] = m;
   sh.lane_max[wave][lane] = mine;
   __syncthreads();
@@ -453,10 +465,12 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, P
   for (int j = 1; j < kWaves; ++j) column = fmaxf(column, sh.lane_max[j][lane]);
   __syncthreads();
   float l = 0.0f, s = 0.0f;
-  if (v.x != -INFINITY || v.y != 0.0f) {
-    const float d = exponent_of_part<T>(v.x, r.m), f = __builtin_amdgcn_exp2f(d);
-    l = f * v.y;
-    s = f > 0.0f ? f * fmaf(v.y, d, v.z) : 0.0f;      // d may be -infinity
+#pragma unroll
+  for (int j = 0; j < kJoinTurns; ++j) {
+    if (v[j].x == -INFINITY && v[j].y == 0.0f) continue;
+    const float d = exponent_of_part<T>(v[j].x, r.m), f = __builtin_amdgcn_exp2f(d);
+    l += f * v[j].y;
+    s += f > 0.0f ? f * fmaf(v[j].y, d, v[j].z) : 0.0f;      // d may be -infinity
   }
   l = wave_sum(l);
   s = wave_sum(s);
@@ -495,12 +509,12 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, P
 }
 
 struct Plan {
-  int groups;      // of a thread: 1, 2, 4, 8 or 16
+  int groups;      // of a thread
   int parts;
 };
 
 // As few parts as give every CU two workgroups.
-constexpr int kMaxGroups = 16, kWanted = 512;
+constexpr int kWanted = 512;
 Plan make_plan(int rows, int vocab, bool f32, bool whole) {
   const int size = f32 ? 4 : 8;
   // Rows that start inside a group (not `whole`) may have one more.
