@@ -2,6 +2,7 @@
 // (paged cache, rotary positions, attention, norm): host-side validation,
 // then launches on the caller's stream. Nothing here allocates memory or
 // synchronizes.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -158,7 +159,10 @@ int set_norms(const Norms& n, int32_t q_heads, int32_t kv_heads, int32_t head_di
   a.k_norm = n.k;
   a.q_norm_stride = n.q_heads == 1 ? 0 : head_dim;
   a.k_norm_stride = n.k_heads == 1 ? 0 : head_dim;
-  a.eps = n.eps;
+  // The kernel's reciprocal root takes a subnormal number for zero, and a head of
+  // zeros would be 0 times infinity. A head of anything else has a mean square of
+  // 2^-57 at least, beside which either eps is nothing.
+  a.eps = n.eps > 0.0f && n.eps < FLT_MIN ? FLT_MIN : n.eps;
   a.per_element = 1.0f / (float)head_dim;
   return QLINEAR_OK;
 }
