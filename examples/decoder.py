@@ -123,11 +123,11 @@ class Decoder:
         where = dict(block_table=ints([p + [0] * (width - len(p)) for p in pages]), kv_len=ints(lens),
                      q_start=ints(starts), max_q_len=max(len(new) for _, new in batch), max_kv_len=max(lens),
                      window=self.window)
-        if self.sinks:
-            where["sinks"] = self.sinks
         if any(shared):
-            del where["window"]                   # there is none
+            del where["window"]                   # there is none, and sinks are seen without one
             where.update(shared_start=ints(groups), shared_len=ints(shared), max_shared_len=max(shared))
+        elif self.sinks:
+            where["sinks"] = self.sinks
         return self.forward(ints(tokens), ints(positions), ints(slots), where)
 
     def _branches(self, seqs) -> tuple[list[int], list[int]]:
