@@ -3,7 +3,7 @@ sequences that come, share a prompt, branch and go: the library's calls in the
 order in which a server makes them. Weights are random.
 
     python examples/decoder.py [--layers 4] [--hidden 4096] [--heads 32] [--kv-heads 8] [--bits 16]
-                               [--window 0] [--sinks 0] [--head-norms 0] [--share 1]
+                               [--window 0] [--sinks 0] [--head-norms 0] [--share 2]
 
 prints the times of a prompt, of single-token steps over four branches of it,
 the pages that the branches share, and how likely the prompt and the branches are.
@@ -22,6 +22,15 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import torch  # noqa: E402
 
 import dequant_matmul_gptq_amd as dq  # noqa: E402
+
+
+# Decoder(share=): never, wherever sequences share a page, where they gain by it.
+SHARE_NEVER, SHARE_ALWAYS, SHARE_GAINS = 0, 1, 2
+# Branches gain from about so many on, behind so many tokens, with up to so many new
+# ones each (us, shared and each by itself, float16: 8 single tokens behind 4096 27 and
+# 29 with 64/8 heads, 20 and 28 with 32/8, 26 and 57 with 32/32; 16 with 4 new ones 43
+# and 51; but 16 with 16 new ones 77 and 78, 16 single ones behind 1024 27 and 20).
+GAINS_SEQUENCES, GAINS_TOKENS, GAINS_NEW = 8, 4096, 4
 
 
 class Linear:
@@ -51,15 +60,16 @@ class Decoder:
     its new tokens: whole prompts, parts of them, drafts, single tokens.
 
     sinks: first tokens that a window leaves in sight; head_norms: the heads of q
-    and k are normed before the rotation; share: neighbours in a batch that are
-    branches of one sequence read the pages they share once for all of them."""
+    and k are normed before the rotation; share: whether neighbours in a batch that
+    are branches of one sequence read the pages they share once for all of them
+    (SHARE_NEVER, SHARE_ALWAYS or True, SHARE_GAINS)."""
 
-    sinks, share = 0, False
+    sinks, share = 0, SHARE_NEVER
 
     def __init__(self, layers: int = 4, hidden: int = 4096, heads: int = 32, kv_heads: int = 8, mlp: int = 11008,
                  vocab: int = 32000, pages: int = 256, page_size: int = 64, max_pos: int = 8192, bits: int = 16,
                  window: int = 0, seed: int = 0, device="cuda", sinks: int = 0, head_norms: bool = False,
-                 share: bool = False):
+                 share: int = SHARE_NEVER):
         gen = torch.Generator(device=device).manual_seed(seed)
         D = hidden // heads
         self.heads, self.kv_heads, self.dim, self.window, self.device = heads, kv_heads, D, window, torch.device(device)
@@ -105,7 +115,7 @@ class Decoder:
         Raises MemoryError, changing nothing, if the pool has too few free pages."""
         ints = lambda x: torch.tensor(x, dtype=torch.int32, device=self.device)    # noqa: E731
         tokens, positions, slots, starts, lens = [], [], [], [0], []
-        groups, shared = self._branches([seq for seq, _ in batch])
+        groups, shared = self._branches(batch)
         for seq, new in batch:
             at = self.pool.length(seq)
             try:
@@ -130,9 +140,10 @@ class Decoder:
             where["sinks"] = self.sinks
         return self.forward(ints(tokens), ints(positions), ints(slots), where)
 
-    def _branches(self, seqs) -> tuple[list[int], list[int]]:
+    def _branches(self, batch) -> tuple[list[int], list[int]]:
         """Neighbours that share pages: where each group starts, and what it shares (a window sees too
         little of it)."""
+        seqs = [seq for seq, _ in batch]
         groups, shared = [0], []
         while self.share and self.window == 0 and groups[-1] < len(seqs):
             at, n, tokens = groups[-1], 1, 0
@@ -141,8 +152,10 @@ class Decoder:
                 if more < max(self.pool.page_size, tokens // 2):
                     break
                 n, tokens = n + 1, more
+            gains = (n >= GAINS_SEQUENCES and tokens >= GAINS_TOKENS
+                     and max(len(new) for _, new in batch[at:at + n]) <= GAINS_NEW)
             groups.append(at + n)
-            shared.append(tokens)
+            shared.append(tokens if gains or self.share != SHARE_GAINS else 0)
         return groups, shared
 
     def forward(self, tokens, positions, slots, where) -> torch.Tensor:
@@ -170,15 +183,19 @@ class Decoder:
         return self.head(dq.rms_norm(x, self.norm, residual=delta))
 
 
-def main() -> None:
+def arguments(args=None) -> argparse.Namespace:
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     for name, value in (("layers", 4), ("hidden", 4096), ("heads", 32), ("kv-heads", 8), ("mlp", 11008),
                         ("bits", 16), ("prompt", 1000), ("steps", 32), ("window", 0), ("sinks", 0), ("head-norms", 0),
-                        ("share", 1)):
+                        ("share", SHARE_GAINS)):
         p.add_argument("--" + name, type=int, default=value)
-    a = p.parse_args()
+    return p.parse_args(args)
+
+
+def main() -> None:
+    a = arguments()
     d = Decoder(a.layers, a.hidden, a.heads, a.kv_heads, a.mlp, bits=a.bits, window=a.window,
-                sinks=a.sinks, head_norms=bool(a.head_norms), share=bool(a.share),
+                sinks=a.sinks, head_norms=bool(a.head_norms), share=a.share,
                 max_pos=a.prompt + a.steps + 1, pages=5 + 5 * (a.prompt + a.steps) // 64)
     prompt = torch.randint(0, 32000, (a.prompt,), generator=torch.Generator().manual_seed(1)).tolist()
 

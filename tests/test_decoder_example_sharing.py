@@ -4,6 +4,7 @@ its layers (no GPU)."""
 import inspect
 
 import dequant_matmul_gptq_amd as dq
+from examples import decoder as example
 from examples.decoder import Decoder
 
 
@@ -45,3 +46,35 @@ def test_sinks_with_a_window_share_nothing():
     _branches(d, 9)
     where = d.step([("a", [1]), ("b", [2])])
     assert _call(where) is dq.paged_attention and (where["window"], where["sinks"]) == (5, 3)
+
+
+def test_shared_only_where_it_gains():
+    """share=SHARE_GAINS: eight branches or more of up to four new tokens each, behind 4096 shared tokens or more."""
+    def step(count, tokens, new, **kw):
+        d = _decoder(pages=6000, page_size=16, **kw)
+        _branches(d, tokens, [chr(97 + i) for i in range(count)])
+        where = d.step([(chr(97 + i), [1] * (new if i else 1)) for i in range(count)])
+        assert _call(where) is (dq.paged_attention_shared if "shared_len" in where else dq.paged_attention)
+        return where["shared_len"].tolist() if "shared_len" in where else None
+
+    gains = dict(share=example.SHARE_GAINS)
+    assert step(8, 4100, 1, **gains) == step(8, 4100, 4, **gains) == [4096]
+    assert step(20, 9000, 2, **gains) == [8992]
+    assert step(7, 4100, 1, **gains) is None            # too few
+    assert step(8, 4095, 1, **gains) is None            # behind too little
+    assert step(8, 4100, 5, **gains) is None            # prompts gain nothing
+    assert step(4, 1000, 1, **gains) is None
+    assert step(2, 20, 9, share=True) == [16] and step(8, 4100, 1) is None
+
+
+def test_each_group_by_itself():
+    d = _decoder(pages=3000, page_size=16, share=example.SHARE_GAINS)
+    _branches(d, 5000, "abcdefgh")
+    _branches(d, 300, "xyz")
+    where = d.step([(n, [1]) for n in "xyzabcdefgh"])
+    assert where["shared_start"].tolist() == [0, 3, 11] and where["shared_len"].tolist() == [0, 4992]
+
+
+def test_the_command_shares_where_it_gains():
+    assert example.arguments([]).share == example.SHARE_GAINS
+    assert example.arguments(["--share", "0"]).share == 0
