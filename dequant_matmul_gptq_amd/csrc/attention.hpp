@@ -37,7 +37,7 @@ namespace qlinear {
 struct ViewArgs : AttentionArgs {
   int sinks, groups;
   const int32_t *shared_start, *shared_len;      // shared_start NULL: one group of all
-  int max_shared_len;
+  int max_shared_len;                            // no plan asks for it: max_kv_len bounds the prefixes' steps too
 };
 
 // What a call takes of its workspace, and what is enough for it and for all

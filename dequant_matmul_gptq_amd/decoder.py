@@ -402,8 +402,8 @@ def paged_attention_shared_workspace_bytes(cache: KVCache, tokens: int, q_heads:
 def paged_attention_shared_workspace(cache: KVCache, tokens: int, q_heads: int, batch: int, max_q_len: int,
                                      max_kv_len: int, groups: int, max_shared_len: int, device) -> torch.Tensor:
     """A paged_attention_shared workspace for calls of up to these sizes with
-    the same q_heads (scratch: needs no initialization; calls that may overlap in
-    time must not share one)."""
+    the same q_heads, whatever max_shared_len (scratch: needs no initialization;
+    calls that may overlap in time must not share one)."""
     n = paged_attention_shared_workspace_bytes(cache, tokens, q_heads, batch, max_q_len, max_kv_len, groups,
                                                max_shared_len)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
@@ -422,9 +422,10 @@ def paged_attention_shared(cache: KVCache, q: torch.Tensor, block_table: torch.T
     [groups + 1]; None: one group of all), whose first shared_len[g] tokens
     (int32 [groups]; PagePool.shared_tokens counts them) are the same slots of
     the cache: at most each one's tokens before its new ones. Sequences of no
-    group share nothing. max_shared_len bounds shared_len for the launch plan
-    (None: width * page_size). The rest is as for paged_attention, which does as
-    well for two branches, short prefixes, and prompts of many new tokens.
+    group share nothing. max_shared_len bounds shared_len (None: width *
+    page_size); it has no effect so far, the launch plan goes by max_kv_len. The
+    rest is as for paged_attention, which does as well for two branches, short
+    prefixes, and prompts of many new tokens.
     """
     dev, D = cache.device, cache.head_dim
     if _current_gpu() != dev:

@@ -586,10 +586,12 @@ int qlinear_paged_attention_sinks(const qlinear_kv_cache* cache, const uint16_t*
  *               which the call does not check: a larger one shows them tokens
  *               that they should not see. Any length, also inside a page; 0
  *               or less: nothing
- *   max_shared_len : upper bound of shared_len, for the launch plan only
+ *   max_shared_len : upper bound of shared_len. Without effect so far: the
+ *               launch plan goes by max_kv_len, and the tiles are cut by the
+ *               lengths on the device
  *   workspace : qlinear_paged_attention_shared_workspace_bytes of the same
- *               sizes, or of larger tokens, batch, max_q_len, max_kv_len, groups
- *               and max_shared_len with the same cache shape and q_heads
+ *               sizes, or of larger tokens, batch, max_q_len, max_kv_len and
+ *               groups with the same cache shape and q_heads
  * The other arguments are those of qlinear_paged_attention; kv_len counts all
  * of a sequence's tokens and its row of the block table has all its pages (those
  * below shared_len are read of a group's first sequence only). Errors: those of
