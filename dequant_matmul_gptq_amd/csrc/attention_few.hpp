@@ -370,14 +370,12 @@ __global__ __launch_bounds__(64 * kFewWaves, few_per_cu(D, 16 * NT, B)) void att
     uint32_t run[D / 8];
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
-      u32x4 v = {0, 0, 0, 0};
-      // In views all lanes load (the tile's first row where there is none): around
-      // a branch here, hipcc 7.2 spilled a register while some lanes were off,
-      // which the others then lacked (tests/test_attention_listing_views.py).
-      if (kView || live)
-        v = *reinterpret_cast<const u32x4*>(p + (B == 16 ? 32 * f + 8 * g : g * (D / 4) + 8 * f));
+      // All lanes load (the tile's first row where there is none): around a branch
+      // here, hipcc 7.2 spilled a register while some lanes were off, which the
+      // others then lacked (tests/test_attention_listing_views.py).
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p + (B == 16 ? 32 * f + 8 * g : g * (D / 4) + 8 * f));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) run[4 * f + e] = kView && !live ? 0 : v[e];
+      for (int e = 0; e < 4; ++e) run[4 * f + e] = live ? v[e] : 0;
     }
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
