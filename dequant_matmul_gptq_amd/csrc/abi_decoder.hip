@@ -22,7 +22,8 @@ constexpr int kMaxRows = (1 << 22) - 1;
 // Query rows of one attention call (a workgroup of 256 threads takes 128 rows
 // of a sequence and key/value head, or fewer where a sequence ends).
 constexpr int64_t kMaxQueryRows = (int64_t)1 << 29;
-// With shared prefixes a wave, or four below a million rows, joins each row.
+// With shared prefixes each row of the output has two results and more in the
+// workspace (69 GB of 256 wide heads at this bound), which are numbered in 31 bits.
 constexpr int64_t kMaxSharedRows = (int64_t)1 << 25;
 // Token slots that a call's block tables name: its steps (32 tokens, four row
 // tiles at most) are counted in 32 bits.

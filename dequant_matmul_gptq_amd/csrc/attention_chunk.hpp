@@ -31,8 +31,8 @@
 // tokens at 16384 over Q8, 40/40 heads: 235 us, 15 of them the join; its
 // unpacking is hidden (a third fewer instructions there changed nothing). 4096
 // tokens of 16/4 heads of 256, one workgroup per CU by its registers (32 to 57 of
-// them spilled, outside the loops of whole steps but for one): 258 us, 533
-// TFLOP/s; over Q8 / Q6 / Q4 242, 268, 255 us.
+// them spilled, outside the loops of whole steps but for one; views 28 to 71, all
+// outside): 258 us, 533 TFLOP/s; over Q8 / Q6 / Q4 242, 268, 255 us.
 #pragma once
 
 #include <type_traits>
