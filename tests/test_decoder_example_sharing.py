@@ -49,7 +49,8 @@ def test_sinks_with_a_window_share_nothing():
 
 
 def test_shared_only_where_it_gains():
-    """share=SHARE_GAINS: eight branches or more of up to four new tokens each, behind 4096 shared tokens or more."""
+    """share=SHARE_GAINS: eight branches or more of up to four new tokens each on average, behind 4096 shared tokens or
+    more."""
     def step(count, tokens, new, **kw):
         d = _decoder(pages=6000, page_size=16, **kw)
         _branches(d, tokens, [chr(97 + i) for i in range(count)])
@@ -73,6 +74,16 @@ def test_each_group_by_itself():
     _branches(d, 300, "xyz")
     where = d.step([(n, [1]) for n in "xyzabcdefgh"])
     assert where["shared_start"].tolist() == [0, 3, 11] and where["shared_len"].tolist() == [0, 4992]
+
+
+def test_a_prompt_among_many_single_tokens_shares_with_them():
+    d = _decoder(pages=3000, page_size=16, share=example.SHARE_GAINS)
+    names = [str(i) for i in range(30)]
+    _branches(d, 5000, names)
+    where = d.step([(n, [1] * (80 if n == "7" else 1)) for n in names])
+    assert where["shared_len"].tolist() == [4992]
+    where = d.step([(n, [1] * (100 if n == "7" else 1)) for n in names])
+    assert "shared_len" not in where
 
 
 def test_the_command_shares_where_it_gains():
