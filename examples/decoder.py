@@ -27,10 +27,10 @@ import dequant_matmul_gptq_amd as dq  # noqa: E402
 # Decoder(share=): never, wherever sequences share a page, where they gain by it.
 SHARE_NEVER, SHARE_ALWAYS, SHARE_GAINS = 0, 1, 2
 # Branches gain from about so many on, behind so many tokens, with up to so many new
-# ones each on average (us, shared and each by itself, float16: 8 single tokens behind 4096 27 and
-# 29 with 64/8 heads, 20 and 28 with 32/8, 26 and 57 with 32/32; 16 with 4 new ones 43
-# and 51; a prompt of 100 among 64 single tokens behind 16384 183 and 683; but 16 with 16 new
-# ones 77 and 78, 16 single ones behind 1024 27 and 20).
+# ones each on average (us, shared and each by itself, float16: 8 single tokens behind
+# 4096 27 and 29 with 64/8 heads, 20 and 28 with 32/8, 26 and 57 with 32/32; with 64/8
+# 16 with 4 new ones 43 and 51, a prompt of 100 among 64 single tokens behind 16384 183
+# and 683, but 16 with 16 new ones 77 and 78, 16 single ones behind 1024 27 and 20).
 GAINS_SEQUENCES, GAINS_TOKENS, GAINS_NEW = 8, 4096, 4
 
 
